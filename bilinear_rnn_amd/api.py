@@ -44,7 +44,11 @@ EXPORTED = ("comba_abi_version", "comba_status_string", "comba_last_error",
             "comba_chunk_fwd_segmented", "comba_chunk_bwd_workspace_size", "comba_chunk_bwd",
             "comba_varlen_order", "comba_mfma_peak_probe", "comba_chunk_states_size", "comba_chunk_fwd_keep_states",
             "comba_chunk_bwd_cached_workspace_size", "comba_chunk_bwd_cached", "comba_chunk_fwd_noalloc",
-            "comba_lds_probe", "comba_check_inputs")
+            "comba_lds_probe", "comba_check_inputs",
+            "comba_short_conv_fwd", "comba_short_conv_step", "comba_short_conv_bwd_workspace_size",
+            "comba_short_conv_bwd", "comba_selective_scan_workspace_size", "comba_selective_scan_fwd",
+            "comba_selective_step", "comba_selective_scan_bwd_workspace_size", "comba_selective_scan_bwd",
+            "comba_block_norm_fwd", "comba_block_norm_bwd_workspace_size", "comba_block_norm_bwd")
 
 
 class CombaError(RuntimeError):
@@ -123,6 +127,36 @@ def lib() -> ctypes.CDLL:
         L.comba_lds_probe.restype = i32
         L.comba_check_inputs.argtypes = [fp, ctypes.c_int64, ip, i32, i32, vp, vp]
         L.comba_check_inputs.restype = i32
+        i64, f32 = ctypes.c_int64, ctypes.c_float
+        L.comba_short_conv_fwd.argtypes = [vp, fp, fp, vp, ip, i32, i32, i32, i32, i32, i32, i32, vp, vp, vp]
+        L.comba_short_conv_fwd.restype = i32
+        L.comba_short_conv_step.argtypes = [vp, fp, fp, vp, i32, i32, i32, i32, i32, vp, vp, vp]
+        L.comba_short_conv_step.restype = i32
+        L.comba_short_conv_bwd_workspace_size.argtypes = [i32] * 5
+        L.comba_short_conv_bwd_workspace_size.restype = sz
+        L.comba_short_conv_bwd.argtypes = [vp, fp, fp, vp, ip, i32, i32, i32, i32, i32, i32, i32, vp, i32, vp, vp,
+                                           fp, fp, vp, vp, sz, vp]
+        L.comba_short_conv_bwd.restype = i32
+        L.comba_selective_scan_workspace_size.argtypes = [i32] * 6
+        L.comba_selective_scan_workspace_size.restype = sz
+        L.comba_selective_scan_fwd.argtypes = [vp, vp, fp, vp, vp, fp, vp, fp, i32, fp, ip, i32, i32, i32, i32, i32,
+                                               i32, i32, vp, fp, vp, sz, vp]
+        L.comba_selective_scan_fwd.restype = i32
+        L.comba_selective_step.argtypes = [vp, vp, fp, vp, vp, fp, vp, fp, i32, fp, i32, i32, i32, i32, i32, vp, fp,
+                                           vp]
+        L.comba_selective_step.restype = i32
+        L.comba_selective_scan_bwd_workspace_size.argtypes = [i32] * 6
+        L.comba_selective_scan_bwd_workspace_size.restype = sz
+        L.comba_selective_scan_bwd.argtypes = [vp, vp, fp, vp, vp, fp, vp, fp, i32, fp, ip, i32, i32, i32, i32, i32,
+                                               i32, i32, vp, fp, vp, vp, fp, vp, vp, fp, vp, fp, fp, vp, sz, vp]
+        L.comba_selective_scan_bwd.restype = i32
+        L.comba_block_norm_fwd.argtypes = [vp, vp, vp, fp, fp, fp, i64, i32, f32, i32, vp, vp, vp]
+        L.comba_block_norm_fwd.restype = i32
+        L.comba_block_norm_bwd_workspace_size.argtypes = [i64, i32]
+        L.comba_block_norm_bwd_workspace_size.restype = sz
+        L.comba_block_norm_bwd.argtypes = [vp, vp, vp, fp, fp, fp, i64, i32, f32, i32, vp, vp, vp, vp, vp, fp, fp,
+                                           fp, vp, sz, vp]
+        L.comba_block_norm_bwd.restype = i32
         _lib = L
     return _lib
 
@@ -457,6 +491,354 @@ def _debug_check(alpha: torch.Tensor, cu_seqlens: Optional[torch.Tensor], T: int
     if bad:
         raise CombaError(COMBA_ERR_INVALID_ARG, "device-side preconditions violated: " +
                          "; ".join(name for bit, name in _CHECK_NAMES if bad & bit))
+
+
+# --- layer operators around the recurrence -----------------------------------------------------------
+
+def _same_device(first: torch.Tensor, **others):
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name} is on {t.device}, not on {first.device}: all tensors must share one device")
+
+
+def _optional(t: Optional[torch.Tensor], name: str, dtype, shape):
+    if t is not None:
+        _require(t, name, dtype, shape)
+
+
+def _activation(t: torch.Tensor, name: str, dims: int):
+    _require(t, name)
+    if t.dtype not in _DT:
+        raise ValueError(f"{name} must be bfloat16 or float32 (got {t.dtype})")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions (got {tuple(t.shape)})")
+
+
+def _sequences(B: int, T: int, cu_seqlens: Optional[torch.Tensor]) -> int:
+    if cu_seqlens is None:
+        return B
+    _require(cu_seqlens, "cu_seqlens", torch.int32)
+    if cu_seqlens.dim() != 1:
+        raise ValueError("cu_seqlens must have one dimension")
+    if DEBUG_CHECKS:
+        none = torch.empty((1,), dtype=torch.float32, device=cu_seqlens.device)
+        _debug_check(none, cu_seqlens, T, check_alpha=False)
+    return cu_seqlens.numel() - 1
+
+
+def _workspace(workspace: Optional[torch.Tensor], nbytes: int, device) -> Optional[torch.Tensor]:
+    """The caller's workspace if it is large enough, else a new one (None where none is needed)."""
+    if nbytes == 0:
+        return None
+    if workspace is not None:
+        _require(workspace, "workspace", torch.uint8)
+        if workspace.device != device:
+            raise ValueError(f"workspace is on {workspace.device}, not on {device}")
+        if workspace.numel() >= nbytes:
+            return workspace
+    return torch.empty((nbytes,), dtype=torch.uint8, device=device)
+
+
+def _at(t: Optional[torch.Tensor]):
+    """Address of a tensor; an empty one has none, but the library wants required tensors non-NULL
+    (it reads nothing of an empty one)."""
+    if t is not None and t.numel() == 0:
+        return ctypes.c_void_p(256)
+    return _ptr(t)
+
+
+def _stream(device):
+    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+
+
+def _ws(workspace: Optional[torch.Tensor]):
+    return _at(workspace), 0 if workspace is None else workspace.numel()
+
+
+def _conv_args(x, weight, bias, initial_state, N, dims):
+    _activation(x, "x", dims)
+    D = x.shape[-1]
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight must be a [D, W] tensor")
+    W = weight.shape[1]
+    _require(weight, "weight", torch.float32, (D, W))
+    _optional(bias, "bias", torch.float32, (D,))
+    _optional(initial_state, "initial_state", x.dtype, (N, W - 1, D))
+    _same_device(x, weight=weight, bias=bias, initial_state=initial_state)
+    return D, W
+
+
+def short_conv(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
+               initial_state: Optional[torch.Tensor] = None, cu_seqlens: Optional[torch.Tensor] = None,
+               silu: bool = True, output_final_state: bool = True, out: Optional[torch.Tensor] = None,
+               final_state: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Short causal depthwise convolution (2 to 4 taps) with optional SiLU through
+    ``comba_short_conv_fwd``. x [B, T, D], weight [D, W] and bias [D] float32; the state holds the
+    last W - 1 inputs of every sequence, [N, W - 1, D] in x's type. Returns (y, final_state)."""
+    _activation(x, "x", 3)
+    B, T, _ = x.shape
+    N = _sequences(B, T, cu_seqlens)
+    D, W = _conv_args(x, weight, bias, initial_state, N, 3)
+    if out is None:
+        out = torch.empty_like(x)
+    _require(out, "out", x.dtype, (B, T, D))
+    if final_state is None and output_final_state:
+        final_state = torch.empty((N, W - 1, D), dtype=x.dtype, device=x.device)
+    _optional(final_state, "final_state", x.dtype, (N, W - 1, D))
+    _same_device(x, cu_seqlens=cu_seqlens, out=out, final_state=final_state)
+    with torch.cuda.device(x.device):
+        _check(lib().comba_short_conv_fwd(
+            _at(x), _at(weight), _at(bias), _at(initial_state), _at(cu_seqlens),
+            N if cu_seqlens is not None else 0, B, T, D, W, _DT[x.dtype], int(bool(silu)), _at(out),
+            _at(final_state), _stream(x.device)))
+    return out, final_state
+
+
+def short_conv_step(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                    initial_state: Optional[torch.Tensor] = None, silu: bool = True, in_place: bool = False,
+                    output_final_state: bool = True, out: Optional[torch.Tensor] = None,
+                    final_state: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """One token per sequence through ``comba_short_conv_step``: x [N, D]. With ``in_place`` the
+    state is updated in ``initial_state`` itself. Returns (y, final_state)."""
+    _activation(x, "x", 2)
+    N = x.shape[0]
+    D, W = _conv_args(x, weight, bias, initial_state, N, 2)
+    if out is None:
+        out = torch.empty_like(x)
+    _require(out, "out", x.dtype, (N, D))
+    final_state = _step_state(initial_state, final_state, in_place, output_final_state, (N, W - 1, D), x.dtype, x.device)
+    _same_device(x, out=out, final_state=final_state)
+    with torch.cuda.device(x.device):
+        _check(lib().comba_short_conv_step(
+            _at(x), _at(weight), _at(bias), _at(initial_state), N, D, W, _DT[x.dtype], int(bool(silu)), _at(out),
+            _at(final_state), _stream(x.device)))
+    return out, final_state
+
+
+def _step_state(initial_state, final_state, in_place, output_final_state, shape, dtype, device):
+    if in_place:
+        if initial_state is None:
+            raise ValueError("in_place requires initial_state")
+        return initial_state
+    if final_state is None and output_final_state:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _optional(final_state, "final_state", dtype, shape)
+    return final_state
+
+
+def short_conv_bwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor], dy: torch.Tensor,
+                   initial_state: Optional[torch.Tensor] = None, cu_seqlens: Optional[torch.Tensor] = None,
+                   d_final_state: Optional[torch.Tensor] = None, silu: bool = True,
+                   workspace: Optional[torch.Tensor] = None) -> dict:
+    """Gradients of ``short_conv`` through ``comba_short_conv_bwd``, from its inputs alone. dy has x's
+    type or float32 (what ``chunk_bwd`` returns). Returns dx and dinitial_state in x's type (the
+    latter None without an initial state), dweight and dbias (None without bias) in float32."""
+    _activation(x, "x", 3)
+    B, T, _ = x.shape
+    N = _sequences(B, T, cu_seqlens)
+    D, W = _conv_args(x, weight, bias, initial_state, N, 3)
+    _require(dy, "dy", None, (B, T, D))
+    if dy.dtype not in (x.dtype, torch.float32):
+        raise ValueError(f"dy must be {x.dtype} or float32 (got {dy.dtype})")
+    _optional(d_final_state, "d_final_state", x.dtype, (N, W - 1, D))
+    _same_device(x, dy=dy, cu_seqlens=cu_seqlens, d_final_state=d_final_state)
+    nseq = N if cu_seqlens is not None else 0
+    L = lib()
+    f32 = dict(dtype=torch.float32, device=x.device)
+    g = dict(dx=torch.empty_like(x), dweight=torch.empty((D, W), **f32),
+             dbias=None if bias is None else torch.empty((D,), **f32),
+             dinitial_state=None if initial_state is None else torch.empty_like(initial_state))
+    workspace = _workspace(workspace, int(L.comba_short_conv_bwd_workspace_size(B, T, D, W, nseq)), x.device)
+    with torch.cuda.device(x.device):
+        _check(L.comba_short_conv_bwd(
+            _at(x), _at(weight), _at(bias), _at(initial_state), _at(cu_seqlens), nseq, B, T, D, W, _DT[x.dtype],
+            int(bool(silu)), _at(dy), _DT[dy.dtype], _at(d_final_state), _at(g["dx"]), _at(g["dweight"]),
+            _at(g["dbias"]), _at(g["dinitial_state"]), *_ws(workspace), _stream(x.device)))
+    return g
+
+
+def _scan_args(x, dt, A, Bm, Cm, skip, z, dt_bias, initial_state, N):
+    rows = tuple(x.shape[:-1])
+    D = x.shape[-1]
+    if not isinstance(A, torch.Tensor) or A.dim() != 2:
+        raise ValueError("A must be a [D, S] tensor")
+    S = A.shape[1]
+    _require(A, "A", torch.float32, (D, S))
+    _require(dt, "dt", x.dtype, rows + (D,))
+    if not isinstance(Bm, torch.Tensor) or Bm.dim() != len(rows) + 2:
+        raise ValueError(f"Bm and Cm must be [{'B, T' if len(rows) == 2 else 'N'}, G, S]")
+    G = Bm.shape[-2]
+    if G < 1 or D % G != 0:
+        raise ValueError(f"the group count {G} must divide the channel count {D}")
+    _require(Bm, "Bm", x.dtype, rows + (G, S))
+    _require(Cm, "Cm", x.dtype, rows + (G, S))
+    _optional(skip, "skip", torch.float32, (D,))
+    _optional(z, "z", x.dtype, rows + (D,))
+    _optional(dt_bias, "dt_bias", torch.float32, (D,))
+    _optional(initial_state, "initial_state", torch.float32, (N, D, S))
+    _same_device(x, dt=dt, A=A, Bm=Bm, Cm=Cm, skip=skip, z=z, dt_bias=dt_bias, initial_state=initial_state)
+    return D, S, G
+
+
+def selective_scan_workspace_size(B: int, T: int, D: int, S: int, G: int = 1, num_seqs: int = 0) -> int:
+    return int(lib().comba_selective_scan_workspace_size(B, T, D, S, G, num_seqs))
+
+
+def selective_scan(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, Bm: torch.Tensor, Cm: torch.Tensor,
+                   skip: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+                   dt_bias: Optional[torch.Tensor] = None, softplus: bool = True,
+                   initial_state: Optional[torch.Tensor] = None, cu_seqlens: Optional[torch.Tensor] = None,
+                   output_final_state: bool = True, out: Optional[torch.Tensor] = None,
+                   final_state: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Selective state space scan through ``comba_selective_scan_fwd``: x, dt, z [B, T, D], A [D, S],
+    Bm, Cm [B, T, G, S], skip and dt_bias [D]. Returns (y, final_state), the state [N, D, S] in
+    float32."""
+    _activation(x, "x", 3)
+    B, T, _ = x.shape
+    N = _sequences(B, T, cu_seqlens)
+    D, S, G = _scan_args(x, dt, A, Bm, Cm, skip, z, dt_bias, initial_state, N)
+    if out is None:
+        out = torch.empty_like(x)
+    _require(out, "out", x.dtype, (B, T, D))
+    if final_state is None and output_final_state:
+        final_state = torch.empty((N, D, S), dtype=torch.float32, device=x.device)
+    _optional(final_state, "final_state", torch.float32, (N, D, S))
+    _same_device(x, cu_seqlens=cu_seqlens, out=out, final_state=final_state)
+    nseq = N if cu_seqlens is not None else 0
+    workspace = _workspace(workspace, selective_scan_workspace_size(B, T, D, S, G, nseq), x.device)
+    with torch.cuda.device(x.device):
+        _check(lib().comba_selective_scan_fwd(
+            _at(x), _at(dt), _at(A), _at(Bm), _at(Cm), _at(skip), _at(z), _at(dt_bias), int(bool(softplus)),
+            _at(initial_state), _at(cu_seqlens), nseq, B, T, D, S, G, _DT[x.dtype], _at(out), _at(final_state),
+            *_ws(workspace), _stream(x.device)))
+    return out, final_state
+
+
+def selective_step(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, Bm: torch.Tensor, Cm: torch.Tensor,
+                   skip: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+                   dt_bias: Optional[torch.Tensor] = None, softplus: bool = True,
+                   initial_state: Optional[torch.Tensor] = None, in_place: bool = False,
+                   output_final_state: bool = True, out: Optional[torch.Tensor] = None,
+                   final_state: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """One token per sequence through ``comba_selective_step``: x, dt, z [N, D], Bm, Cm [N, G, S]. With
+    ``in_place`` the state is updated in ``initial_state`` itself. Returns (y, final_state)."""
+    _activation(x, "x", 2)
+    N = x.shape[0]
+    D, S, G = _scan_args(x, dt, A, Bm, Cm, skip, z, dt_bias, initial_state, N)
+    if out is None:
+        out = torch.empty_like(x)
+    _require(out, "out", x.dtype, (N, D))
+    final_state = _step_state(initial_state, final_state, in_place, output_final_state, (N, D, S), torch.float32,
+                              x.device)
+    _same_device(x, out=out, final_state=final_state)
+    with torch.cuda.device(x.device):
+        _check(lib().comba_selective_step(
+            _at(x), _at(dt), _at(A), _at(Bm), _at(Cm), _at(skip), _at(z), _at(dt_bias), int(bool(softplus)),
+            _at(initial_state), N, D, S, G, _DT[x.dtype], _at(out), _at(final_state), _stream(x.device)))
+    return out, final_state
+
+
+def selective_scan_bwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, Bm: torch.Tensor, Cm: torch.Tensor,
+                       dy: torch.Tensor, skip: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+                       dt_bias: Optional[torch.Tensor] = None, softplus: bool = True,
+                       initial_state: Optional[torch.Tensor] = None, cu_seqlens: Optional[torch.Tensor] = None,
+                       d_final_state: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None) -> dict:
+    """Gradients of ``selective_scan`` through ``comba_selective_scan_bwd``, from its inputs alone.
+    Returns dx, ddt, dz, dB and dC in x's type, dA, dskip, ddt_bias and dinitial_state in float32;
+    the gradient of an input that was not given is None."""
+    _activation(x, "x", 3)
+    B, T, _ = x.shape
+    N = _sequences(B, T, cu_seqlens)
+    D, S, G = _scan_args(x, dt, A, Bm, Cm, skip, z, dt_bias, initial_state, N)
+    _require(dy, "dy", x.dtype, (B, T, D))
+    _optional(d_final_state, "d_final_state", torch.float32, (N, D, S))
+    _same_device(x, dy=dy, cu_seqlens=cu_seqlens, d_final_state=d_final_state)
+    nseq = N if cu_seqlens is not None else 0
+    L = lib()
+
+    def like(t):
+        return None if t is None else torch.empty_like(t)
+    g = dict(dx=like(x), ddt=like(dt), dA=like(A), dB=like(Bm), dC=like(Cm), dskip=like(skip), dz=like(z),
+             ddt_bias=like(dt_bias), dinitial_state=like(initial_state))
+    workspace = _workspace(workspace, int(L.comba_selective_scan_bwd_workspace_size(B, T, D, S, G, nseq)), x.device)
+    with torch.cuda.device(x.device):
+        _check(L.comba_selective_scan_bwd(
+            _at(x), _at(dt), _at(A), _at(Bm), _at(Cm), _at(skip), _at(z), _at(dt_bias), int(bool(softplus)),
+            _at(initial_state), _at(cu_seqlens), nseq, B, T, D, S, G, _DT[x.dtype], _at(dy), _at(d_final_state),
+            _at(g["dx"]), _at(g["ddt"]), _at(g["dA"]), _at(g["dB"]), _at(g["dC"]), _at(g["dskip"]),
+            _at(g["dz"]), _at(g["ddt_bias"]), _at(g["dinitial_state"]), *_ws(workspace), _stream(x.device)))
+    return g
+
+
+def _norm_args(y, gate, residual, scale, post_weight, pre_weight):
+    _require(y, "y")
+    if y.dtype not in _DT:
+        raise ValueError(f"y must be bfloat16 or float32 (got {y.dtype})")
+    if y.dim() < 1 or y.shape[-1] < 1:
+        raise ValueError("y must be [..., D]")
+    D = y.shape[-1]
+    _optional(gate, "gate", y.dtype, y.shape)
+    _optional(residual, "residual", y.dtype, y.shape)
+    _optional(scale, "scale", torch.float32, (D,))
+    _optional(post_weight, "post_weight", torch.float32, (D,))
+    _optional(pre_weight, "pre_weight", torch.float32, (D,))
+    _same_device(y, gate=gate, residual=residual, scale=scale, post_weight=post_weight, pre_weight=pre_weight)
+    return y.numel() // D, D
+
+
+def block_norm(y: torch.Tensor, gate: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+               scale: Optional[torch.Tensor] = None, post_weight: Optional[torch.Tensor] = None,
+               pre_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, out: Optional[torch.Tensor] = None,
+               out_norm: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """The norms after and before a block, with its gate, residual scale and residual sum, through
+    ``comba_block_norm_fwd``. y, gate, residual [..., D]; scale and weights [D] in float32; every part
+    but y is optional. Returns (r, n): r = residual + scale * (norm(y) post_weight silu(gate)), and
+    n = norm(r) pre_weight (None without pre_weight)."""
+    rows, D = _norm_args(y, gate, residual, scale, post_weight, pre_weight)
+    if out is None:
+        out = torch.empty_like(y)
+    _require(out, "out", y.dtype, y.shape)
+    if pre_weight is None:
+        if out_norm is not None:
+            raise ValueError("out_norm goes with pre_weight")
+    elif out_norm is None:
+        out_norm = torch.empty_like(y)
+    _optional(out_norm, "out_norm", y.dtype, y.shape)
+    _same_device(y, out=out, out_norm=out_norm)
+    with torch.cuda.device(y.device):
+        _check(lib().comba_block_norm_fwd(
+            _at(y), _at(gate), _at(residual), _at(scale), _at(post_weight), _at(pre_weight), rows, D, float(eps),
+            _DT[y.dtype], _at(out), _at(out_norm), _stream(y.device)))
+    return out, out_norm
+
+
+def block_norm_bwd(y: torch.Tensor, dr: Optional[torch.Tensor] = None, dn: Optional[torch.Tensor] = None,
+                   gate: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+                   scale: Optional[torch.Tensor] = None, post_weight: Optional[torch.Tensor] = None,
+                   pre_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                   workspace: Optional[torch.Tensor] = None) -> dict:
+    """Gradients of ``block_norm`` through ``comba_block_norm_bwd``, from its inputs alone, for
+    dr = dL/dr and dn = dL/dn (one of them may be None). Returns dy, dgate and dresidual in y's type,
+    dscale, dpost_weight and dpre_weight in float32; the gradient of a part that was not given is None."""
+    rows, D = _norm_args(y, gate, residual, scale, post_weight, pre_weight)
+    _optional(dr, "dr", y.dtype, y.shape)
+    _optional(dn, "dn", y.dtype, y.shape)
+    _same_device(y, dr=dr, dn=dn)
+    L = lib()
+
+    def like(t):
+        return None if t is None else torch.empty_like(t)
+    g = dict(dy=like(y), dgate=like(gate), dresidual=like(residual), dscale=like(scale),
+             dpost_weight=like(post_weight), dpre_weight=like(pre_weight))
+    workspace = _workspace(workspace, int(L.comba_block_norm_bwd_workspace_size(rows, D)), y.device)
+    with torch.cuda.device(y.device):
+        _check(L.comba_block_norm_bwd(
+            _at(y), _at(gate), _at(residual), _at(scale), _at(post_weight), _at(pre_weight), rows, D, float(eps),
+            _DT[y.dtype], _at(dr), _at(dn), _at(g["dy"]), _at(g["dgate"]), _at(g["dresidual"]),
+            _at(g["dscale"]), _at(g["dpost_weight"]), _at(g["dpre_weight"]), *_ws(workspace), _stream(y.device)))
+    return g
 
 
 PEAK_PROBE_FLOPS_PER_BLOCK_ITER = 4 * 4 * 16384   # wavefronts x MFMAs per iteration x flops per MFMA

@@ -8,6 +8,7 @@
 
 #include "comba.h"
 #include "launch.h"
+#include "layer.h"
 #include "measure.h"
 
 #define COMBA_API extern "C" __attribute__((visibility("default")))
@@ -95,6 +96,11 @@ int32_t launched(hipError_t e) {
 }
 
 }  // namespace
+
+namespace comba {
+int32_t report(int32_t code, const char* what) { return fail(code, what); }
+int32_t report_launch(hipError_t e) { return launched(e); }
+}  // namespace comba
 
 COMBA_API int32_t comba_abi_version(void) { return COMBA_ABI_VERSION; }
 

@@ -1,0 +1,453 @@
+// Short causal depthwise convolution in front of a recurrence, with optional SiLU:
+//   p[t, c] = bias[c] + sum_k weight[c, k] x[t - (W - 1) + k, c],   y = p or p sigmoid(p)
+// where tokens before a sequence come from its state (its last W - 1 inputs) or are 0.
+//
+// A few operations per element: bound by HBM (one read of x, one write of y). A thread owns 16
+// bytes of channels (one channel where rows are not 16-byte aligned) and walks along a tile of
+// tokens with the last W - 1 inputs in registers, so that every input is loaded once per tile;
+// eight loads are in flight before the first is used. Sums and the SiLU are float32, the output
+// is rounded once.
+#include "comba.h"
+#include "column_sums.h"
+#include "launch.h"
+#include "layer.h"
+#include "layer_common.h"
+
+namespace comba {
+
+constexpr int kConvBlock = 256;
+constexpr int kConvAhead = 8;   // tokens loaded ahead
+
+// Tokens per tile: 64 once that gives two wavefronts per SIMD (131072 threads); shorter for small
+// batches, down to 4, where the threads count and not the W - 1 inputs read twice.
+static int conv_tile(int64_t tokens, int64_t groups) {
+  int t = 64;
+  while (t > 4 && (tokens / t) * groups < 131072) t >>= 2;
+  return t;
+}
+
+static int64_t tiles_of(int64_t B, int64_t T, bool packed, int TT) {
+  const int64_t per = (T + TT - 1) / TT;
+  return packed ? per : B * per;
+}
+
+// Whether 16-byte pieces of rows of D elements may be used, and elements per piece.
+static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+static int piece_of(int dtype) { return dtype == COMBA_BF16 ? 8 : 4; }
+
+struct ConvPos {  // one thread's place: a tile of tokens (or a sequence's state) and a channel group
+  int tile, c, nc;
+  bool done;
+};
+
+template <int E>
+__device__ __forceinline__ ConvPos conv_pos(int D, int tiles) {
+  const uint32_t groups = (D + E - 1) / E;
+  const uint32_t item = blockIdx.x * static_cast<uint32_t>(kConvBlock) + threadIdx.x;
+  ConvPos p;
+  p.tile = static_cast<int>(item / groups);
+  p.c = static_cast<int>(item % groups) * E;
+  p.nc = min(E, D - p.c);
+  p.done = p.tile >= tiles;
+  return p;
+}
+
+template <int E, int W>
+__device__ __forceinline__ void load_weights(const float* weight, const float* bias, int c, int nc,
+                                             float (&w)[W][E], float (&b)[E]) {
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+#pragma unroll
+    for (int k = 0; k < W; ++k) w[k][e] = e < nc ? weight[static_cast<int64_t>(c + e) * W + k] : 0.f;
+    b[e] = bias && e < nc ? bias[c + e] : 0.f;
+  }
+}
+
+// The W - 1 inputs before token t of a sequence [s, ...) into win[0 .. W-2], oldest first. `x` is
+// the row of token 0 of the batch row; `state` the sequence's first state row, or null.
+template <typename T, int E, bool V, int W>
+__device__ __forceinline__ void load_history(const T* x, const T* state, int64_t D, int s, int t, int nc,
+                                             float (&win)[W][E]) {
+#pragma unroll
+  for (int k = 0; k < W - 1; ++k) {
+    const int pos = t - (W - 1) + k;  // token of this place
+    if (pos >= s) {
+      Pack<T, E, V>::load(x + pos * D, win[k], nc);
+    } else if (state) {
+      Pack<T, E, V>::load(state + (W - 1 + pos - s) * D, win[k], nc);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) win[k][e] = 0.f;
+    }
+  }
+}
+
+template <int E, int W>
+__device__ __forceinline__ void conv_dot(const float (&win)[W][E], const float (&w)[W][E], const float (&b)[E],
+                                         float (&p)[E]) {
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    p[e] = b[e];
+#pragma unroll
+    for (int k = 0; k < W; ++k) p[e] = fmaf(w[k][e], win[k][e], p[e]);
+  }
+}
+
+template <int E, int W>
+__device__ __forceinline__ void shift_window(float (&win)[W][E]) {
+#pragma unroll
+  for (int k = 0; k < W - 1; ++k)
+#pragma unroll
+    for (int e = 0; e < E; ++e) win[k][e] = win[k + 1][e];
+}
+
+// Calls piece(n, s, e, m, mend) for the part [m, mend) of every sequence [s, e) that the tile holds.
+template <typename F>
+__device__ __forceinline__ void for_pieces(const int32_t* cu, int N, int T, int b, int m0, int m1, F piece) {
+  if (!cu) {
+    piece(b, 0, T, m0, m1);
+    return;
+  }
+  for (int n = find_sequence(cu, N, m0); n < N; ++n) {
+    int s, e;
+    packed_range(cu, n, T, s, e);
+    if (s >= m1) break;
+    const int a = max(s, m0), z = min(e, m1);
+    if (a < z) piece(n, s, e, a, z);
+  }
+}
+
+template <typename T, int E, bool V, int W>
+__global__ __launch_bounds__(kConvBlock) void conv_fwd_kernel(
+    const T* __restrict__ x, const float* __restrict__ weight, const float* __restrict__ bias,
+    const T* __restrict__ init, const int32_t* __restrict__ cu, int N, int Tn, int64_t D, int TT, int tiles,
+    bool silu, T* __restrict__ y, T* __restrict__ fin) {
+  const ConvPos p = conv_pos<E>(static_cast<int>(D), tiles + (fin ? N : 0));
+  if (p.done) return;
+  const int c = p.c, nc = p.nc;
+  if (p.tile >= tiles) {  // the last W - 1 inputs of sequence n: exact copies
+    const int n = p.tile - tiles;
+    int s = 0, e = Tn;
+    if (cu) packed_range(cu, n, Tn, s, e);
+    const T* xr = x + (cu ? 0 : static_cast<int64_t>(n) * Tn * D) + c;
+    const T* st = init ? init + static_cast<int64_t>(n) * (W - 1) * D + c : nullptr;
+    float win[W][E];
+    load_history<T, E, V, W>(xr, st, D, s, e, nc, win);
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k)
+      Pack<T, E, V>::store(fin + (static_cast<int64_t>(n) * (W - 1) + k) * D + c, win[k], nc);
+    return;
+  }
+  const int per = (Tn + TT - 1) / TT;
+  const int b = p.tile / per, m0 = (p.tile - b * per) * TT, m1 = min(m0 + TT, Tn);
+  float w[W][E], bs[E];
+  load_weights<E, W>(weight, bias, c, nc, w, bs);
+  const T* xr = x + static_cast<int64_t>(b) * Tn * D + c;
+  T* yr = y + static_cast<int64_t>(b) * Tn * D + c;
+  for_pieces(cu, N, Tn, b, m0, m1, [&](int n, int s, int e, int m, int mend) {
+    const T* st = init ? init + static_cast<int64_t>(n) * (W - 1) * D + c : nullptr;
+    float win[W][E];
+    load_history<T, E, V, W>(xr, st, D, s, m, nc, win);
+    for (; m < mend; m += kConvAhead) {
+      float in[kConvAhead][E];
+#pragma unroll
+      for (int u = 0; u < kConvAhead; ++u) Pack<T, E, V>::load(xr + min(m + u, mend - 1) * D, in[u], nc);
+#pragma unroll
+      for (int u = 0; u < kConvAhead; ++u) {
+        if (m + u < mend) {
+          float o[E];
+#pragma unroll
+          for (int i = 0; i < E; ++i) win[W - 1][i] = in[u][i];
+          conv_dot<E, W>(win, w, bs, o);
+          if (silu)
+#pragma unroll
+            for (int i = 0; i < E; ++i) o[i] *= sigmoid_fast(o[i]);
+          Pack<T, E, V>::store(yr + (m + u) * D, o, nc);
+          shift_window<E, W>(win);
+        }
+      }
+    }
+  });
+}
+
+// One token per sequence: the state is read, shifted by the token and written (in place if the
+// caller asks for it: a thread reads its slots before it writes them). HBM-bound.
+template <typename T, int E, bool V, int W>
+__global__ __launch_bounds__(kConvBlock) void conv_step_kernel(
+    const T* __restrict__ x, const float* __restrict__ weight, const float* __restrict__ bias, const T* init, int N,
+    int64_t D, bool silu, T* __restrict__ y, T* fin) {
+  const ConvPos p = conv_pos<E>(static_cast<int>(D), N);
+  if (p.done) return;
+  const int c = p.c, nc = p.nc;
+  const int64_t n = p.tile, so = n * (W - 1) * D + c;
+  float win[W][E], w[W][E], bs[E], o[E];
+  Pack<T, E, V>::load(x + n * D + c, win[W - 1], nc);
+#pragma unroll
+  for (int k = 0; k < W - 1; ++k) {
+    if (init) Pack<T, E, V>::load(init + so + k * D, win[k], nc);
+    else
+#pragma unroll
+      for (int i = 0; i < E; ++i) win[k][i] = 0.f;
+  }
+  load_weights<E, W>(weight, bias, c, nc, w, bs);
+  conv_dot<E, W>(win, w, bs, o);
+  if (silu)
+#pragma unroll
+    for (int i = 0; i < E; ++i) o[i] *= sigmoid_fast(o[i]);
+  Pack<T, E, V>::store(y + n * D + c, o, nc);
+  if (fin)
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) Pack<T, E, V>::store(fin + so + k * D, win[k + 1], nc);
+}
+
+// d loss / d p from d loss / d y: y = p sigmoid(p), y' = s (1 + p (1 - s)).
+template <int E>
+__device__ __forceinline__ void silu_grad(const float (&p)[E], float (&d)[E]) {
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    const float s = sigmoid_fast(p[i]);
+    d[i] *= s * fmaf(p[i], 1.f - s, 1.f);
+  }
+}
+
+// Backward: dp as above from the recomputed p; dx[t] = sum_k weight[k] dp[t + W - 1 - k] (tokens of
+// the same sequence), dweight[c, k] = sum_t dp[t] x[t - (W - 1) + k], dbias = sum_t dp. A thread
+// walks its tile and the W - 1 tokens after it, whose dp it recomputes for its own dx. Parameter
+// gradients: one float32 partial sum per tile, added up in a fixed order by a second kernel.
+// The last N items form the gradients of the initial states from the first W - 1 tokens.
+template <typename T, typename G, int E, bool V, int W>
+__global__ __launch_bounds__(kConvBlock) void conv_bwd_kernel(
+    const T* __restrict__ x, const float* __restrict__ weight, const float* __restrict__ bias,
+    const T* __restrict__ init, const int32_t* __restrict__ cu, int N, int Tn, int64_t D, int TT, int tiles, bool silu,
+    const G* __restrict__ dy, const T* __restrict__ dfin, T* __restrict__ dx, T* __restrict__ dinit,
+    float* __restrict__ part) {
+  const ConvPos pp = conv_pos<E>(static_cast<int>(D), tiles + (dinit ? N : 0));
+  if (pp.done) return;
+  const int c = pp.c, nc = pp.nc;
+  float w[W][E], bs[E];
+  load_weights<E, W>(weight, bias, c, nc, w, bs);
+  if (pp.tile >= tiles) {
+    const int n = pp.tile - tiles;
+    int s = 0, e = Tn;
+    if (cu) packed_range(cu, n, Tn, s, e);
+    const int64_t row = cu ? 0 : static_cast<int64_t>(n) * Tn * D;
+    const int64_t so = static_cast<int64_t>(n) * (W - 1) * D + c;
+    float win[W][E], acc[W][E];
+    load_history<T, E, V, W>(x + row + c, init ? init + so : nullptr, D, s, s, nc, win);
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+      for (int i = 0; i < E; ++i) acc[j][i] = 0.f;
+#pragma unroll
+    for (int q = 0; q < W - 1; ++q) {
+      if (s + q < e) {  // token q of the sequence sees slot j through weight j - q
+        float p[E], d[E];
+        Pack<T, E, V>::load(x + row + c + (s + q) * D, win[W - 1], nc);
+        Pack<G, E, V>::load(dy + row + c + (s + q) * D, d, nc);
+        conv_dot<E, W>(win, w, bs, p);
+        if (silu) silu_grad<E>(p, d);
+#pragma unroll
+        for (int j = q; j < W - 1; ++j)
+#pragma unroll
+          for (int i = 0; i < E; ++i) acc[j][i] = fmaf(w[j - q][i], d[i], acc[j][i]);
+        shift_window<E, W>(win);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+      if (dfin && j >= e - s) {  // the slot is still in the final state, moved up by the length
+        float f[E];
+        Pack<T, E, V>::load(dfin + so + (j - (e - s)) * D, f, nc);
+#pragma unroll
+        for (int i = 0; i < E; ++i) acc[j][i] += f[i];
+      }
+      Pack<T, E, V>::store(dinit + so + j * D, acc[j], nc);
+    }
+    return;
+  }
+  const int per = (Tn + TT - 1) / TT;
+  const int b = pp.tile / per, m0 = (pp.tile - b * per) * TT, m1 = min(m0 + TT, Tn);
+  const int64_t row = static_cast<int64_t>(b) * Tn * D + c;
+  float dw[W + 1][E];
+#pragma unroll
+  for (int k = 0; k <= W; ++k)
+#pragma unroll
+    for (int i = 0; i < E; ++i) dw[k][i] = 0.f;
+  for_pieces(cu, N, Tn, b, m0, m1, [&](int n, int s, int e, int m, int mend) {
+    const int64_t so = static_cast<int64_t>(n) * (W - 1) * D + c;
+    float win[W][E], ring[W][E];  // ring: dp of the last W tokens
+    load_history<T, E, V, W>(x + row, init ? init + so : nullptr, D, s, m, nc, win);
+#pragma unroll
+    for (int k = 0; k < W; ++k)
+#pragma unroll
+      for (int i = 0; i < E; ++i) ring[k][i] = 0.f;
+    const int first = m, stop = mend + W - 1, have = min(stop, e);
+    constexpr int U = 4;
+    for (; m < stop; m += U) {
+      float in[U][E], d[U][E];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int t = min(m + u, have - 1);
+        Pack<T, E, V>::load(x + row + t * D, in[u], nc);
+        Pack<G, E, V>::load(dy + row + t * D, d[u], nc);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int t = m + u;
+        if (t < stop) {
+#pragma unroll
+          for (int i = 0; i < E; ++i) win[W - 1][i] = in[u][i];
+          if (t >= have) {
+#pragma unroll
+            for (int i = 0; i < E; ++i) d[u][i] = 0.f;
+          } else if (silu) {
+            float p[E];
+            conv_dot<E, W>(win, w, bs, p);
+            silu_grad<E>(p, d[u]);
+          }
+          if (t < mend) {
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+#pragma unroll
+              for (int k = 0; k < W; ++k) dw[k][i] = fmaf(d[u][i], win[k][i], dw[k][i]);
+              dw[W][i] += d[u][i];
+            }
+          }
+          shift_window<E, W>(win);
+#pragma unroll
+          for (int i = 0; i < E; ++i) {
+#pragma unroll
+            for (int k = 0; k < W - 1; ++k) ring[k][i] = ring[k + 1][i];
+            ring[W - 1][i] = d[u][i];
+          }
+          const int to = t - (W - 1);  // its dx is complete: ring[o] is dp[to + o]
+          if (to >= first) {
+            float g[E];
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+              g[i] = 0.f;
+#pragma unroll
+              for (int o = 0; o < W; ++o) g[i] = fmaf(w[W - 1 - o][i], ring[o][i], g[i]);
+            }
+            const int slot = to - (e - (W - 1));
+            if (dfin && slot >= 0) {
+              float f[E];
+              Pack<T, E, V>::load(dfin + so + slot * D, f, nc);
+#pragma unroll
+              for (int i = 0; i < E; ++i) g[i] += f[i];
+            }
+            Pack<T, E, V>::store(dx + row + to * D, g, nc);
+          }
+        }
+      }
+    }
+  });
+#pragma unroll
+  for (int k = 0; k <= W; ++k)
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+      if (i < nc) part[(static_cast<int64_t>(pp.tile) * (W + 1) + k) * D + c + i] = dw[k][i];
+}
+
+// --- launches -----------------------------------------------------------------------------------
+
+static unsigned conv_grid(int64_t rows, int64_t groups) {
+  return static_cast<unsigned>((rows * groups + kConvBlock - 1) / kConvBlock);
+}
+
+template <typename T, int E, bool V, int W>
+static hipError_t conv_fwd_t(const ConvArgs& a, hipStream_t st) {
+  const int64_t groups = (a.D + E - 1) / E;
+  const int TT = conv_tile(static_cast<int64_t>(a.B) * a.T, groups);
+  const int64_t tiles = tiles_of(a.B, a.T, a.cu_seqlens != nullptr, TT);
+  const unsigned grid = conv_grid(tiles + (a.fin ? a.N : 0), groups);
+  if (grid == 0) return hipSuccess;
+  conv_fwd_kernel<T, E, V, W><<<grid, kConvBlock, 0, st>>>(
+      static_cast<const T*>(a.x), a.weight, a.bias, static_cast<const T*>(a.init), a.cu_seqlens, a.N, a.T, a.D, TT,
+      static_cast<int>(tiles), a.silu, static_cast<T*>(a.y), static_cast<T*>(a.fin));
+  return hipGetLastError();
+}
+
+template <typename T, int E, bool V, int W>
+static hipError_t conv_step_t(const ConvArgs& a, hipStream_t st) {
+  conv_step_kernel<T, E, V, W><<<conv_grid(a.N, (a.D + E - 1) / E), kConvBlock, 0, st>>>(
+      static_cast<const T*>(a.x), a.weight, a.bias, static_cast<const T*>(a.init), a.N, a.D, a.silu,
+      static_cast<T*>(a.y), static_cast<T*>(a.fin));
+  return hipGetLastError();
+}
+
+int64_t conv_tiles(int64_t B, int64_t T, int64_t D, bool packed) {
+  return tiles_of(B, T, packed, conv_tile(B * T, D));
+}
+
+// Tiles of the backward: by eight channels per thread whatever the alignment, so that the
+// workspace's size follows from the sizes alone.
+static int conv_bwd_tile(int64_t B, int64_t T, int64_t D) { return conv_tile(B * T, (D + 7) / 8); }
+
+int64_t conv_bwd_tiles(int64_t B, int64_t T, int64_t D, bool packed) {
+  return tiles_of(B, T, packed, conv_bwd_tile(B, T, D));
+}
+
+template <typename T, typename G, int E, bool V, int W>
+static hipError_t conv_bwd_t(const ConvBwdArgs& a, hipStream_t st) {
+  const ConvArgs& f = a.f;
+  const int TT = conv_bwd_tile(f.B, f.T, f.D);
+  const int64_t tiles = conv_bwd_tiles(f.B, f.T, f.D, f.cu_seqlens != nullptr);
+  const unsigned grid = conv_grid(tiles + (a.dinit ? f.N : 0), (f.D + E - 1) / E);
+  if (grid > 0) {
+    conv_bwd_kernel<T, G, E, V, W><<<grid, kConvBlock, 0, st>>>(
+        static_cast<const T*>(f.x), f.weight, f.bias, static_cast<const T*>(f.init), f.cu_seqlens, f.N, f.T, f.D, TT,
+        static_cast<int>(tiles), f.silu, static_cast<const G*>(a.dy), static_cast<const T*>(a.dfin),
+        static_cast<T*>(a.dx), static_cast<T*>(a.dinit), a.part);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  // column k * D + c of the partial sums: dweight[c, k], the last D columns dbias
+  float* dw = a.dweight;
+  float* db = a.dbias;
+  const int D = f.D;
+  return column_sums(a.part, tiles, static_cast<int64_t>(W + 1) * D, (W + (db ? 1 : 0)) * D, st,
+                     [=] __device__(int col, float s) {
+                       const int k = col / D, ch = col - k * D;
+                       if (k < W) dw[static_cast<int64_t>(ch) * W + k] = s;
+                       else db[ch] = s;
+                     });
+}
+
+template <typename T, int E, bool V>
+static hipError_t conv_w(const ConvArgs& a, bool step, hipStream_t st) {
+  switch (a.W) {
+    case 2: return step ? conv_step_t<T, E, V, 2>(a, st) : conv_fwd_t<T, E, V, 2>(a, st);
+    case 3: return step ? conv_step_t<T, E, V, 3>(a, st) : conv_fwd_t<T, E, V, 3>(a, st);
+    default: return step ? conv_step_t<T, E, V, 4>(a, st) : conv_fwd_t<T, E, V, 4>(a, st);
+  }
+}
+
+static hipError_t conv_any(const ConvArgs& a, bool step, hipStream_t st) {
+  const bool v = a.D % piece_of(a.dtype) == 0 && aligned16(a.x) && aligned16(a.y) && aligned16(a.init) && aligned16(a.fin);
+  if (a.dtype == COMBA_BF16) return v ? conv_w<u16, 8, true>(a, step, st) : conv_w<u16, 1, false>(a, step, st);
+  return v ? conv_w<float, 4, true>(a, step, st) : conv_w<float, 1, false>(a, step, st);
+}
+
+hipError_t launch_conv(const ConvArgs& a, hipStream_t st) { return conv_any(a, false, st); }
+hipError_t launch_conv_step(const ConvArgs& a, hipStream_t st) { return conv_any(a, true, st); }
+
+template <typename T, typename G, int E, bool V>
+static hipError_t conv_bwd_w(const ConvBwdArgs& a, hipStream_t st) {
+  switch (a.f.W) {
+    case 2: return conv_bwd_t<T, G, E, V, 2>(a, st);
+    case 3: return conv_bwd_t<T, G, E, V, 3>(a, st);
+    default: return conv_bwd_t<T, G, E, V, 4>(a, st);
+  }
+}
+
+hipError_t launch_conv_bwd(const ConvBwdArgs& a, hipStream_t st) {
+  const ConvArgs& f = a.f;
+  const bool v = f.D % piece_of(f.dtype) == 0 && aligned16(f.x) && aligned16(f.init) && aligned16(a.dy) &&
+                 aligned16(a.dfin) && aligned16(a.dx) && aligned16(a.dinit);
+  if (f.dtype == COMBA_FP32) return v ? conv_bwd_w<float, float, 4, true>(a, st) : conv_bwd_w<float, float, 1, false>(a, st);
+  if (a.dy_dtype == COMBA_FP32) return v ? conv_bwd_w<u16, float, 8, true>(a, st) : conv_bwd_w<u16, float, 1, false>(a, st);
+  return v ? conv_bwd_w<u16, u16, 8, true>(a, st) : conv_bwd_w<u16, u16, 1, false>(a, st);
+}
+
+}  // namespace comba

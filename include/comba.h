@@ -431,6 +431,160 @@ int32_t comba_mfma_peak_probe(float* sink, int32_t blocks, int32_t iters, void* 
 int32_t comba_lds_probe(int32_t kind, const int32_t* lane_offsets, int32_t iters, uint32_t* sink, int32_t blocks,
                         void* stream);
 
+/*
+ * Layer operators: what a recurrent layer needs around its mixer. They share
+ * the conventions at the top of this header (caller-owned device memory,
+ * contiguous row-major tensors, cu_seqlens, streams, status codes, no
+ * allocation, no synchronisation) with these differences:
+ * - `dtype` (COMBA_BF16 or COMBA_FP32) is the type of every activation and of
+ *   its gradient; parameters, their gradients and recurrent states are
+ *   float32. All arithmetic is float32, each output is rounded once.
+ * - Channel counts are free. 16-byte aligned tensors whose rows are multiples
+ *   of 16 bytes take the fast path; any other address that is aligned to its
+ *   elements works.
+ * - With cu_seqlens, tokens before cu_seqlens[0] or from cu_seqlens[N] on
+ *   belong to no sequence: they are not read, and their rows of an output are
+ *   left as they were.
+ * - Outputs must not overlap inputs or each other, except where a state may be
+ *   updated in place as stated.
+ * COMBA_ABI_VERSION stays while existing entry points keep their signature
+ * and meaning; a caller that needs an added one looks it up by name.
+ */
+
+/*
+ * Short causal depthwise convolution, W = 2, 3 or 4 taps (the convolution of
+ * q, k and v, or of a scan's input, in front of the recurrence):
+ *     p[t, c] = bias[c] + sum_k weight[c, k] x[t - (W - 1) + k, c]
+ *     y = p, or with `silu` (non-zero) p * sigmoid(p)
+ * Tokens before a sequence's first come from its state: the last W - 1 inputs
+ * of what went before, oldest first (zeros without one).
+ *   x, y           [B, T, D]        dtype
+ *   weight, bias   [D, W], [D]      float32; bias may be NULL
+ *   initial_state  [N, W - 1, D]    dtype, or NULL for zeros
+ *   final_state    [N, W - 1, D]    dtype, or NULL (not written); the inputs
+ *                                   copied exactly. Must not overlap
+ *                                   initial_state.
+ * comba_short_conv_step is the single-token form: x, y [N, D], one token for
+ * each of N sequences; final_state may be initial_state itself (in place), any
+ * other overlap is not allowed.
+ * comba_short_conv_bwd: gradients for dy = dL/dy (dy_dtype: dtype, or
+ * COMBA_FP32 for a float32 gradient of a bf16 tensor, as comba_chunk_bwd
+ * returns it) and d_final_state = dL/dfinal_state (dtype; NULL: 0):
+ *   dx [B, T, D] dtype; dweight [D, W], dbias [D] float32 (dbias may be NULL);
+ *   d_initial_state [N, W - 1, D] dtype (may be NULL: not written).
+ * It needs comba_short_conv_bwd_workspace_size(...) bytes of workspace
+ * (num_seqs is N with cu_seqlens and 0 without), 256-byte aligned, and gives
+ * the same bits on every run.
+ * Errors: COMBA_ERR_UNSUPPORTED for other W, and for tensors of more than 2^31
+ * (token tile, channel) pairs or 2^31 - 1 tokens.
+ */
+int32_t comba_short_conv_fwd(const void* x, const float* weight, const float* bias, const void* initial_state,
+                             const int32_t* cu_seqlens, int32_t num_seqs, int32_t B, int32_t T, int32_t D, int32_t W,
+                             int32_t dtype, int32_t silu, void* y, void* final_state, void* stream);
+
+int32_t comba_short_conv_step(const void* x, const float* weight, const float* bias, const void* initial_state,
+                              int32_t N, int32_t D, int32_t W, int32_t dtype, int32_t silu, void* y,
+                              void* final_state, void* stream);
+
+size_t comba_short_conv_bwd_workspace_size(int32_t B, int32_t T, int32_t D, int32_t W, int32_t num_seqs);
+
+int32_t comba_short_conv_bwd(const void* x, const float* weight, const float* bias, const void* initial_state,
+                             const int32_t* cu_seqlens, int32_t num_seqs, int32_t B, int32_t T, int32_t D, int32_t W,
+                             int32_t dtype, int32_t silu, const void* dy, int32_t dy_dtype,
+                             const void* d_final_state, void* dx, float* dweight, float* dbias,
+                             void* d_initial_state, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Selective state space scan: a diagonal recurrence with S states per channel
+ * (1 <= S <= 64) whose decay, input and output maps vary with the token. For
+ * channel c of group g = c / (D / G) and state s:
+ *     d_t    = softplus(dt_t + dt_bias)      (dt_t + dt_bias without `softplus`)
+ *     h_t[s] = exp(d_t A[c, s]) h_{t-1}[s] + d_t x_t Bm_t[g, s]
+ *     y_t    = (sum_s Cm_t[g, s] h_t[s] + skip x_t) * z_t sigmoid(z_t)
+ *   x, dt, z, y    [B, T, D]        dtype; z may be NULL (no gate)
+ *   A              [D, S]           float32 (negative for a decay; not checked)
+ *   Bm, Cm         [B, T, G, S]     dtype; G divides D
+ *   skip, dt_bias  [D]              float32, either may be NULL (0)
+ *   initial_state  [N, D, S]        float32, or NULL for zeros
+ *   final_state    [N, D, S]        float32, or NULL (not written); may be
+ *                                   initial_state itself, but no other overlap
+ * comba_selective_scan_fwd cuts batches with too few sequences and channels
+ * for the chip along time; it then needs workspace of
+ * comba_selective_scan_workspace_size(...) bytes, 256-byte aligned (0: none,
+ * NULL is accepted). num_seqs is N with cu_seqlens and 0 without.
+ * comba_selective_step is the single-token form: x, dt, z, y [N, D], Bm, Cm
+ * [N, G, S], one token for each of N sequences.
+ * comba_selective_scan_bwd: gradients for dy = dL/dy [B, T, D] (dtype) and
+ * d_final_state (float32 [N, D, S]; NULL: 0). Nothing is kept from the
+ * forward. Outputs, written in full:
+ *   dx, ddt, dz [B, T, D] dtype (dz NULL exactly when z is); dA [D, S]
+ *   float32; dBm, dCm [B, T, G, S] dtype; dskip, ddt_bias [D] float32 and
+ *   d_initial_state [N, D, S] float32 (each may be NULL: not written).
+ * It needs comba_selective_scan_bwd_workspace_size(...) bytes, 256-byte
+ * aligned, and gives the same bits on every run.
+ * Errors: COMBA_ERR_UNSUPPORTED for S > 64, D > 2^22, more than 2^31 - 1
+ * tokens or workgroups.
+ */
+size_t comba_selective_scan_workspace_size(int32_t B, int32_t T, int32_t D, int32_t S, int32_t G, int32_t num_seqs);
+
+int32_t comba_selective_scan_fwd(const void* x, const void* dt, const float* A, const void* Bm, const void* Cm,
+                                 const float* skip, const void* z, const float* dt_bias, int32_t softplus,
+                                 const float* initial_state, const int32_t* cu_seqlens, int32_t num_seqs,
+                                 int32_t B, int32_t T, int32_t D, int32_t S, int32_t G, int32_t dtype,
+                                 void* y, float* final_state, void* workspace, size_t workspace_bytes, void* stream);
+
+int32_t comba_selective_step(const void* x, const void* dt, const float* A, const void* Bm, const void* Cm,
+                             const float* skip, const void* z, const float* dt_bias, int32_t softplus,
+                             const float* initial_state, int32_t N, int32_t D, int32_t S, int32_t G, int32_t dtype,
+                             void* y, float* final_state, void* stream);
+
+size_t comba_selective_scan_bwd_workspace_size(int32_t B, int32_t T, int32_t D, int32_t S, int32_t G,
+                                               int32_t num_seqs);
+
+int32_t comba_selective_scan_bwd(const void* x, const void* dt, const float* A, const void* Bm, const void* Cm,
+                                 const float* skip, const void* z, const float* dt_bias, int32_t softplus,
+                                 const float* initial_state, const int32_t* cu_seqlens, int32_t num_seqs,
+                                 int32_t B, int32_t T, int32_t D, int32_t S, int32_t G, int32_t dtype,
+                                 const void* dy, const float* d_final_state, void* dx, void* ddt, float* dA,
+                                 void* dBm, void* dCm, float* dskip, void* dz, float* ddt_bias,
+                                 float* d_initial_state, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The norms after and before a block, fused with the block's gate, its
+ * residual scale and the residual sum. Per row of D elements, each part only
+ * if its pointer is given:
+ *     u = y * rsqrt(mean(y^2) + eps) * post_weight          (else u = y)
+ *     u = u * gate sigmoid(gate)
+ *     r = residual + scale u                                (scale: per column)
+ *     n = r * rsqrt(mean(r^2) + eps) * pre_weight           (from r before its rounding)
+ *   y, gate, residual, r, n   [rows, D]   dtype; n is given exactly when
+ *                                         pre_weight is
+ *   scale, post_weight, pre_weight   [D]  float32
+ * With D the head width and post_weight and gate alone it is the gated norm of
+ * a recurrence's output; with residual and pre_weight the seam between two
+ * blocks. At least one part must be given. 1 <= D <= 16384 (else
+ * COMBA_ERR_UNSUPPORTED); rows >= 0.
+ * comba_block_norm_bwd: gradients for dr = dL/dr and dn = dL/dn (dtype; dr may
+ * be NULL if dn is given, dn only with pre_weight, NULL: 0), from the forward's
+ * inputs alone:
+ *   dy, dgate, dresidual   [rows, D]   dtype, dgate and dresidual exactly when
+ *                                      their input is given
+ *   dscale, dpost_weight, dpre_weight  [D] float32, exactly when theirs is
+ * It needs comba_block_norm_bwd_workspace_size(rows, D) bytes, 256-byte
+ * aligned, and gives the same bits on every run.
+ */
+int32_t comba_block_norm_fwd(const void* y, const void* gate, const void* residual, const float* scale,
+                             const float* post_weight, const float* pre_weight, int64_t rows, int32_t D, float eps,
+                             int32_t dtype, void* r, void* n, void* stream);
+
+size_t comba_block_norm_bwd_workspace_size(int64_t rows, int32_t D);
+
+int32_t comba_block_norm_bwd(const void* y, const void* gate, const void* residual, const float* scale,
+                             const float* post_weight, const float* pre_weight, int64_t rows, int32_t D, float eps,
+                             int32_t dtype, const void* dr, const void* dn, void* dy, void* dgate, void* dresidual,
+                             float* dscale, float* dpost_weight, float* dpre_weight, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
