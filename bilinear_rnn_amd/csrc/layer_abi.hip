@@ -182,7 +182,7 @@ ScanBwdWorkspace scan_bwd_workspace(const comba::ScanPlan& p, int64_t rows, int6
   w.dA = w.dsum + up256(f * p.slots * D);
   w.dD = w.dA + states;
   w.dBC = w.dD + up256(f * p.slots * 2 * D);
-  w.total = w.dBC + up256(f * (comba::scan_channel_blocks(D, G) / G) * rows * G * 2 * SP);
+  w.total = w.dBC + up256(f * (comba::scan_bwd_channel_blocks(D, G) / G) * rows * G * 2 * SP);
   return w;
 }
 

@@ -1,6 +1,7 @@
 // Device helpers shared by the layer operators.
 #pragma once
 
+#include "bf16_tiles.h"
 #include "device_common.h"
 
 namespace comba {
@@ -54,6 +55,31 @@ template <typename T, int E> struct Pack<T, E, false> {
       if (i < n) Elem<T>::store(p, i, x[i]);
   }
 };
+
+// A range of memory read and written through a buffer resource: loads past its end give 0, stores
+// past its end are dropped, so that the ends of a tensor need no branches. Offsets are 32-bit byte
+// offsets; kNowhere is past every end.
+constexpr uint32_t kNowhere = 0x80000000u;
+template <typename T> struct Range {
+  __amdgpu_buffer_rsrc_t r;
+  __device__ __forceinline__ Range(const T* base, int64_t bytes)
+      : r(__builtin_amdgcn_make_buffer_rsrc(uniform_ptr(const_cast<T*>(base)), static_cast<short>(0),
+                                            __builtin_amdgcn_readfirstlane(static_cast<int>(bytes)), kBufferWord3)) {}
+  // The element's bits; value() makes them a float.
+  __device__ __forceinline__ uint32_t load(uint32_t off) const {
+    if constexpr (sizeof(T) == 2) return __builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0);
+    else return __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
+  }
+  static __device__ __forceinline__ float value(uint32_t bits) { return __uint_as_float(sizeof(T) == 2 ? bits << 16 : bits); }
+  __device__ __forceinline__ void store(uint32_t off, float x) const {
+    if constexpr (sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b16(float_to_bf16_bits(x), r, off, 0, 0);
+    else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), r, off, 0, 0);
+  }
+};
+
+// Keeps x where it is computed: the compiler neither moves its computation below this point nor
+// turns a selection of it into a branch. No instruction.
+__device__ __forceinline__ void pin(float& x) { asm volatile("" : "+v"(x)); }
 
 constexpr float kLog2E = 1.44269504088896340736f;
 

@@ -1,54 +1,67 @@
 // Device code shared by the selective scan's forward and backward.
 //
-// A channel's SP = 4 * NPL states (S padded with states that stay 0) are spread over the 4 lanes of a
-// quad, NPL consecutive states each; a wavefront holds 16 channels, a workgroup 64 channels of one
-// B / C group. Why quads: the sum over a channel's states is two DPP steps, values of one token reach
-// the quad's other lanes as a DPP operand of the instruction that uses them (quad_perm costs
-// nothing), and 16 channels per wavefront still give a wavefront per SIMD at 16384 channels. Each
-// lane owns one of four consecutive tokens for the work per (token, channel): step size, gate, loads,
-// stores.
+// A channel's SP states (S padded with states that stay 0) are spread over LPC neighbouring lanes, NPL
+// consecutive states each; a workgroup holds channels of one B / C group.
 #pragma once
+
+#include <type_traits>
 
 #include "layer.h"
 #include "layer_common.h"
 
 namespace comba {
 
-constexpr int kScanBlock = 256;     // 4 wavefronts
-constexpr int kScanChannels = 64;   // channels per workgroup
+// Step and backward: 64 channels in quads per workgroup.
+constexpr int kScanBlock = 256, kScanChannels = 64;
+
+template <int CTRL>
+__device__ __forceinline__ float dpp_move(float x) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true));
+}
 
 // Value of lane K of the quad.
 template <int K>
 __device__ __forceinline__ float quad_bcast(float x) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), K * 0x55, 0xf, 0xf, true));
+  return dpp_move<K * 0x55>(x);
 }
 
-// v[k] summed over the quad, for the lane's own k = lane & 3.
-__device__ __forceinline__ float quad_sums(const float (&v)[4], int q) {
-  const bool hi = q & 2, odd = q & 1;
-  const float a = (hi ? v[2] : v[0]) + dpp_flip<1>(hi ? v[0] : v[2]);
-  const float b = (hi ? v[3] : v[1]) + dpp_flip<1>(hi ? v[1] : v[3]);
-  return (odd ? b : a) + dpp_flip<0>(odd ? a : b);
+// f(integral_constant<int, 0>{}), ..., f(integral_constant<int, N - 1>{})
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void each(F f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    each<N, I + 1>(f);
+  }
 }
 
-__device__ __forceinline__ float quad_total(float x) {
+// v[k] summed over the LPC lanes, for the lane's own k.
+template <int LPC>
+__device__ __forceinline__ float lane_sums(float (&v)[LPC], int lane) {
+  if constexpr (LPC >= 8) halve_dpp<2, 4>(v, lane);
+  halve_dpp<1, 2>(v, lane);
+  halve_dpp<0, 1>(v, lane);
+  return v[0];
+}
+
+// x summed over the LPC lanes.
+template <int LPC>
+__device__ __forceinline__ float lane_total(float x) {
   x += dpp_flip<0>(x);
-  return x + dpp_flip<1>(x);
+  x += dpp_flip<1>(x);
+  if constexpr (LPC >= 8) x += dpp_flip<2>(x);
+  return x;
 }
 
 // log(1 + e^u), to float32's accuracy also where the result is small. With e = e^-|u| in (0, 1],
-// log(1 + e) = 2 atanh(s), s = e / (2 + e) <= 1/3, as the odd series s + s^3/3 + s^5/5 + ...: cut
-// after s^15/15, the remainder is below s (1/9)^8 / 17 * 9/8 < 2^-29 of the value.
+// log(1 + e) = 2 atanh(s), s = e / (2 + e) <= 1/3. 2 atanh(s) / s is an even function: a polynomial of
+// degree 4 in s^2, fitted on [0, 1/9] for the least relative error (Remez exchange), is 4e-9 off.
 __device__ __forceinline__ float softplus_f32(float u) {
   const float e = __builtin_amdgcn_exp2f(-kLog2E * fabsf(u));
   const float s = e * __builtin_amdgcn_rcpf(2.f + e), s2 = s * s;
-  float p = 2.f / 15.f;
-  p = fmaf(p, s2, 2.f / 13.f);
-  p = fmaf(p, s2, 2.f / 11.f);
-  p = fmaf(p, s2, 2.f / 9.f);
-  p = fmaf(p, s2, 2.f / 7.f);
-  p = fmaf(p, s2, 2.f / 5.f);
-  p = fmaf(p, s2, 2.f / 3.f);
+  float p = 0.28178334f;
+  p = fmaf(p, s2, 0.27960601f);
+  p = fmaf(p, s2, 0.40024909f);
+  p = fmaf(p, s2, 0.66666317f);
   p = fmaf(p, s2, 2.f);
   return fmaf(s, p, fmaxf(u, 0.f));
 }
@@ -65,14 +78,15 @@ __device__ __forceinline__ int segments_of(int len, int L) {
   return L && len > L ? (len - 1) / L + 1 : 1;
 }
 
+template <int CH>
 __device__ __forceinline__ ScanPlace scan_place(int64_t slot, int cb, const int32_t* cu, int N, int T, int D, int G,
                                                 int L) {
   ScanPlace p;
-  const int dg = D / G, per = (dg + kScanChannels - 1) / kScanChannels;
+  const int dg = D / G, per = (dg + CH - 1) / CH;
   p.g = cb / per;
-  const int in = (cb - p.g * per) * kScanChannels;
+  const int in = (cb - p.g * per) * CH;
   p.c0 = p.g * dg + in;
-  p.cl = min(kScanChannels, dg - in);
+  p.cl = min(CH, dg - in);
   p.slot = slot;
   if (!cu) {
     const int per_seq = L ? (T + L - 1) / L : 1;

@@ -8,9 +8,9 @@
 // Per (token, channel, state) one exponential, three multiplications and two fused multiply-adds
 // against 8 / S bytes of HBM per state (bf16): at S = 16 the vector ALU is the bound, not HBM, and
 // since A differs per channel and state no matrix product can take the work over. The kernel
-// therefore keeps everything but those six instructions out of the inner loop: B and C as float32 in
-// LDS, one 16-byte read per four of them; step sizes and gates formed once per (token, channel);
-// sums over the states transposed over the quad, four tokens at a time.
+// therefore keeps everything but those six instructions out of the inner loop: B, C, step sizes and
+// inputs as float32 in LDS, formed once; sums over the states halved over the channel's lanes, eight
+// tokens at a time.
 //
 // Parallel over sequences and channels; a batch with too few of them for the chip is cut along time
 // into segments of L tokens (scan_plan): every segment's end state from 0, a pass that carries the
@@ -21,7 +21,13 @@
 
 namespace comba {
 
-constexpr int kScanTile = 32;  // tokens per LDS tile
+// Tokens per LDS tile, channels per workgroup and lanes per channel of the forward. 32 channels make
+// workgroups of four wavefronts whose phases do not line up, so that one's barrier and loads hide
+// behind another's arithmetic; 8 lanes make twice the wavefronts of 4 for the same channels. Measured
+// at B = 8, T = 4096, D = 2048, S = 16, bf16 (8 lanes): 16 / 32 / 64 tokens 449 / 406 / 392 us at 32
+// channels, 32 tokens at 16 / 64 channels 413 / 417 us; 4 lanes 595 us, 16 lanes (16 channels)
+// 439 us. At B = 1, T = 65536, cut: 966 / 949 / 1028 us, 1055 / 952, 1140, 1089.
+constexpr int kScanTile = 32, kFwdChannels = 32, kFwdLanes = 8;
 
 template <typename T> struct ScanK {
   const T* x;
@@ -39,6 +45,7 @@ template <typename T> struct ScanK {
   float* hseg;
   float* dsum;
   int N, T_, D, S, G, L;
+  int64_t slots;
   bool softplus;
 };
 
@@ -55,23 +62,38 @@ __device__ __forceinline__ void store_states(float* row, int s0, int S, const fl
     if (s0 + i < S) row[s0 + i] = h[i];
 }
 
-// One workgroup: 64 channels over one segment. STATE: only the segment's end state from 0 and its
+// One workgroup: 32 channels over one segment. STATE: only the segment's end state from 0 and its
 // sum of step sizes, for the carry.
+//
+// Work per (token, channel) is done with a lane per channel, so that loads and stores take pieces of
+// rows: a thread forms the step size d and the input d x of its tokens and puts the pair into
+// LDS. The recurrence then runs with 8 lanes per channel, which read the pair, B and C from there
+// (a broadcast read costs the vector ALU nothing; taking them from a lane's register by DPP costs
+// 5 to 7 cycles instead of 4 for every use), and leaves y, summed over the states, in LDS, where the
+// channel's lane finds it behind the next barrier: one barrier per tile of TT tokens.
 template <typename T, int NPL, bool STATE>
-__global__ __launch_bounds__(kScanBlock) void scan_fwd_kernel(ScanK<T> a) {
-  constexpr int SP = 4 * NPL, TT = kScanTile, Q = TT / 4;
-  constexpr int PT = (TT * SP + kScanBlock - 1) / kScanBlock;  // B (and C) elements staged per thread
-  __shared__ __align__(16) float bc[2][TT][4][2 * NPL];
-  const int tid = threadIdx.x, lane = tid & 63, q = lane & 3;
-  const int cblocks = a.G * ((a.D / a.G + kScanChannels - 1) / kScanChannels);
-  const int cb = blockIdx.x % cblocks;
-  const ScanPlace p = scan_place(blockIdx.x / cblocks, cb, a.cu, a.N, a.T_, a.D, a.G, a.L);
+__global__ __launch_bounds__(kFwdChannels* kFwdLanes) void scan_fwd_kernel(ScanK<T> a) {
+  constexpr int LPC = kFwdLanes, TT = kScanTile, CH = kFwdChannels, SP = LPC * NPL, TH = CH * LPC, TG = TH / CH, R = TT / TG;  // R: tokens per thread, TG apart
+  constexpr int PT = (TT * SP + TH - 1) / TH;    // B (and C) elements staged per thread
+  constexpr int YP = CH + 64 / LPC;              // row of y, padded: the tokens of a store hit different banks
+  constexpr int AHEAD = NPL >= 16 ? 1 : 2;       // tokens read from LDS ahead
+  __shared__ __align__(16) float bc[2][TT][LPC][STATE ? NPL : 2 * NPL];
+  __shared__ __align__(16) f32x2 xd[2][TT][CH];
+  __shared__ float yb[STATE ? 1 : 2][STATE ? 1 : TT][YP];
+  const int tid = threadIdx.x, lane = tid & 63, q = lane & (LPC - 1);
+  // workgroups go round the 8 XCDs: neighbouring channels, which share lines, on one of them
+  const int cblocks = a.G * ((a.D / a.G + CH - 1) / CH);
+  const int per = (gridDim.x + 7) / 8, id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  const int cb = id % cblocks;
+  if (id >= a.slots * cblocks) return;
+  const ScanPlace p = scan_place<CH>(id / cblocks, cb, a.cu, a.N, a.T_, a.D, a.G, a.L);
   if (!p.ok) return;
   if (STATE && p.t1 >= p.s1) return;  // nothing follows the last segment
-  const int in = (tid >> 6) * 16 + (lane >> 2);
+
+  // the recurrence's channel and states
+  const int in = tid / LPC;
   const bool live = in < p.cl;
   const int c = p.c0 + (live ? in : p.cl - 1);
-
   float A2[NPL], h[NPL];
   load_states<NPL>(a.A + static_cast<int64_t>(c) * a.S, q * NPL, a.S, A2);
 #pragma unroll
@@ -83,101 +105,159 @@ __global__ __launch_bounds__(kScanBlock) void scan_fwd_kernel(ScanK<T> a) {
     if (a.L) load_states<NPL>(a.hseg + (p.slot * a.D + c) * SP, q * NPL, SP, h);
     else if (a.init) load_states<NPL>(a.init + (static_cast<int64_t>(p.n) * a.D + c) * a.S, q * NPL, a.S, h);
   }
-  const float bias = a.dt_bias ? a.dt_bias[c] : 0.f, skip = !STATE && a.skip ? a.skip[c] : 0.f;
 
-  // Elements of the tile that starts at token t: the lane's own token of each group of four, and the
-  // thread's share of B and C. Rows of the batch row: 32-bit offsets from the tile's first row.
+  // channel and first token for the work per token; threads behind the last channel read and write nowhere
+  const int ch = tid % CH, tk = tid / CH;
+  const bool have = ch < p.cl;
+  const int lc = p.c0 + (have ? ch : p.cl - 1);
+  const float bias = a.dt_bias ? a.dt_bias[lc] : 0.f, skip = !STATE && a.skip ? a.skip[lc] : 0.f;
+  const bool gated = a.z != nullptr;
+  const T* zp = gated ? a.z : a.x;  // without a gate x is loaded in its place, and not used
   const int64_t row0 = static_cast<int64_t>(p.b) * a.T_;
-  T rx[Q], rd[Q], rz[Q] = {}, rb[PT], rc[PT] = {};
-  auto fetch = [&](int t) {
-    const T* x = a.x + (row0 + t) * a.D;
-    const T* d = a.dt + (row0 + t) * a.D;
-    const T* z = a.z ? a.z + (row0 + t) * a.D : nullptr;
+  uint32_t own[R], boff[PT];  // byte offsets from the tile's first row
 #pragma unroll
-    for (int j = 0; j < Q; ++j) {
-      const uint32_t o = static_cast<uint32_t>(min(4 * j + q, p.t1 - 1 - t)) * static_cast<uint32_t>(a.D) + c;
-      rx[j] = x[o];
-      rd[j] = d[o];
-      if (!STATE && z) rz[j] = z[o];
+  for (int j = 0; j < R; ++j)
+    own[j] = have ? (static_cast<uint32_t>(tk + TG * j) * a.D + lc) * static_cast<uint32_t>(sizeof(T)) : kNowhere;
+#pragma unroll
+  for (int k = 0; k < PT; ++k) {
+    const int e = tid + k * TH, tt = e / SP, s = e % SP;
+    boff[k] = tt < TT && s < a.S ? (static_cast<uint32_t>(tt) * a.G * a.S + s) * static_cast<uint32_t>(sizeof(T)) : kNowhere;
+  }
+  uint32_t rx[R], rd[R], rz[R], rb[PT], rc[PT];
+  auto fetch = [&](int t) {
+    const int rows = max(0, min(TT, p.t1 - t));
+    const int64_t at = (row0 + t) * a.D, bytes = static_cast<int64_t>(rows) * a.D * sizeof(T);
+    const Range<T> x(a.x + at, bytes), d(a.dt + at, bytes), z(zp + at, STATE ? 0 : bytes);
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      rx[j] = x.load(own[j]);
+      rd[j] = d.load(own[j]);
+      if (!STATE) rz[j] = z.load(own[j]);
     }
-    const int64_t bo = ((row0 + t) * a.G + p.g) * a.S;
-    const T* B = a.Bm + bo;
-    const T* C = a.Cm + bo;
+    const int64_t bat = ((row0 + t) * a.G + p.g) * a.S;
+    const int64_t bbytes = rows ? (static_cast<int64_t>(rows - 1) * a.G * a.S + a.S) * sizeof(T) : 0;
+    const Range<T> B(a.Bm + bat, bbytes), C(a.Cm + bat, STATE ? 0 : bbytes);
 #pragma unroll
     for (int k = 0; k < PT; ++k) {
-      const int e = tid + k * kScanBlock, tt = e / SP, s = e % SP;
-      const bool have = tt < TT && t + tt < p.t1 && s < a.S;
-      const uint32_t o = have ? static_cast<uint32_t>(tt) * a.G * a.S + s : 0u;
-      rb[k] = have ? B[o] : T(0);
-      if (!STATE) rc[k] = have ? C[o] : T(0);
+      rb[k] = B.load(boff[k]);
+      if (!STATE) rc[k] = C.load(boff[k]);
+    }
+  };
+  // The fetched elements become the next tile in LDS; x and the gate stay with the lane.
+  float xv[R], zv[R], dtot = 0.f;
+  auto stage = [&](int t, int buf) {
+#pragma unroll
+    for (int k = 0; k < PT; ++k) {
+      const int e = tid + k * TH, tt = e / SP, s = e % SP;
+      if (PT * TH == TT * SP || tt < TT) {
+        bc[buf][tt][s / NPL][s % NPL] = Range<T>::value(rb[k]);
+        if (!STATE) bc[buf][tt][s / NPL][NPL + s % NPL] = Range<T>::value(rc[k]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      xv[j] = Range<T>::value(rx[j]);
+      const float u = Range<T>::value(rd[j]) + bias;
+      float d = softplus_f32(u);
+      pin(d);
+      d = a.softplus ? d : u;
+      if (t + tk + TG * j >= p.t1) d = 0.f;  // tokens behind the segment: decay 1, no input
+      if (STATE) dtot += d;
+      xd[buf][tk + TG * j][ch] = f32x2{d, d * xv[j]};
+      if (!STATE) zv[j] = Range<T>::value(rz[j]);
+    }
+  };
+  // Gate and store of the tile at t, whose y is complete in LDS; px, pz: its x and gate.
+  auto finish = [&](int t, int buf, const float (&px)[R], const float (&pz)[R]) {
+    const Range<T> out(a.y + (row0 + t) * a.D, static_cast<int64_t>(min(TT, p.t1 - t)) * a.D * sizeof(T));
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      float s = pz[j] * sigmoid_fast(pz[j]);
+      pin(s);
+      const float y = fmaf(skip, px[j], yb[buf][tk + TG * j][ch]);
+      out.store(own[j], gated ? y * s : y);
     }
   };
 
-  float dtot = 0.f;
+  fetch(p.t0);
+  stage(p.t0, 0);
+  fetch(p.t0 + TT);
   int buf = 0;
-  if (p.t0 < p.t1) fetch(p.t0);
+  float px[R], pz[R];
   for (int t = p.t0; t < p.t1; t += TT, buf ^= 1) {
+    __syncthreads();  // the tile is staged, the last one's y complete; the other buffers are free
+    if (!STATE && t > p.t0) finish(t - TT, buf ^ 1, px, pz);
+    if (!STATE)
 #pragma unroll
-    for (int k = 0; k < PT; ++k) {
-      const int e = tid + k * kScanBlock, tt = e / SP, s = e % SP;
-      if (tt < TT) {
-        bc[buf][tt][s / NPL][s % NPL] = Elem<T>::load(&rb[k], 0);
-        if (!STATE) bc[buf][tt][s / NPL][NPL + s % NPL] = Elem<T>::load(&rc[k], 0);
+      for (int j = 0; j < R; ++j) {
+        px[j] = xv[j];
+        pz[j] = zv[j];
       }
-    }
-    T cx[Q], cd[Q], cz[Q];
+    // What the next AHEAD tokens need is read while the present ones are worked on: the scheduling
+    // barrier keeps the compiler from moving the reads down to their use.
+    f32x2 dn[AHEAD], dc[AHEAD];
+    float bn[AHEAD][2 * NPL], bcur[AHEAD][2 * NPL];
+    auto pull = [&](int tt) {
 #pragma unroll
-    for (int j = 0; j < Q; ++j) {
-      cx[j] = rx[j];
-      cd[j] = rd[j];
-      cz[j] = rz[j];
-    }
-    if (t + TT < p.t1) fetch(t + TT);
-    __syncthreads();  // one barrier per tile: the other buffer is written again only behind the next one
+      for (int k = 0; k < AHEAD; ++k) {
+        dn[k] = xd[buf][tt + k][in];
 #pragma unroll
-    for (int j = 0; j < Q; ++j) {
-      const int mine = t + 4 * j + q;
-      const bool in_seg = mine < p.t1;
-      const float xv = Elem<T>::load(&cx[j], 0);
-      float dl = Elem<T>::load(&cd[j], 0) + bias;
-      if (a.softplus) dl = softplus_f32(dl);
-      if (!in_seg) dl = 0.f;                       // tokens behind the segment: decay 1, no input
-      const float dx = in_seg ? dl * xv : 0.f;
-      if (STATE) dtot += dl;
-      float ys[4];
-      auto token = [&](auto kc) {
+        for (int i = 0; i < (STATE ? NPL : 2 * NPL); ++i) bn[k][i] = bc[buf][tt + k][q][i];
+      }
+    };
+    pull(0);
+#pragma unroll
+    for (int j = 0; j < TT / LPC; ++j) {
+      float ys[LPC];
+      each<LPC>([&](auto kc) {
         constexpr int K = decltype(kc)::value;
-        const float dk = quad_bcast<K>(dl), xk = quad_bcast<K>(dx);
-        const float* r = bc[buf][4 * j + K][q];
-        float y = 0.f;
+        if constexpr (K % AHEAD == 0) {
+#pragma unroll
+          for (int k = 0; k < AHEAD; ++k) {
+            dc[k] = dn[k];
+#pragma unroll
+            for (int i = 0; i < (STATE ? NPL : 2 * NPL); ++i) bcur[k][i] = bn[k][i];
+          }
+          if (LPC * j + K + AHEAD < TT) pull(LPC * j + K + AHEAD);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        const f32x2 dd = dc[K % AHEAD];
+        const float(&r)[2 * NPL] = bcur[K % AHEAD];
+        float o = 0.f;
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
-          const float e = __builtin_amdgcn_exp2f(dk * A2[i]);
-          h[i] = fmaf(e, h[i], xk * r[i]);
-          if (!STATE) y = fmaf(h[i], r[NPL + i], y);
+          const float e = __builtin_amdgcn_exp2f(dd[0] * A2[i]);
+          h[i] = fmaf(e, h[i], dd[1] * r[i]);
+          if (!STATE) o = i ? fmaf(h[i], r[NPL + i], o) : h[i] * r[NPL];
         }
-        ys[K] = y;
-      };
-      token(std::integral_constant<int, 0>{});
-      token(std::integral_constant<int, 1>{});
-      token(std::integral_constant<int, 2>{});
-      token(std::integral_constant<int, 3>{});
-      if (!STATE) {
-        float y = fmaf(skip, xv, quad_sums(ys, q));
-        if (a.z) {
-          const float zv = Elem<T>::load(&cz[j], 0);
-          y *= zv * sigmoid_fast(zv);
-        }
-        if (in_seg && live) Elem<T>::store(a.y + (row0 + t) * a.D, static_cast<uint32_t>(4 * j + q) * static_cast<uint32_t>(a.D) + c, y);
-      }
+        if constexpr (K % AHEAD == AHEAD - 1)
+#pragma unroll
+          for (int i = 0; i < NPL; ++i) pin(h[i]);
+        ys[K] = o;
+      });
+      if (!STATE) yb[buf][LPC * j + q][in] = lane_sums<LPC>(ys, lane);
     }
+    // Staged before the next tile's loads and behind no new store: the wait for the loads waits for
+    // nothing else.
+    stage(t + TT, buf ^ 1);
+    fetch(t + 2 * TT);
   }
-  if (!live) return;
+  if (!STATE && p.t0 < p.t1) {
+    __syncthreads();
+    finish(p.t0 + (p.t1 - 1 - p.t0) / TT * TT, buf ^ 1, px, pz);
+  }
   if (STATE) {
-    store_states<NPL>(a.hseg + (p.slot * a.D + c) * SP, q * NPL, SP, h);
-    dtot = quad_total(dtot);
-    if (q == 0) a.dsum[p.slot * a.D + c] = dtot;
-  } else if (a.fin && p.t1 >= p.s1) {
+    __shared__ float tot[TG][CH];
+    tot[tk][ch] = dtot;
+    __syncthreads();
+    if (tk == 0 && have) {
+      float s = 0.f;
+#pragma unroll
+      for (int w = 0; w < TG; ++w) s += tot[w][ch];
+      a.dsum[p.slot * a.D + lc] = s;
+    }
+    if (live) store_states<NPL>(a.hseg + (p.slot * a.D + c) * SP, q * NPL, SP, h);
+  } else if (live && a.fin && p.t1 >= p.s1) {
     store_states<NPL>(a.fin + (static_cast<int64_t>(p.n) * a.D + c) * a.S, q * NPL, a.S, h);
   }
 }
@@ -229,7 +309,7 @@ __global__ __launch_bounds__(kScanBlock) void scan_step_kernel(
     bool softplus, const float* init, int N, int64_t D, int S, int G, int per, T* __restrict__ y, float* fin) {
   const int lane = threadIdx.x & 63, q = lane & 3;
   const int cblocks = G * ((static_cast<int>(D) / G + kScanChannels - 1) / kScanChannels);
-  const ScanPlace p = scan_place(0, blockIdx.x % cblocks, nullptr, 1, 1, static_cast<int>(D), G, 0);
+  const ScanPlace p = scan_place<kScanChannels>(0, blockIdx.x % cblocks, nullptr, 1, 1, static_cast<int>(D), G, 0);
   const int in = (threadIdx.x >> 6) * 16 + (lane >> 2);
   if (in >= p.cl) return;
   const int c = p.c0 + in, s0 = q * NPL;
@@ -268,7 +348,7 @@ __global__ __launch_bounds__(kScanBlock) void scan_step_kernel(
       h[i] = fmaf(__builtin_amdgcn_exp2f(dl * A2[i]), h[i], dx * b);
       o = fmaf(h[i], cc, o);
     }
-    o = fmaf(sk, xv, quad_total(o));
+    o = fmaf(sk, xv, lane_total<4>(o));
     if (z) {
       const float zv = Elem<T>::load(z, n * D + c);
       o *= zv * sigmoid_fast(zv);
@@ -290,29 +370,28 @@ __global__ __launch_bounds__(kScanBlock) void scan_step_kernel(
 // --- launches -----------------------------------------------------------------------------------
 
 int scan_padded_states(int S) {
-  int sp = 4;
+  int sp = 8;
   while (sp < S) sp *= 2;
   return sp;
 }
 
-int64_t scan_channel_blocks(int64_t D, int64_t G) { return G * ((D / G + kScanChannels - 1) / kScanChannels); }
+int64_t scan_channel_blocks(int64_t D, int64_t G) { return G * ((D / G + kFwdChannels - 1) / kFwdChannels); }
 
-// Cutting costs a second pass over the inputs and the exponentials (about 3/4 of a scan), so it pays
-// where less than half of the 256 compute units would have a workgroup. Segments then make about
-// 1024 workgroups (a wavefront per SIMD four times over), of 256 tokens at least. In a packed batch
-// the lengths are unknown here: no sequence may run longer than the whole batch's share of a
-// compute unit, at least 512 tokens.
+// Cutting costs a second pass over the inputs and the exponentials (about half a scan), so it pays
+// where the uncut scan leaves SIMDs with one wavefront or none, 256 workgroups of four wavefronts.
+// Measured at D = 2048, S = 16, T = 4096, bf16, uncut / cut: 261 / 79 us for B = 1, 265 / 136 for 2,
+// 261 / 183 for 3, 271 / 237 for 4, 359 / 343 for 6; at B = 1, T = 65536 4640 / 874. Segments make
+// 1024 workgroups, within 128 tokens (B = 1, T = 1024: 32 us against 42 with 256) and 1024 tokens
+// (T = 65536: 874 us, 951 with 4096).
+// A packed batch's lengths are not known here. Its long sequences are cut, to 512 tokens at the most
+// (64 lognormal sequences, 47204 tokens: 742 us, 966 uncut), but where there are enough sequences to
+// fill the chip not below their mean length, so that sequences of one length stay whole.
 ScanPlan scan_plan(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N, bool packed) {
-  const int64_t cb = scan_channel_blocks(D, G);
-  int64_t L;
-  if (packed) {
-    L = T * cb / 256;
-    L = L < 512 ? 512 : L;
-  } else {
-    if (B * cb > 128) return ScanPlan{0, N};
-    L = B * T * cb / 1024;
-    L = L < 256 ? 256 : L;
-  }
+  const int64_t cb = scan_channel_blocks(D, G), most = packed ? 512 : 1024;
+  if (!packed && B * cb > 256) return ScanPlan{0, N};
+  int64_t L = B * T * cb / 2048;
+  L = L < 128 ? 128 : (L > most ? most : L);
+  if (packed && N * cb >= 512 && L < (T + N - 1) / N) L = (T + N - 1) / N;
   L = (L + kScanTile - 1) / kScanTile * kScanTile;
   if (L >= T) return ScanPlan{0, N};
   return ScanPlan{static_cast<int>(L), packed ? T / L + N + 1 : B * ((T + L - 1) / L)};
@@ -322,26 +401,26 @@ template <typename T, int NPL>
 static hipError_t scan_t(const ScanArgs& a, const ScanPlan& p, float* hseg, float* dsum, hipStream_t st) {
   const ScanK<T> k{static_cast<const T*>(a.x), static_cast<const T*>(a.dt), a.A, static_cast<const T*>(a.Bm),
                    static_cast<const T*>(a.Cm), a.skip, static_cast<const T*>(a.z), a.dt_bias, a.init, a.cu_seqlens,
-                   static_cast<T*>(a.y), a.fin, hseg, dsum, a.N, a.T, a.D, a.S, a.G, p.L, a.softplus};
-  const int64_t cb = scan_channel_blocks(a.D, a.G);
-  const unsigned grid = static_cast<unsigned>(p.slots * cb);
+                   static_cast<T*>(a.y), a.fin, hseg, dsum, a.N, a.T, a.D, a.S, a.G, p.L, p.slots, a.softplus};
+  constexpr int TH = kFwdChannels * kFwdLanes, SP = kFwdLanes * NPL;
+  const unsigned grid = static_cast<unsigned>((p.slots * scan_channel_blocks(a.D, a.G) + 7) / 8 * 8);
   if (p.L) {
-    scan_fwd_kernel<T, NPL, true><<<grid, kScanBlock, 0, st>>>(k);
+    scan_fwd_kernel<T, NPL, true><<<grid, TH, 0, st>>>(k);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const int64_t threads = static_cast<int64_t>(a.N) * a.D * 4 * NPL;
+    const int64_t threads = static_cast<int64_t>(a.N) * a.D * SP;
     scan_carry_kernel<<<static_cast<unsigned>((threads + kScanBlock - 1) / kScanBlock), kScanBlock, 0, st>>>(
-        a.A, a.init, a.cu_seqlens, a.N, a.T, a.D, a.S, 4 * NPL, p.L, hseg, dsum);
+        a.A, a.init, a.cu_seqlens, a.N, a.T, a.D, a.S, SP, p.L, hseg, dsum);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  scan_fwd_kernel<T, NPL, false><<<grid, kScanBlock, 0, st>>>(k);
+  scan_fwd_kernel<T, NPL, false><<<grid, TH, 0, st>>>(k);
   return hipGetLastError();
 }
 
 template <typename T, int NPL>
 static hipError_t scan_step_t(const ScanArgs& a, hipStream_t st) {
-  const int64_t cb = scan_channel_blocks(a.D, a.G);
+  const int64_t cb = a.G * ((a.D / a.G + kScanChannels - 1) / kScanChannels);
   // sequences per workgroup: up to 8 while eight workgroups per compute unit remain
   int64_t per = a.N * cb / 2048;
   per = per < 1 ? 1 : (per > 8 ? 8 : per);
@@ -361,6 +440,19 @@ static hipError_t scan_step_t(const ScanArgs& a, hipStream_t st) {
   return run(std::false_type{});
 }
 
+hipError_t launch_scan(const ScanArgs& a, const ScanPlan& p, float* hseg, float* dsum, hipStream_t st) {
+  auto run = [&](auto npl) {
+    constexpr int NPL = decltype(npl)::value;
+    return a.dtype == COMBA_BF16 ? scan_t<u16, NPL>(a, p, hseg, dsum, st) : scan_t<float, NPL>(a, p, hseg, dsum, st);
+  };
+  switch (scan_padded_states(a.S)) {
+    case 8: return run(std::integral_constant<int, 1>{});
+    case 16: return run(std::integral_constant<int, 2>{});
+    case 32: return run(std::integral_constant<int, 4>{});
+    default: return run(std::integral_constant<int, 8>{});
+  }
+}
+
 template <typename F>
 static hipError_t with_states(int S, F f) {
   if (S <= 4) return f(std::integral_constant<int, 1>{});
@@ -368,13 +460,6 @@ static hipError_t with_states(int S, F f) {
   if (S <= 16) return f(std::integral_constant<int, 4>{});
   if (S <= 32) return f(std::integral_constant<int, 8>{});
   return f(std::integral_constant<int, 16>{});
-}
-
-hipError_t launch_scan(const ScanArgs& a, const ScanPlan& p, float* hseg, float* dsum, hipStream_t st) {
-  return with_states(a.S, [&](auto npl) {
-    constexpr int NPL = decltype(npl)::value;
-    return a.dtype == COMBA_BF16 ? scan_t<u16, NPL>(a, p, hseg, dsum, st) : scan_t<float, NPL>(a, p, hseg, dsum, st);
-  });
 }
 
 hipError_t launch_scan_step(const ScanArgs& a, hipStream_t st) {

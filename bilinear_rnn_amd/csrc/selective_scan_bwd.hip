@@ -151,7 +151,7 @@ __global__ __launch_bounds__(kScanBlock) void scan_bwd_ends_kernel(ScanBwdK<T> a
   __shared__ __align__(16) float bc[L][4][2 * NPL];
   const int tid = threadIdx.x, lane = tid & 63, q = lane & 3;
   const int cblocks = a.G * ((a.D / a.G + kScanChannels - 1) / kScanChannels);
-  const ScanPlace p = scan_place(blockIdx.x / cblocks, blockIdx.x % cblocks, a.cu, a.N, a.T_, a.D, a.G, L);
+  const ScanPlace p = scan_place<kScanChannels>(blockIdx.x / cblocks, blockIdx.x % cblocks, a.cu, a.N, a.T_, a.D, a.G, L);
   if (!p.ok) return;
   stage_bc<T, NPL, L>(a, p, bc);
   const int in = (tid >> 6) * 16 + (lane >> 2);
@@ -215,7 +215,7 @@ __global__ __launch_bounds__(kScanBlock) void scan_bwd_ends_kernel(ScanBwdK<T> a
     a.hseg[at + i] = h[i];
     a.gseg[at + i] = gs[i];
   }
-  dtot = quad_total(dtot);
+  dtot = lane_total<4>(dtot);
   if (q == 0) a.dsum[p.slot * a.D + c] = dtot;
 }
 
@@ -272,7 +272,7 @@ __global__ __launch_bounds__(kScanBlock) void scan_bwd_kernel(ScanBwdK<T> a) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, q = lane & 3;
   const int dg = a.D / a.G, per = (dg + kScanChannels - 1) / kScanChannels, cblocks = a.G * per;
   const int cb = blockIdx.x % cblocks;
-  const ScanPlace p = scan_place(blockIdx.x / cblocks, cb, a.cu, a.N, a.T_, a.D, a.G, L);
+  const ScanPlace p = scan_place<kScanChannels>(blockIdx.x / cblocks, cb, a.cu, a.N, a.T_, a.D, a.G, L);
   const int in = wave * 16 + (lane >> 2);
   const bool live = in < p.cl;
   const int c = p.c0 + (live ? in : p.cl - 1);
@@ -375,7 +375,7 @@ __global__ __launch_bounds__(kScanBlock) void scan_bwd_kernel(ScanBwdK<T> a) {
       token(std::integral_constant<int, 1>{});
       token(std::integral_constant<int, 2>{});
       token(std::integral_constant<int, 3>{});
-      yr[j] = quad_sums(ys, q);
+      yr[j] = lane_sums<4>(ys, lane);
     }
 #pragma unroll
     for (int j = Q - 1; j >= 0; --j) {
@@ -408,7 +408,7 @@ __global__ __launch_bounds__(kScanBlock) void scan_bwd_kernel(ScanBwdK<T> a) {
       token(std::integral_constant<int, 2>{});
       token(std::integral_constant<int, 1>{});
       token(std::integral_constant<int, 0>{});
-      const float b = quad_sums(sb, q), d = quad_sums(sa, q) * (1.f / kLog2E);
+      const float b = lane_sums<4>(sb, lane), d = lane_sums<4>(sa, lane) * (1.f / kLog2E);
       if (live && k * CT + 4 * j + q < len) {
         const int64_t o = (row0 + k * CT + 4 * j + q) * a.D + c;
         Elem<T>::store(a.dx, o, fmaf(dl[j], b, skip * dyp[j]));
@@ -438,8 +438,8 @@ __global__ __launch_bounds__(kScanBlock) void scan_bwd_kernel(ScanBwdK<T> a) {
   if (!live) return;
 #pragma unroll
   for (int i = 0; i < NPL; ++i) a.dApart[at + i] = dA[i];
-  dskip = quad_total(dskip);
-  dbias = quad_total(dbias);
+  dskip = lane_total<4>(dskip);
+  dbias = lane_total<4>(dbias);
   if (q == 0) {
     a.dDpart[dpart] = dskip;
     a.dDpart[dpart + a.D] = dbias;
@@ -467,10 +467,12 @@ __global__ __launch_bounds__(kScanBlock) void scan_bwd_bc_kernel(const float* __
   Elem<T>::store(which ? dC : dB, rg * S + s, v);
 }
 
+int64_t scan_bwd_channel_blocks(int64_t D, int64_t G) { return G * ((D / G + kScanChannels - 1) / kScanChannels); }
+
 ScanPlan scan_bwd_plan(int64_t B, int64_t T, int64_t N, int S, bool packed) {
   const int npl = scan_padded_states(S) / 4;
   const int L = npl <= 4 ? BwdTile<4>::L : npl == 8 ? BwdTile<8>::L : BwdTile<16>::L;
-  static_assert(BwdTile<1>::L == BwdTile<4>::L && BwdTile<2>::L == BwdTile<4>::L, "one segment length up to 16 states");
+  static_assert(BwdTile<2>::L == BwdTile<4>::L, "one segment length up to 16 states");
   return ScanPlan{L, packed ? T / L + N + 1 : B * ((T + L - 1) / L)};
 }
 
@@ -483,7 +485,7 @@ static hipError_t scan_bwd_t(const ScanBwdArgs& a, const ScanPlan& p, hipStream_
                       static_cast<const T*>(a.dy), a.dfin, static_cast<T*>(a.dx), static_cast<T*>(a.ddt),
                       static_cast<T*>(a.dz), a.dinit, a.hseg, a.gseg, a.dsum, a.dApart, a.dDpart, a.dBCpart,
                       f.N, f.T, f.D, f.S, f.G, p.L, f.softplus};
-  const int64_t cb = scan_channel_blocks(f.D, f.G), rows = static_cast<int64_t>(f.B) * f.T;
+  const int64_t cb = scan_bwd_channel_blocks(f.D, f.G), rows = static_cast<int64_t>(f.B) * f.T;
   const unsigned grid = static_cast<unsigned>(p.slots * cb);
   hipError_t e;
   scan_bwd_ends_kernel<T, NPL><<<grid, kScanBlock, 0, st>>>(k);
@@ -526,7 +528,6 @@ hipError_t launch_scan_bwd(const ScanBwdArgs& a, const ScanPlan& p, hipStream_t 
     return a.f.dtype == COMBA_BF16 ? scan_bwd_t<u16, NPL>(a, p, st) : scan_bwd_t<float, NPL>(a, p, st);
   };
   switch (scan_padded_states(a.f.S)) {
-    case 4: return run(std::integral_constant<int, 1>{});
     case 8: return run(std::integral_constant<int, 2>{});
     case 16: return run(std::integral_constant<int, 4>{});
     case 32: return run(std::integral_constant<int, 8>{});
