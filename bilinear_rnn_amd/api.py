@@ -495,31 +495,40 @@ def _debug_check(alpha: torch.Tensor, cu_seqlens: Optional[torch.Tensor], T: int
 
 # --- layer operators around the recurrence -----------------------------------------------------------
 
-def _same_device(first: torch.Tensor, **others):
-    for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name} is on {t.device}, not on {first.device}: all tensors must share one device")
+def _need(t: torch.Tensor, name: str, dtype, shape, index: int):
+    """A required tensor: one combined test, and the reason only where it fails. Decoding calls take
+    a few microseconds on the GPU, so these checks count."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
+    _require(t, name, dtype, shape)
+    raise ValueError(f"{name} is on {t.device}, not on cuda:{index}: all tensors must share one device")
 
 
-def _optional(t: Optional[torch.Tensor], name: str, dtype, shape):
+def _may(t: Optional[torch.Tensor], name: str, dtype, shape, index: int):
     if t is not None:
-        _require(t, name, dtype, shape)
+        _need(t, name, dtype, shape, index)
 
 
-def _activation(t: torch.Tensor, name: str, dims: int):
+def _activation(t: torch.Tensor, name: str, dims: int) -> int:
+    """Checks the tensor that the others are measured by; returns its device's index."""
     _require(t, name)
     if t.dtype not in _DT:
         raise ValueError(f"{name} must be bfloat16 or float32 (got {t.dtype})")
     if t.dim() != dims:
         raise ValueError(f"{name} must have {dims} dimensions (got {tuple(t.shape)})")
+    return t.get_device()
 
 
-def _sequences(B: int, T: int, cu_seqlens: Optional[torch.Tensor]) -> int:
+def _sequences(B: int, T: int, cu_seqlens: Optional[torch.Tensor], index: int) -> int:
     if cu_seqlens is None:
         return B
     _require(cu_seqlens, "cu_seqlens", torch.int32)
     if cu_seqlens.dim() != 1:
         raise ValueError("cu_seqlens must have one dimension")
+    _need(cu_seqlens, "cu_seqlens", torch.int32, cu_seqlens.shape, index)
     if DEBUG_CHECKS:
         none = torch.empty((1,), dtype=torch.float32, device=cu_seqlens.device)
         _debug_check(none, cu_seqlens, T, check_alpha=False)
@@ -542,29 +551,37 @@ def _workspace(workspace: Optional[torch.Tensor], nbytes: int, device) -> Option
 def _at(t: Optional[torch.Tensor]):
     """Address of a tensor; an empty one has none, but the library wants required tensors non-NULL
     (it reads nothing of an empty one)."""
-    if t is not None and t.numel() == 0:
-        return ctypes.c_void_p(256)
-    return _ptr(t)
-
-
-def _stream(device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    if t is None:
+        return None
+    return t.data_ptr() or (256 if t.numel() == 0 else None)
 
 
 def _ws(workspace: Optional[torch.Tensor]):
     return _at(workspace), 0 if workspace is None else workspace.numel()
 
 
-def _conv_args(x, weight, bias, initial_state, N, dims):
-    _activation(x, "x", dims)
+# The current stream's handle without building a torch.cuda.Stream, where torch has that.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _run(fn, index: int, *args):
+    """Calls an entry point on the device's current stream."""
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return _run(fn, index, *args)
+    status = fn(*args, _raw_stream(index) if _raw_stream else torch.cuda.current_stream(index).cuda_stream)
+    if status != COMBA_OK:
+        _check(status)
+
+
+def _conv_args(x, weight, bias, initial_state, N, index):
     D = x.shape[-1]
     if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("weight must be a [D, W] tensor")
     W = weight.shape[1]
-    _require(weight, "weight", torch.float32, (D, W))
-    _optional(bias, "bias", torch.float32, (D,))
-    _optional(initial_state, "initial_state", x.dtype, (N, W - 1, D))
-    _same_device(x, weight=weight, bias=bias, initial_state=initial_state)
+    _need(weight, "weight", torch.float32, (D, W), index)
+    _may(bias, "bias", torch.float32, (D,), index)
+    _may(initial_state, "initial_state", x.dtype, (N, W - 1, D), index)
     return D, W
 
 
@@ -575,22 +592,22 @@ def short_conv(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
     """Short causal depthwise convolution (2 to 4 taps) with optional SiLU through
     ``comba_short_conv_fwd``. x [B, T, D], weight [D, W] and bias [D] float32; the state holds the
     last W - 1 inputs of every sequence, [N, W - 1, D] in x's type. Returns (y, final_state)."""
-    _activation(x, "x", 3)
+    index = _activation(x, "x", 3)
     B, T, _ = x.shape
-    N = _sequences(B, T, cu_seqlens)
-    D, W = _conv_args(x, weight, bias, initial_state, N, 3)
+    N = _sequences(B, T, cu_seqlens, index)
+    D, W = _conv_args(x, weight, bias, initial_state, N, index)
     if out is None:
         out = torch.empty_like(x)
-    _require(out, "out", x.dtype, (B, T, D))
-    if final_state is None and output_final_state:
+    else:
+        _need(out, "out", x.dtype, (B, T, D), index)
+    if final_state is not None or not output_final_state:
+        _may(final_state, "final_state", x.dtype, (N, W - 1, D), index)
+    else:
         final_state = torch.empty((N, W - 1, D), dtype=x.dtype, device=x.device)
-    _optional(final_state, "final_state", x.dtype, (N, W - 1, D))
-    _same_device(x, cu_seqlens=cu_seqlens, out=out, final_state=final_state)
-    with torch.cuda.device(x.device):
-        _check(lib().comba_short_conv_fwd(
-            _at(x), _at(weight), _at(bias), _at(initial_state), _at(cu_seqlens),
-            N if cu_seqlens is not None else 0, B, T, D, W, _DT[x.dtype], int(bool(silu)), _at(out),
-            _at(final_state), _stream(x.device)))
+    _run(lib().comba_short_conv_fwd, index,
+         _at(x), _at(weight), _at(bias), _at(initial_state), _at(cu_seqlens),
+         N if cu_seqlens is not None else 0, B, T, D, W, _DT[x.dtype], int(bool(silu)), _at(out),
+         _at(final_state))
     return out, final_state
 
 
@@ -600,29 +617,29 @@ def short_conv_step(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.
                     final_state: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """One token per sequence through ``comba_short_conv_step``: x [N, D]. With ``in_place`` the
     state is updated in ``initial_state`` itself. Returns (y, final_state)."""
-    _activation(x, "x", 2)
+    index = _activation(x, "x", 2)
     N = x.shape[0]
-    D, W = _conv_args(x, weight, bias, initial_state, N, 2)
+    D, W = _conv_args(x, weight, bias, initial_state, N, index)
     if out is None:
         out = torch.empty_like(x)
-    _require(out, "out", x.dtype, (N, D))
-    final_state = _step_state(initial_state, final_state, in_place, output_final_state, (N, W - 1, D), x.dtype, x.device)
-    _same_device(x, out=out, final_state=final_state)
-    with torch.cuda.device(x.device):
-        _check(lib().comba_short_conv_step(
-            _at(x), _at(weight), _at(bias), _at(initial_state), N, D, W, _DT[x.dtype], int(bool(silu)), _at(out),
-            _at(final_state), _stream(x.device)))
+    else:
+        _need(out, "out", x.dtype, (N, D), index)
+    final_state = _step_state(initial_state, final_state, in_place, output_final_state, (N, W - 1, D), x.dtype,
+                              x.device, index)
+    _run(lib().comba_short_conv_step, index,
+         _at(x), _at(weight), _at(bias), _at(initial_state), N, D, W, _DT[x.dtype], int(bool(silu)), _at(out),
+         _at(final_state))
     return out, final_state
 
 
-def _step_state(initial_state, final_state, in_place, output_final_state, shape, dtype, device):
+def _step_state(initial_state, final_state, in_place, output_final_state, shape, dtype, device, index):
     if in_place:
         if initial_state is None:
             raise ValueError("in_place requires initial_state")
         return initial_state
     if final_state is None and output_final_state:
         return torch.empty(shape, dtype=dtype, device=device)
-    _optional(final_state, "final_state", dtype, shape)
+    _may(final_state, "final_state", dtype, shape, index)
     return final_state
 
 
@@ -633,15 +650,15 @@ def short_conv_bwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.T
     """Gradients of ``short_conv`` through ``comba_short_conv_bwd``, from its inputs alone. dy has x's
     type or float32 (what ``chunk_bwd`` returns). Returns dx and dinitial_state in x's type (the
     latter None without an initial state), dweight and dbias (None without bias) in float32."""
-    _activation(x, "x", 3)
+    index = _activation(x, "x", 3)
     B, T, _ = x.shape
-    N = _sequences(B, T, cu_seqlens)
-    D, W = _conv_args(x, weight, bias, initial_state, N, 3)
-    _require(dy, "dy", None, (B, T, D))
+    N = _sequences(B, T, cu_seqlens, index)
+    D, W = _conv_args(x, weight, bias, initial_state, N, index)
+    _require(dy, "dy")
     if dy.dtype not in (x.dtype, torch.float32):
         raise ValueError(f"dy must be {x.dtype} or float32 (got {dy.dtype})")
-    _optional(d_final_state, "d_final_state", x.dtype, (N, W - 1, D))
-    _same_device(x, dy=dy, cu_seqlens=cu_seqlens, d_final_state=d_final_state)
+    _need(dy, "dy", dy.dtype, (B, T, D), index)
+    _may(d_final_state, "d_final_state", x.dtype, (N, W - 1, D), index)
     nseq = N if cu_seqlens is not None else 0
     L = lib()
     f32 = dict(dtype=torch.float32, device=x.device)
@@ -649,34 +666,32 @@ def short_conv_bwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.T
              dbias=None if bias is None else torch.empty((D,), **f32),
              dinitial_state=None if initial_state is None else torch.empty_like(initial_state))
     workspace = _workspace(workspace, int(L.comba_short_conv_bwd_workspace_size(B, T, D, W, nseq)), x.device)
-    with torch.cuda.device(x.device):
-        _check(L.comba_short_conv_bwd(
-            _at(x), _at(weight), _at(bias), _at(initial_state), _at(cu_seqlens), nseq, B, T, D, W, _DT[x.dtype],
-            int(bool(silu)), _at(dy), _DT[dy.dtype], _at(d_final_state), _at(g["dx"]), _at(g["dweight"]),
-            _at(g["dbias"]), _at(g["dinitial_state"]), *_ws(workspace), _stream(x.device)))
+    _run(L.comba_short_conv_bwd, index,
+         _at(x), _at(weight), _at(bias), _at(initial_state), _at(cu_seqlens), nseq, B, T, D, W, _DT[x.dtype],
+         int(bool(silu)), _at(dy), _DT[dy.dtype], _at(d_final_state), _at(g["dx"]), _at(g["dweight"]),
+         _at(g["dbias"]), _at(g["dinitial_state"]), *_ws(workspace))
     return g
 
 
-def _scan_args(x, dt, A, Bm, Cm, skip, z, dt_bias, initial_state, N):
+def _scan_args(x, dt, A, Bm, Cm, skip, z, dt_bias, initial_state, N, index):
     rows = tuple(x.shape[:-1])
     D = x.shape[-1]
     if not isinstance(A, torch.Tensor) or A.dim() != 2:
         raise ValueError("A must be a [D, S] tensor")
     S = A.shape[1]
-    _require(A, "A", torch.float32, (D, S))
-    _require(dt, "dt", x.dtype, rows + (D,))
+    _need(A, "A", torch.float32, (D, S), index)
+    _need(dt, "dt", x.dtype, rows + (D,), index)
     if not isinstance(Bm, torch.Tensor) or Bm.dim() != len(rows) + 2:
         raise ValueError(f"Bm and Cm must be [{'B, T' if len(rows) == 2 else 'N'}, G, S]")
     G = Bm.shape[-2]
     if G < 1 or D % G != 0:
         raise ValueError(f"the group count {G} must divide the channel count {D}")
-    _require(Bm, "Bm", x.dtype, rows + (G, S))
-    _require(Cm, "Cm", x.dtype, rows + (G, S))
-    _optional(skip, "skip", torch.float32, (D,))
-    _optional(z, "z", x.dtype, rows + (D,))
-    _optional(dt_bias, "dt_bias", torch.float32, (D,))
-    _optional(initial_state, "initial_state", torch.float32, (N, D, S))
-    _same_device(x, dt=dt, A=A, Bm=Bm, Cm=Cm, skip=skip, z=z, dt_bias=dt_bias, initial_state=initial_state)
+    _need(Bm, "Bm", x.dtype, rows + (G, S), index)
+    _need(Cm, "Cm", x.dtype, rows + (G, S), index)
+    _may(skip, "skip", torch.float32, (D,), index)
+    _may(z, "z", x.dtype, rows + (D,), index)
+    _may(dt_bias, "dt_bias", torch.float32, (D,), index)
+    _may(initial_state, "initial_state", torch.float32, (N, D, S), index)
     return D, S, G
 
 
@@ -694,24 +709,24 @@ def selective_scan(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, Bm: torch
     """Selective state space scan through ``comba_selective_scan_fwd``: x, dt, z [B, T, D], A [D, S],
     Bm, Cm [B, T, G, S], skip and dt_bias [D]. Returns (y, final_state), the state [N, D, S] in
     float32."""
-    _activation(x, "x", 3)
+    index = _activation(x, "x", 3)
     B, T, _ = x.shape
-    N = _sequences(B, T, cu_seqlens)
-    D, S, G = _scan_args(x, dt, A, Bm, Cm, skip, z, dt_bias, initial_state, N)
+    N = _sequences(B, T, cu_seqlens, index)
+    D, S, G = _scan_args(x, dt, A, Bm, Cm, skip, z, dt_bias, initial_state, N, index)
     if out is None:
         out = torch.empty_like(x)
-    _require(out, "out", x.dtype, (B, T, D))
-    if final_state is None and output_final_state:
+    else:
+        _need(out, "out", x.dtype, (B, T, D), index)
+    if final_state is not None or not output_final_state:
+        _may(final_state, "final_state", torch.float32, (N, D, S), index)
+    else:
         final_state = torch.empty((N, D, S), dtype=torch.float32, device=x.device)
-    _optional(final_state, "final_state", torch.float32, (N, D, S))
-    _same_device(x, cu_seqlens=cu_seqlens, out=out, final_state=final_state)
     nseq = N if cu_seqlens is not None else 0
     workspace = _workspace(workspace, selective_scan_workspace_size(B, T, D, S, G, nseq), x.device)
-    with torch.cuda.device(x.device):
-        _check(lib().comba_selective_scan_fwd(
-            _at(x), _at(dt), _at(A), _at(Bm), _at(Cm), _at(skip), _at(z), _at(dt_bias), int(bool(softplus)),
-            _at(initial_state), _at(cu_seqlens), nseq, B, T, D, S, G, _DT[x.dtype], _at(out), _at(final_state),
-            *_ws(workspace), _stream(x.device)))
+    _run(lib().comba_selective_scan_fwd, index,
+         _at(x), _at(dt), _at(A), _at(Bm), _at(Cm), _at(skip), _at(z), _at(dt_bias), int(bool(softplus)),
+         _at(initial_state), _at(cu_seqlens), nseq, B, T, D, S, G, _DT[x.dtype], _at(out), _at(final_state),
+         *_ws(workspace))
     return out, final_state
 
 
@@ -723,19 +738,18 @@ def selective_step(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, Bm: torch
                    final_state: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """One token per sequence through ``comba_selective_step``: x, dt, z [N, D], Bm, Cm [N, G, S]. With
     ``in_place`` the state is updated in ``initial_state`` itself. Returns (y, final_state)."""
-    _activation(x, "x", 2)
+    index = _activation(x, "x", 2)
     N = x.shape[0]
-    D, S, G = _scan_args(x, dt, A, Bm, Cm, skip, z, dt_bias, initial_state, N)
+    D, S, G = _scan_args(x, dt, A, Bm, Cm, skip, z, dt_bias, initial_state, N, index)
     if out is None:
         out = torch.empty_like(x)
-    _require(out, "out", x.dtype, (N, D))
+    else:
+        _need(out, "out", x.dtype, (N, D), index)
     final_state = _step_state(initial_state, final_state, in_place, output_final_state, (N, D, S), torch.float32,
-                              x.device)
-    _same_device(x, out=out, final_state=final_state)
-    with torch.cuda.device(x.device):
-        _check(lib().comba_selective_step(
-            _at(x), _at(dt), _at(A), _at(Bm), _at(Cm), _at(skip), _at(z), _at(dt_bias), int(bool(softplus)),
-            _at(initial_state), N, D, S, G, _DT[x.dtype], _at(out), _at(final_state), _stream(x.device)))
+                              x.device, index)
+    _run(lib().comba_selective_step, index,
+         _at(x), _at(dt), _at(A), _at(Bm), _at(Cm), _at(skip), _at(z), _at(dt_bias), int(bool(softplus)),
+         _at(initial_state), N, D, S, G, _DT[x.dtype], _at(out), _at(final_state))
     return out, final_state
 
 
@@ -748,13 +762,12 @@ def selective_scan_bwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, Bm: t
     """Gradients of ``selective_scan`` through ``comba_selective_scan_bwd``, from its inputs alone.
     Returns dx, ddt, dz, dB and dC in x's type, dA, dskip, ddt_bias and dinitial_state in float32;
     the gradient of an input that was not given is None."""
-    _activation(x, "x", 3)
+    index = _activation(x, "x", 3)
     B, T, _ = x.shape
-    N = _sequences(B, T, cu_seqlens)
-    D, S, G = _scan_args(x, dt, A, Bm, Cm, skip, z, dt_bias, initial_state, N)
-    _require(dy, "dy", x.dtype, (B, T, D))
-    _optional(d_final_state, "d_final_state", torch.float32, (N, D, S))
-    _same_device(x, dy=dy, cu_seqlens=cu_seqlens, d_final_state=d_final_state)
+    N = _sequences(B, T, cu_seqlens, index)
+    D, S, G = _scan_args(x, dt, A, Bm, Cm, skip, z, dt_bias, initial_state, N, index)
+    _need(dy, "dy", x.dtype, (B, T, D), index)
+    _may(d_final_state, "d_final_state", torch.float32, (N, D, S), index)
     nseq = N if cu_seqlens is not None else 0
     L = lib()
 
@@ -763,12 +776,11 @@ def selective_scan_bwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, Bm: t
     g = dict(dx=like(x), ddt=like(dt), dA=like(A), dB=like(Bm), dC=like(Cm), dskip=like(skip), dz=like(z),
              ddt_bias=like(dt_bias), dinitial_state=like(initial_state))
     workspace = _workspace(workspace, int(L.comba_selective_scan_bwd_workspace_size(B, T, D, S, G, nseq)), x.device)
-    with torch.cuda.device(x.device):
-        _check(L.comba_selective_scan_bwd(
-            _at(x), _at(dt), _at(A), _at(Bm), _at(Cm), _at(skip), _at(z), _at(dt_bias), int(bool(softplus)),
-            _at(initial_state), _at(cu_seqlens), nseq, B, T, D, S, G, _DT[x.dtype], _at(dy), _at(d_final_state),
-            _at(g["dx"]), _at(g["ddt"]), _at(g["dA"]), _at(g["dB"]), _at(g["dC"]), _at(g["dskip"]),
-            _at(g["dz"]), _at(g["ddt_bias"]), _at(g["dinitial_state"]), *_ws(workspace), _stream(x.device)))
+    _run(L.comba_selective_scan_bwd, index,
+         _at(x), _at(dt), _at(A), _at(Bm), _at(Cm), _at(skip), _at(z), _at(dt_bias), int(bool(softplus)),
+         _at(initial_state), _at(cu_seqlens), nseq, B, T, D, S, G, _DT[x.dtype], _at(dy), _at(d_final_state),
+         _at(g["dx"]), _at(g["ddt"]), _at(g["dA"]), _at(g["dB"]), _at(g["dC"]), _at(g["dskip"]),
+         _at(g["dz"]), _at(g["ddt_bias"]), _at(g["dinitial_state"]), *_ws(workspace))
     return g
 
 
@@ -779,13 +791,13 @@ def _norm_args(y, gate, residual, scale, post_weight, pre_weight):
     if y.dim() < 1 or y.shape[-1] < 1:
         raise ValueError("y must be [..., D]")
     D = y.shape[-1]
-    _optional(gate, "gate", y.dtype, y.shape)
-    _optional(residual, "residual", y.dtype, y.shape)
-    _optional(scale, "scale", torch.float32, (D,))
-    _optional(post_weight, "post_weight", torch.float32, (D,))
-    _optional(pre_weight, "pre_weight", torch.float32, (D,))
-    _same_device(y, gate=gate, residual=residual, scale=scale, post_weight=post_weight, pre_weight=pre_weight)
-    return y.numel() // D, D
+    index = y.get_device()
+    _may(gate, "gate", y.dtype, y.shape, index)
+    _may(residual, "residual", y.dtype, y.shape, index)
+    _may(scale, "scale", torch.float32, (D,), index)
+    _may(post_weight, "post_weight", torch.float32, (D,), index)
+    _may(pre_weight, "pre_weight", torch.float32, (D,), index)
+    return y.numel() // D, D, index
 
 
 def block_norm(y: torch.Tensor, gate: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
@@ -796,21 +808,21 @@ def block_norm(y: torch.Tensor, gate: Optional[torch.Tensor] = None, residual: O
     ``comba_block_norm_fwd``. y, gate, residual [..., D]; scale and weights [D] in float32; every part
     but y is optional. Returns (r, n): r = residual + scale * (norm(y) post_weight silu(gate)), and
     n = norm(r) pre_weight (None without pre_weight)."""
-    rows, D = _norm_args(y, gate, residual, scale, post_weight, pre_weight)
+    rows, D, index = _norm_args(y, gate, residual, scale, post_weight, pre_weight)
     if out is None:
         out = torch.empty_like(y)
-    _require(out, "out", y.dtype, y.shape)
+    else:
+        _need(out, "out", y.dtype, y.shape, index)
     if pre_weight is None:
         if out_norm is not None:
             raise ValueError("out_norm goes with pre_weight")
     elif out_norm is None:
         out_norm = torch.empty_like(y)
-    _optional(out_norm, "out_norm", y.dtype, y.shape)
-    _same_device(y, out=out, out_norm=out_norm)
-    with torch.cuda.device(y.device):
-        _check(lib().comba_block_norm_fwd(
-            _at(y), _at(gate), _at(residual), _at(scale), _at(post_weight), _at(pre_weight), rows, D, float(eps),
-            _DT[y.dtype], _at(out), _at(out_norm), _stream(y.device)))
+    else:
+        _need(out_norm, "out_norm", y.dtype, y.shape, index)
+    _run(lib().comba_block_norm_fwd, index,
+         _at(y), _at(gate), _at(residual), _at(scale), _at(post_weight), _at(pre_weight), rows, D, float(eps),
+         _DT[y.dtype], _at(out), _at(out_norm))
     return out, out_norm
 
 
@@ -822,10 +834,9 @@ def block_norm_bwd(y: torch.Tensor, dr: Optional[torch.Tensor] = None, dn: Optio
     """Gradients of ``block_norm`` through ``comba_block_norm_bwd``, from its inputs alone, for
     dr = dL/dr and dn = dL/dn (one of them may be None). Returns dy, dgate and dresidual in y's type,
     dscale, dpost_weight and dpre_weight in float32; the gradient of a part that was not given is None."""
-    rows, D = _norm_args(y, gate, residual, scale, post_weight, pre_weight)
-    _optional(dr, "dr", y.dtype, y.shape)
-    _optional(dn, "dn", y.dtype, y.shape)
-    _same_device(y, dr=dr, dn=dn)
+    rows, D, index = _norm_args(y, gate, residual, scale, post_weight, pre_weight)
+    _may(dr, "dr", y.dtype, y.shape, index)
+    _may(dn, "dn", y.dtype, y.shape, index)
     L = lib()
 
     def like(t):
@@ -833,11 +844,10 @@ def block_norm_bwd(y: torch.Tensor, dr: Optional[torch.Tensor] = None, dn: Optio
     g = dict(dy=like(y), dgate=like(gate), dresidual=like(residual), dscale=like(scale),
              dpost_weight=like(post_weight), dpre_weight=like(pre_weight))
     workspace = _workspace(workspace, int(L.comba_block_norm_bwd_workspace_size(rows, D)), y.device)
-    with torch.cuda.device(y.device):
-        _check(L.comba_block_norm_bwd(
-            _at(y), _at(gate), _at(residual), _at(scale), _at(post_weight), _at(pre_weight), rows, D, float(eps),
-            _DT[y.dtype], _at(dr), _at(dn), _at(g["dy"]), _at(g["dgate"]), _at(g["dresidual"]),
-            _at(g["dscale"]), _at(g["dpost_weight"]), _at(g["dpre_weight"]), *_ws(workspace), _stream(y.device)))
+    _run(L.comba_block_norm_bwd, index,
+         _at(y), _at(gate), _at(residual), _at(scale), _at(post_weight), _at(pre_weight), rows, D, float(eps),
+         _DT[y.dtype], _at(dr), _at(dn), _at(g["dy"]), _at(g["dgate"]), _at(g["dresidual"]),
+         _at(g["dscale"]), _at(g["dpost_weight"]), _at(g["dpre_weight"]), *_ws(workspace))
     return g
 
 
