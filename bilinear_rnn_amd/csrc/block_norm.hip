@@ -7,10 +7,10 @@
 // n is formed from the float32 r, before r is rounded.
 //
 // Bound by HBM: every input is read once and every output written once, with the row in registers
-// between the reductions. A row is spread over LPR lanes in pieces of 8 elements (piece j of lane l:
-// columns 8 (j LPR + l)), a part of a wavefront up to 512 columns (several rows per wavefront,
-// reductions without LDS), a workgroup above 1024. Workgroups walk over many rows with the
-// parameters in registers.
+// between the reductions. A row is spread over LPR lanes, 8 NV elements each: a part of a wavefront
+// up to 512 columns (several rows per wavefront, reductions without LDS), a workgroup above 1024.
+// Workgroups walk over many rows with the parameters in registers, and load the next row before they
+// work on the present one. Parts that are not given read 0 from an empty range, without a branch.
 #include "column_sums.h"
 #include "comba.h"
 #include "launch.h"
@@ -22,7 +22,7 @@ namespace comba {
 constexpr int kNormThreads = 256;
 
 // Sum over the LPR lanes that share a row, in every one of them. `red`: LDS of one float per
-// wavefront and value; the caller alternates between two such arrays, so that one barrier per
+// wavefront of the workgroup and value; the caller alternates between two such arrays, so that one barrier per
 // reduction is enough.
 template <int LPR, int K>
 __device__ __forceinline__ void row_sums(float (&v)[K], float* red) {
@@ -33,13 +33,20 @@ __device__ __forceinline__ void row_sums(float (&v)[K], float* red) {
     x += dpp_flip<1>(x);
     x += dpp_flip<2>(x);
     if constexpr (LPR >= 16) x += dpp_flip<3>(x);
-    if constexpr (LPR >= 32) x += __shfl_xor(x, 16, kWave);
-    if constexpr (LPR >= 64) x += __shfl_xor(x, 32, kWave);
+    if constexpr (LPR >= 32) {  // both halves of the pair of rows, then of the wavefront
+      const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+      x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
+    if constexpr (LPR >= 64) {
+      const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+      x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
     v[k] = x;
   }
   if constexpr (LPR > 64) {
     constexpr int NW = LPR / 64;
-    const int w = threadIdx.x / kWave;
+    const int w = threadIdx.x % LPR / kWave;
+    red += threadIdx.x / LPR * (K * NW);
     if ((threadIdx.x & (kWave - 1)) == 0)
 #pragma unroll
       for (int k = 0; k < K; ++k) red[k * NW + w] = v[k];
@@ -60,23 +67,59 @@ struct NormShape {
   float eps, inv;  // inv = 1 / D
 };
 
-// 8 elements of column c of a row, with the pieces behind the row's end reading 0.
-template <typename T, bool V>
-__device__ __forceinline__ void load8(const T* row, int c, int D, float (&x)[8]) {
-  if (c < D) {
-    Pack<T, 8, V>::load(row + c, x, D - c);
-  } else {
+// A lane's 8 elements number j of a row. V: columns 8 (j LPR + l) + i, one or two 16-byte pieces;
+// otherwise (8 j + i) LPR + l, so that a load instruction still reads neighbouring elements.
+template <typename T, bool V, int LPR> struct Eight {
+  static __device__ __forceinline__ int col(int l, int j, int i) { return V ? 8 * (j * LPR + l) + i : (8 * j + i) * LPR + l; }
+  uint32_t raw[V && sizeof(T) == 2 ? 4 : 8];
+  // `at`: byte offset of the row in the range. Columns behind the row's end are read as 0.
+  __device__ __forceinline__ void load(const Range<T>& m, uint32_t at, int l, int j, int D) {
+    if constexpr (V) {
+      const uint32_t o = col(l, j, 0) < D ? at + col(l, j, 0) * sizeof(T) : kNowhere;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = 0.f;
+      for (int k = 0; k < sizeof(raw) / 16; ++k) {
+        const u32x4 v = m.load16(o + 16 * k);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) raw[4 * k + i] = v[i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) raw[i] = m.load(col(l, j, i) < D ? at + col(l, j, i) * sizeof(T) : kNowhere);
+    }
   }
-}
-template <typename T, bool V>
-__device__ __forceinline__ void store8(T* row, int c, int D, const float (&x)[8]) {
-  if (c < D) Pack<T, 8, V>::store(row + c, x, D - c);
-}
-__device__ __forceinline__ void load_param(const float* p, int c, int D, float (&x)[8]) {
+  __device__ __forceinline__ float operator[](int i) const {
+    if constexpr (V && sizeof(T) == 2) return __uint_as_float(i & 1 ? raw[i / 2] & 0xffff0000u : raw[i / 2] << 16);
+    else return Range<T>::value(raw[i]);
+  }
+  static __device__ __forceinline__ void store(const Range<T>& m, uint32_t at, int l, int j, int D, const float (&x)[8]) {
+    if constexpr (V) {
+      const uint32_t o = col(l, j, 0) < D ? at + col(l, j, 0) * sizeof(T) : kNowhere;
+      if constexpr (sizeof(T) == 2) {
+        bf16x8 v;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = p && c + i < D ? p[c + i] : 0.f;
+        for (int i = 0; i < 8; ++i) v[i] = to_bf16(x[i]);
+        m.store16(o, __builtin_bit_cast(u32x4, v));
+      } else {
+        m.store16(o, __builtin_bit_cast(u32x4, f32x4{x[0], x[1], x[2], x[3]}));
+        m.store16(o + 16, __builtin_bit_cast(u32x4, f32x4{x[4], x[5], x[6], x[7]}));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m.store(col(l, j, i) < D ? at + col(l, j, i) * sizeof(T) : kNowhere, x[i]);
+    }
+  }
+  static __device__ __forceinline__ void params(const float* p, int l, int j, int D, float none, float (&x)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = !p ? none : col(l, j, i) < D ? p[col(l, j, i)] : 0.f;
+  }
+};
+
+// The rows of a workgroup's step as a range: RPB rows from `first` on, those behind the tensor's end
+// missing; empty if the tensor is not given.
+template <typename T, int RPB>
+__device__ __forceinline__ Range<T> step_range(const T* base, int64_t first, const NormShape& s) {
+  const int64_t left = s.rows - first, n = left < 0 ? 0 : (left < RPB ? left : RPB);
+  return Range<T>(base + (base && n > 0 ? first * s.D : 0), base ? n * s.D * static_cast<int64_t>(sizeof(T)) : 0);
 }
 
 template <typename T, bool V, int LPR, int NV>
@@ -85,53 +128,69 @@ __global__ __launch_bounds__(LPR > kNormThreads ? LPR : kNormThreads) void norm_
     const float* __restrict__ scale, const float* __restrict__ post, const float* __restrict__ pre, NormShape s,
     T* __restrict__ r_out, T* __restrict__ n_out) {
   constexpr int TH = LPR > kNormThreads ? LPR : kNormThreads, RPB = TH / LPR;
-  __shared__ float red[2][LPR > 64 ? LPR / 64 : 1];
+  constexpr bool PF = TH <= 512 && NV == 1;  // else there are no registers for a second row
+  using E = Eight<T, V, LPR>;
+  __shared__ float red[2][TH / 64];
   const int l = threadIdx.x % LPR, D = s.D;
+  const uint32_t at = static_cast<uint32_t>(threadIdx.x / LPR) * D * sizeof(T);
   float wpost[NV][8], wpre[NV][8], sc[NV][8];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int c = 8 * (j * LPR + l);
-    load_param(post, c, D, wpost[j]);
-    load_param(pre, c, D, wpre[j]);
-    load_param(scale, c, D, sc[j]);
+    E::params(post, l, j, D, 1.f, wpost[j]);
+    E::params(pre, l, j, D, 1.f, wpre[j]);
+    E::params(scale, l, j, D, 1.f, sc[j]);
   }
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * RPB + threadIdx.x / LPR;
-       row - threadIdx.x / LPR < s.rows; row += static_cast<int64_t>(gridDim.x) * RPB) {
-    const bool live = row < s.rows;  // rows of one workgroup share its barriers
-    const int64_t at = (live ? row : s.rows - 1) * D;
-    float u[NV][8], g[NV][8], r[NV][8];
+  E yn[NV], gn[NV], rn[NV];
+  auto fetch = [&](int64_t first) {
+    const Range<T> ym = step_range<T, RPB>(y, first, s), gm = step_range<T, RPB>(gate, first, s),
+                   rm = step_range<T, RPB>(residual, first, s);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = 8 * (j * LPR + l);
-      load8<T, V>(y + at, c, D, u[j]);
-      if (gate) load8<T, V>(gate + at, c, D, g[j]);
-      if (residual) load8<T, V>(residual + at, c, D, r[j]);
+      yn[j].load(ym, at, l, j, D);
+      gn[j].load(gm, at, l, j, D);
+      rn[j].load(rm, at, l, j, D);
     }
+  };
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * RPB;
+  int64_t first = static_cast<int64_t>(blockIdx.x) * RPB;
+  if (PF) fetch(first);
+  for (; first < s.rows; first += stride) {
+    if (!PF) fetch(first);
+    E yc[NV], gc[NV], rc[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      yc[j] = yn[j];
+      gc[j] = gn[j];
+      rc[j] = rn[j];
+    }
+    if (PF) fetch(first + stride);
+    float k1 = 1.f;
     if (post) {
       float ss[1] = {0.f};
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss[0] = fmaf(u[j][i], u[j][i], ss[0]);
+        for (int i = 0; i < 8; ++i) ss[0] = fmaf(yc[j][i], yc[j][i], ss[0]);
       row_sums<LPR, 1>(ss, red[0]);
-      const float k1 = 1.f / sqrtf(fmaf(ss[0], s.inv, s.eps));
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) u[j][i] *= k1 * wpost[j][i];
+      k1 = 1.f / sqrtf(fmaf(ss[0], s.inv, s.eps));
     }
+    float u[NV][8];
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float v = u[j][i];
-        if (gate) v *= g[j][i] * sigmoid_fast(g[j][i]);
-        if (scale) v *= sc[j][i];
-        u[j][i] = residual ? v + r[j][i] : v;
-      }
-    if (live)
+      for (int i = 0; i < 8; ++i) u[j][i] = yc[j][i] * (k1 * wpost[j][i]);
+    if (gate)
 #pragma unroll
-      for (int j = 0; j < NV; ++j) store8<T, V>(r_out + at, 8 * (j * LPR + l), D, u[j]);
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[j][i] *= gc[j][i] * sigmoid_fast(gc[j][i]);
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) u[j][i] = residual ? fmaf(u[j][i], sc[j][i], rc[j][i]) : u[j][i] * sc[j][i];
+    const Range<T> ro = step_range<T, RPB>(r_out, first, s);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) E::store(ro, at, l, j, D, u[j]);
     if (pre) {
       float ss[1] = {0.f};
 #pragma unroll
@@ -140,11 +199,12 @@ __global__ __launch_bounds__(LPR > kNormThreads ? LPR : kNormThreads) void norm_
         for (int i = 0; i < 8; ++i) ss[0] = fmaf(u[j][i], u[j][i], ss[0]);
       row_sums<LPR, 1>(ss, red[1]);
       const float k2 = 1.f / sqrtf(fmaf(ss[0], s.inv, s.eps));
+      const Range<T> no = step_range<T, RPB>(n_out, first, s);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) u[j][i] *= k2 * wpre[j][i];
-        if (live) store8<T, V>(n_out + at, 8 * (j * LPR + l), D, u[j]);
+        E::store(no, at, l, j, D, u[j]);
       }
     }
     if constexpr (LPR > 64) {
@@ -167,62 +227,83 @@ __global__ __launch_bounds__(LPR > kNormThreads ? LPR : kNormThreads) void norm_
     const float* __restrict__ scale, const float* __restrict__ post, const float* __restrict__ pre,
     const T* __restrict__ dr, const T* __restrict__ dn, NormShape s, T* __restrict__ dy, T* __restrict__ dgate,
     T* __restrict__ dres, float* __restrict__ part) {
-  constexpr int TH = LPR > kNormThreads ? LPR : kNormThreads, RPB = TH / LPR, NW = LPR > 64 ? LPR / 64 : 1;
-  __shared__ float red[3][2 * NW];
+  constexpr int TH = LPR > kNormThreads ? LPR : kNormThreads, RPB = TH / LPR;
+  constexpr bool PF = TH <= 512 && NV == 1;  // else there are no registers for a second row
+  using E = Eight<T, V, LPR>;
+  __shared__ float red[3][2 * (TH / 64)];
   __shared__ float cols[RPB > 1 ? RPB : 1][RPB > 1 ? LPR * 8 : 1];
   const int l = threadIdx.x % LPR, D = s.D;
+  const uint32_t at = static_cast<uint32_t>(threadIdx.x / LPR) * D * sizeof(T);
   float wpost[NV][8], wpre[NV][8], sc[NV][8], a_post[NV][8], a_pre[NV][8], a_sc[NV][8];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int c = 8 * (j * LPR + l);
-    load_param(post, c, D, wpost[j]);
-    load_param(pre, c, D, wpre[j]);
-    load_param(scale, c, D, sc[j]);
+    E::params(post, l, j, D, 1.f, wpost[j]);
+    E::params(pre, l, j, D, 1.f, wpre[j]);
+    E::params(scale, l, j, D, 1.f, sc[j]);
 #pragma unroll
     for (int i = 0; i < 8; ++i) a_post[j][i] = a_pre[j][i] = a_sc[j][i] = 0.f;
   }
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * RPB + threadIdx.x / LPR;
-       row - threadIdx.x / LPR < s.rows; row += static_cast<int64_t>(gridDim.x) * RPB) {
-    const bool live = row < s.rows;
-    const int64_t at = (live ? row : s.rows - 1) * D;
-    float yv[NV][8], g[NV][8], r[NV][8], d[NV][8], e[NV][8];
+  E yn[NV], gn[NV], rn[NV], dn_[NV], en[NV];
+  const T* res = dn ? residual : nullptr;  // the residual is needed for r alone
+  auto fetch = [&](int64_t first) {
+    const Range<T> ym = step_range<T, RPB>(y, first, s), gm = step_range<T, RPB>(gate, first, s),
+                   rm = step_range<T, RPB>(res, first, s), dm = step_range<T, RPB>(dr, first, s),
+                   em = step_range<T, RPB>(dn, first, s);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = 8 * (j * LPR + l);
-      load8<T, V>(y + at, c, D, yv[j]);
-      if (gate) load8<T, V>(gate + at, c, D, g[j]);
-      if (residual && dn) load8<T, V>(residual + at, c, D, r[j]);
-      if (dr) load8<T, V>(dr + at, c, D, d[j]);
-      if (dn) load8<T, V>(dn + at, c, D, e[j]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (!dr) d[j][i] = 0.f;
+      yn[j].load(ym, at, l, j, D);
+      gn[j].load(gm, at, l, j, D);
+      rn[j].load(rm, at, l, j, D);
+      en[j].load(em, at, l, j, D);
+      dn_[j].load(dm, at, l, j, D);
     }
+  };
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * RPB;
+  int64_t first = static_cast<int64_t>(blockIdx.x) * RPB;
+  if (PF) fetch(first);
+  for (; first < s.rows; first += stride) {
+    if (!PF) fetch(first);
+    const bool live = first + threadIdx.x / LPR < s.rows;
+    E yc[NV], gc[NV], rc[NV], dc[NV], ec[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      yc[j] = yn[j];
+      gc[j] = gn[j];
+      rc[j] = rn[j];
+      dc[j] = dn_[j];
+      ec[j] = en[j];
+    }
+    if (PF) fetch(first + stride);
     float k1 = 1.f;
     if (post) {
       float ss[1] = {0.f};
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss[0] = fmaf(yv[j][i], yv[j][i], ss[0]);
+        for (int i = 0; i < 8; ++i) ss[0] = fmaf(yc[j][i], yc[j][i], ss[0]);
       row_sums<LPR, 1>(ss, red[0]);
       k1 = 1.f / sqrtf(fmaf(ss[0], s.inv, s.eps));
     }
-    // h: the value before the gate; u = h (gate sigmoid(gate))
-    auto value = [&](int j, int i) { return post ? yv[j][i] * k1 * wpost[j][i] : yv[j][i]; };
+    float d[NV][8], sg[NV][8];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        d[j][i] = dc[j][i];
+        sg[j][i] = gate ? sigmoid_fast(gc[j][i]) : 1.f;
+      }
+    // h: the value before the gate, gs: the gate's factor
+    auto h = [&](int j, int i) { return yc[j][i] * (k1 * wpost[j][i]); };
+    auto gs = [&](int j, int i) { return gate ? gc[j][i] * sg[j][i] : 1.f; };
     if (dn) {
-      float ss[2] = {0.f, 0.f};
+      float ss[2] = {0.f, 0.f}, r[NV][8];
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          float v = value(j, i);
-          if (gate) v *= g[j][i] * sigmoid_fast(g[j][i]);
-          if (scale) v *= sc[j][i];
-          if (residual) v += r[j][i];
-          r[j][i] = v;
-          ss[0] = fmaf(v, v, ss[0]);
-          ss[1] = fmaf(e[j][i] * wpre[j][i], v, ss[1]);
+          r[j][i] = fmaf(h(j, i) * gs(j, i), sc[j][i], rc[j][i]);
+          ss[0] = fmaf(r[j][i], r[j][i], ss[0]);
+          ss[1] = fmaf(ec[j][i] * wpre[j][i], r[j][i], ss[1]);
         }
       row_sums<LPR, 2>(ss, red[1]);
       const float k2 = 1.f / sqrtf(fmaf(ss[0], s.inv, s.eps)), m = ss[1] * s.inv * k2 * k2;
@@ -230,51 +311,56 @@ __global__ __launch_bounds__(LPR > kNormThreads ? LPR : kNormThreads) void norm_
       for (int j = 0; j < NV; ++j)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          if (live) a_pre[j][i] = fmaf(e[j][i], r[j][i] * k2, a_pre[j][i]);
-          d[j][i] += k2 * (e[j][i] * wpre[j][i] - r[j][i] * m);
+          if (live) a_pre[j][i] = fmaf(ec[j][i], r[j][i] * k2, a_pre[j][i]);
+          d[j][i] += k2 * (ec[j][i] * wpre[j][i] - r[j][i] * m);
         }
     }
-    float ss[1] = {0.f};
+    if (dres) {
+      const Range<T> o = step_range<T, RPB>(dres, first, s);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = 8 * (j * LPR + l);
-      if (dres && live) store8<T, V>(dres + at, c, D, d[j]);
-      float dg[8];
+      for (int j = 0; j < NV; ++j) E::store(o, at, l, j, D, d[j]);
+    }
+    if (scale)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float h = value(j, i);
-        float sg = 1.f, gs = 1.f;
-        if (gate) {
-          sg = sigmoid_fast(g[j][i]);
-          gs = g[j][i] * sg;
-        }
-        if (scale) {
-          if (live) a_sc[j][i] = fmaf(h * gs, d[j][i], a_sc[j][i]);
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (live) a_sc[j][i] = fmaf(h(j, i) * gs(j, i), d[j][i], a_sc[j][i]);
           d[j][i] *= sc[j][i];
         }
-        if (gate) {
-          dg[i] = d[j][i] * h * (sg * fmaf(g[j][i], 1.f - sg, 1.f));
-          d[j][i] *= gs;
+    if (gate) {
+      const Range<T> o = step_range<T, RPB>(dgate, first, s);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        float dg[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          dg[i] = d[j][i] * h(j, i) * (sg[j][i] * fmaf(gc[j][i], 1.f - sg[j][i], 1.f));
+          d[j][i] *= gs(j, i);
         }
-        if (post) {
-          if (live) a_post[j][i] = fmaf(d[j][i], yv[j][i] * k1, a_post[j][i]);
-          d[j][i] *= wpost[j][i];
-          ss[0] = fmaf(d[j][i], yv[j][i], ss[0]);
-        }
+        E::store(o, at, l, j, D, dg);
       }
-      if (dgate && live) store8<T, V>(dgate + at, c, D, dg);
     }
     if (post) {
+      float ss[1] = {0.f};
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (live) a_post[j][i] = fmaf(d[j][i], yc[j][i] * k1, a_post[j][i]);
+          d[j][i] *= wpost[j][i];
+          ss[0] = fmaf(d[j][i], yc[j][i], ss[0]);
+        }
       row_sums<LPR, 1>(ss, red[2]);
       const float m = ss[0] * s.inv * k1 * k1;
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) d[j][i] = k1 * (d[j][i] - yv[j][i] * m);
+        for (int i = 0; i < 8; ++i) d[j][i] = k1 * (d[j][i] - yc[j][i] * m);
     }
-    if (live)
+    const Range<T> o = step_range<T, RPB>(dy, first, s);
 #pragma unroll
-      for (int j = 0; j < NV; ++j) store8<T, V>(dy + at, 8 * (j * LPR + l), D, d[j]);
+    for (int j = 0; j < NV; ++j) E::store(o, at, l, j, D, d[j]);
     if constexpr (LPR > 64) {
       if (!post && dn) __syncthreads();  // the one reduction's array is free for the next row
     }
@@ -284,11 +370,10 @@ __global__ __launch_bounds__(LPR > kNormThreads ? LPR : kNormThreads) void norm_
   auto emit = [&](int which, float (&a)[NV][8]) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = 8 * (j * LPR + l);
       if constexpr (RPB > 1) {
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) cols[threadIdx.x / LPR][l * 8 + i] = a[j][i];
+        for (int i = 0; i < 8; ++i) cols[threadIdx.x / LPR][E::col(l, 0, i)] = a[j][i];
         __syncthreads();
         for (int k = threadIdx.x; k < LPR * 8; k += TH) {
           float t = 0.f;
@@ -299,7 +384,7 @@ __global__ __launch_bounds__(LPR > kNormThreads ? LPR : kNormThreads) void norm_
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (c + i < D) out[which * static_cast<int64_t>(D) + c + i] = a[j][i];
+          if (E::col(l, j, i) < D) out[which * static_cast<int64_t>(D) + E::col(l, j, i)] = a[j][i];
       }
     }
   };
@@ -321,9 +406,9 @@ static hipError_t with_tile(int D, F f) {
   if (D <= 128) return f(NormTile<16, 1>{});
   if (D <= 256) return f(NormTile<32, 1>{});
   if (D <= 512) return f(NormTile<64, 1>{});
-  if (D <= 1024) return f(NormTile<64, 2>{});
+  if (D <= 1024) return f(NormTile<128, 1>{});
   if (D <= 2048) return f(NormTile<256, 1>{});
-  if (D <= 4096) return f(NormTile<256, 2>{});
+  if (D <= 4096) return f(NormTile<512, 1>{});
   if (D <= 8192) return f(NormTile<512, 2>{});
   return f(NormTile<1024, 2>{});
 }
@@ -339,7 +424,7 @@ template <typename T, bool V>
 static hipError_t norm_fwd_t(const NormArgs& a, hipStream_t st) {
   return with_tile(a.D, [&](auto tile) {
     constexpr int LPR = decltype(tile)::LPR, NV = decltype(tile)::NV, TH = LPR > kNormThreads ? LPR : kNormThreads;
-    const int64_t grid = norm_blocks(a.rows, TH / LPR, 256 * (2048 / TH));
+    const int64_t grid = norm_blocks(a.rows, TH / LPR, 256 * (1024 / TH));
     const NormShape s{a.rows, a.D, a.eps, 1.f / a.D};
     norm_fwd_kernel<T, V, LPR, NV><<<static_cast<unsigned>(grid), TH, 0, st>>>(
         static_cast<const T*>(a.y), static_cast<const T*>(a.gate), static_cast<const T*>(a.residual), a.scale,
@@ -356,8 +441,9 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t st) {
   return v ? norm_fwd_t<float, true>(a, st) : norm_fwd_t<float, false>(a, st);
 }
 
-// Four wavefronts per SIMD.
-constexpr int64_t kNormBwdThreads = 1 << 18;
+// Two wavefronts per SIMD: at 8192 rows of 2048, bf16, all parts, 64 us against 66 with three and 79 with
+// four (three are resident; more workgroups mean more partial sums and a second round).
+constexpr int64_t kNormBwdThreads = 1 << 17;
 
 template <typename Tile> static int64_t norm_bwd_grid(int64_t rows) {
   constexpr int TH = Tile::LPR > kNormThreads ? Tile::LPR : kNormThreads;
@@ -390,15 +476,18 @@ static hipError_t norm_bwd_t(const NormBwdArgs& a, hipStream_t st) {
     });
     if (e != hipSuccess) return e;
   }
-  float* to[3] = {a.dscale, a.dpost, a.dpre};
-  const bool have[3] = {true, true, a.dn != nullptr};
-  for (int k = 0; k < 3; ++k) {
-    if (!to[k]) continue;
-    const hipError_t e = launch_column_sums(a.part ? a.part + static_cast<int64_t>(k) * f.D : nullptr, have[k] ? grid : 0,
-                                            3 * static_cast<int64_t>(f.D), f.D, to[k], st);
-    if (e != hipSuccess) return e;
-  }
-  return hipSuccess;
+  // the parts that were summed; without dn the gradient of pre_weight is 0
+  float* sc = a.dscale;
+  float* post = a.dpost;
+  float* pre = a.dpre;
+  if (!sc && !post && !pre) return hipSuccess;
+  const int D = f.D;
+  const bool no_dn = a.dn == nullptr;
+  return column_sums(a.part, grid, 3 * static_cast<int64_t>(D), 3 * D, st, [=] __device__(int col, float v) {
+    const int k = col / D;
+    float* to = k == 0 ? sc : k == 1 ? post : pre;
+    if (to) to[col - k * D] = k == 2 && no_dn ? 0.f : v;
+  });
 }
 
 hipError_t launch_norm_bwd(const NormBwdArgs& a, hipStream_t st) {
@@ -408,10 +497,6 @@ hipError_t launch_norm_bwd(const NormBwdArgs& a, hipStream_t st) {
                  norm_aligned(a.dresidual);
   if (f.dtype == COMBA_BF16) return v ? norm_bwd_t<u16, true>(a, st) : norm_bwd_t<u16, false>(a, st);
   return v ? norm_bwd_t<float, true>(a, st) : norm_bwd_t<float, false>(a, st);
-}
-
-hipError_t launch_column_sums(const float* part, int64_t rows, int64_t stride, int cols, float* out, hipStream_t st) {
-  return column_sums(part, rows, stride, cols, st, [=] __device__(int c, float s) { out[c] = s; });
 }
 
 }  // namespace comba

@@ -33,15 +33,15 @@ struct ConvBwdArgs {
   float* dweight;             // [D, W]
   float* dbias;               // [D] or null
   void* dinit;                // [N, W-1, D] x's type, or null
-  float* part;                // workspace: [tiles, W + 1, D]
+  float* part;                // workspace: [sets of four tiles, W + 1, D]
 };
 
 hipError_t launch_conv(const ConvArgs& a, hipStream_t st);
 hipError_t launch_conv_step(const ConvArgs& a, hipStream_t st);
 hipError_t launch_conv_bwd(const ConvBwdArgs& a, hipStream_t st);
-// Token tiles of the forward with one channel per thread (its largest launch), and of the backward.
+// Token tiles of the forward, and sets of four tiles of the backward.
 int64_t conv_tiles(int64_t B, int64_t T, int64_t D, bool packed);
-int64_t conv_bwd_tiles(int64_t B, int64_t T, int64_t D, bool packed);
+int64_t conv_bwd_sets(int64_t B, int64_t T, int64_t D, bool packed);
 
 struct NormArgs {
   const void* y;              // [rows, D]
@@ -135,8 +135,5 @@ constexpr int kScanMaxStates = 64;
 hipError_t launch_scan(const ScanArgs& a, const ScanPlan& p, float* hseg, float* dsum, hipStream_t st);
 hipError_t launch_scan_step(const ScanArgs& a, hipStream_t st);
 hipError_t launch_scan_bwd(const ScanBwdArgs& a, const ScanPlan& p, hipStream_t st);
-
-// out[c] = sum over r < rows of part[r * stride + c], c < cols, in a fixed order.
-hipError_t launch_column_sums(const float* part, int64_t rows, int64_t stride, int cols, float* out, hipStream_t st);
 
 }  // namespace comba

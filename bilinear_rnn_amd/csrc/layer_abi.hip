@@ -60,9 +60,10 @@ int32_t check_conv(const void* x, const float* weight, int32_t D, int32_t W, int
   return COMBA_OK;
 }
 
-// One thread per channel of every tile and state, at the most.
+// Threads of the largest launch: one per four channels of every tile and state.
 int32_t check_conv_items(int64_t B, int64_t T, int64_t D, int64_t N, bool packed) {
-  if ((comba::conv_tiles(B, T, D, packed) + N) * D > INT_MAX)
+  const int64_t fwd = comba::conv_tiles(B, T, D, packed), bwd = 4 * comba::conv_bwd_sets(B, T, D, packed);
+  if (((fwd > bwd ? fwd : bwd) + N + 4) * ((D + 3) / 4 + 64) > INT_MAX)
     return report(COMBA_ERR_UNSUPPORTED, "too many (token tile, channel) pairs for one launch");
   return COMBA_OK;
 }
@@ -105,7 +106,7 @@ COMBA_API int32_t comba_short_conv_step(const void* x, const float* weight, cons
 
 COMBA_API size_t comba_short_conv_bwd_workspace_size(int32_t B, int32_t T, int32_t D, int32_t W, int32_t num_seqs) {
   if (B < 1 || T < 0 || D < 1 || W < 2 || W > 4 || D > kMaxWidth) return 0;
-  return up256(sizeof(float) * comba::conv_bwd_tiles(B, T, D, num_seqs > 0) * (W + 1) * static_cast<size_t>(D));
+  return up256(sizeof(float) * comba::conv_bwd_sets(B, T, D, num_seqs > 0) * (W + 1) * static_cast<size_t>(D));
 }
 
 COMBA_API int32_t comba_short_conv_bwd(const void* x, const float* weight, const float* bias,

@@ -6,59 +6,64 @@
 
 namespace comba {
 
-// E consecutive elements as float32. V: the 16-byte path (16-byte aligned address, all E
-// present); otherwise element by element, `n` of them (the rest 0).
-template <typename T, int E, bool V> struct Pack;
+// E consecutive elements as float32, at any address that is aligned to the element: the hardware
+// takes 8- and 16-byte accesses off their natural alignment. V: all E are there; otherwise `n` of
+// them (the rest 0).
+template <typename Q> struct __attribute__((packed, aligned(2))) Loose { Q v; };
 
-template <int E> struct Pack<u16, E, true> {
-  static_assert(E == 8, "16 bytes");
-  __device__ static void load(const u16* p, float (&x)[E], int) {
-    const uint4 t = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  }
-  __device__ static void store(u16* p, const float (&x)[E], int) {
-    bf16x8 v;
-#pragma unroll
-    for (int i = 0; i < E; ++i) v[i] = to_bf16(x[i]);
-    *reinterpret_cast<bf16x8*>(p) = v;
-  }
-};
-
-template <int E> struct Pack<float, E, true> {
-  static_assert(E % 4 == 0, "16-byte pieces");
-  __device__ static void load(const float* p, float (&x)[E], int) {
-#pragma unroll
-    for (int i = 0; i < E; i += 4) {
-      const f32x4 t = *reinterpret_cast<const f32x4*>(p + i);
-      x[i] = t[0]; x[i + 1] = t[1]; x[i + 2] = t[2]; x[i + 3] = t[3];
-    }
-  }
-  __device__ static void store(float* p, const float (&x)[E], int) {
-#pragma unroll
-    for (int i = 0; i < E; i += 4) *reinterpret_cast<f32x4*>(p + i) = f32x4{x[i], x[i + 1], x[i + 2], x[i + 3]};
-  }
-};
-
-template <typename T, int E> struct Pack<T, E, false> {
-  __device__ static void load(const T* p, float (&x)[E], int n) {
+template <typename T, int E, bool V> struct Pack {
+  static constexpr int W = E * sizeof(T) / 4;  // 32-bit words
+  typedef uint32_t Words __attribute__((ext_vector_type(W)));
+  static __device__ __forceinline__ Words fetch(const T* p, int n) {
+    if (V || n == E) return reinterpret_cast<const Loose<Words>*>(p)->v;
+    float x[E];
 #pragma unroll
     for (int i = 0; i < E; ++i) x[i] = i < n ? Elem<T>::load(p, i) : 0.f;
+    return words(x);
   }
-  __device__ static void store(T* p, const float (&x)[E], int n) {
+  static __device__ __forceinline__ void unpack(const Words& w, float (&x)[E]) {
 #pragma unroll
-    for (int i = 0; i < E; ++i)
-      if (i < n) Elem<T>::store(p, i, x[i]);
+    for (int i = 0; i < E; ++i) {
+      if constexpr (sizeof(T) == 2) x[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+      else x[i] = __uint_as_float(w[i]);
+    }
+  }
+  static __device__ __forceinline__ void load(const T* p, float (&x)[E], int n) { unpack(fetch(p, n), x); }
+  static __device__ __forceinline__ Words words(const float (&x)[E]) {
+    Words w;
+    if constexpr (sizeof(T) == 2) {
+      typedef __bf16 Half __attribute__((ext_vector_type(E)));
+      Half h;
+#pragma unroll
+      for (int i = 0; i < E; ++i) h[i] = to_bf16(x[i]);
+      w = __builtin_bit_cast(Words, h);
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i) w[i] = __float_as_uint(x[i]);
+    }
+    return w;
+  }
+  // STREAM: past the caches, for outputs that are written once and not read here.
+  template <bool STREAM = false>
+  static __device__ __forceinline__ void store(T* p, const float (&x)[E], int n) {
+    if (V || n == E) {
+      if constexpr (STREAM && W * 4 <= 16) {
+        __builtin_nontemporal_store(words(x), &reinterpret_cast<Loose<Words>*>(p)->v);
+      } else {
+        reinterpret_cast<Loose<Words>*>(p)->v = words(x);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i)
+        if (i < n) Elem<T>::store(p, i, x[i]);
+    }
   }
 };
 
 // A range of memory read and written through a buffer resource: loads past its end give 0, stores
 // past its end are dropped, so that the ends of a tensor need no branches. Offsets are 32-bit byte
 // offsets; kNowhere is past every end.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 constexpr uint32_t kNowhere = 0x80000000u;
 template <typename T> struct Range {
   __amdgpu_buffer_rsrc_t r;
@@ -69,6 +74,12 @@ template <typename T> struct Range {
   __device__ __forceinline__ uint32_t load(uint32_t off) const {
     if constexpr (sizeof(T) == 2) return __builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0);
     else return __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
+  }
+  __device__ __forceinline__ u32x4 load16(uint32_t off) const { return __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0); }
+  // Not kept in the caches on its way out (bit 1: nontemporal): a stream of outputs then leaves the
+  // lines of the inputs alone.
+  __device__ __forceinline__ void store16(uint32_t off, u32x4 v) const {
+    __builtin_amdgcn_raw_buffer_store_b128(v, r, off, 0, 2);
   }
   static __device__ __forceinline__ float value(uint32_t bits) { return __uint_as_float(sizeof(T) == 2 ? bits << 16 : bits); }
   __device__ __forceinline__ void store(uint32_t off, float x) const {

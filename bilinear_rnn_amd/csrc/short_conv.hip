@@ -3,10 +3,9 @@
 // where tokens before a sequence come from its state (its last W - 1 inputs) or are 0.
 //
 // A few operations per element: bound by HBM (one read of x, one write of y). A thread owns 16
-// bytes of channels (one channel where rows are not 16-byte aligned) and walks along a tile of
-// tokens with the last W - 1 inputs in registers, so that every input is loaded once per tile;
-// eight loads are in flight before the first is used. Sums and the SiLU are float32, the output
-// is rounded once.
+// bytes of channels and walks along a tile of tokens with the last W - 1 inputs in registers, so
+// that every input is loaded once per tile; eight loads are in flight before the first is used.
+// Sums and the SiLU are float32, the output is rounded once.
 #include "comba.h"
 #include "column_sums.h"
 #include "launch.h"
@@ -31,10 +30,6 @@ static int64_t tiles_of(int64_t B, int64_t T, bool packed, int TT) {
   return packed ? per : B * per;
 }
 
-// Whether 16-byte pieces of rows of D elements may be used, and elements per piece.
-static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-static int piece_of(int dtype) { return dtype == COMBA_BF16 ? 8 : 4; }
-
 struct ConvPos {  // one thread's place: a tile of tokens (or a sequence's state) and a channel group
   int tile, c, nc;
   bool done;
@@ -52,15 +47,16 @@ __device__ __forceinline__ ConvPos conv_pos(int D, int tiles) {
   return p;
 }
 
-template <int E, int W>
+template <int E, bool V, int W>
 __device__ __forceinline__ void load_weights(const float* weight, const float* bias, int c, int nc,
                                              float (&w)[W][E], float (&b)[E]) {
 #pragma unroll
   for (int e = 0; e < E; ++e) {
 #pragma unroll
-    for (int k = 0; k < W; ++k) w[k][e] = e < nc ? weight[static_cast<int64_t>(c + e) * W + k] : 0.f;
-    b[e] = bias && e < nc ? bias[c + e] : 0.f;
+    for (int k = 0; k < W; ++k) w[k][e] = V || e < nc ? weight[static_cast<int64_t>(c + e) * W + k] : 0.f;
   }
+#pragma unroll
+  for (int e = 0; e < E; ++e) b[e] = bias && (V || e < nc) ? bias[c + e] : 0.f;
 }
 
 // The W - 1 inputs before token t of a sequence [s, ...) into win[0 .. W-2], oldest first. `x` is
@@ -141,7 +137,7 @@ __global__ __launch_bounds__(kConvBlock) void conv_fwd_kernel(
   const int per = (Tn + TT - 1) / TT;
   const int b = p.tile / per, m0 = (p.tile - b * per) * TT, m1 = min(m0 + TT, Tn);
   float w[W][E], bs[E];
-  load_weights<E, W>(weight, bias, c, nc, w, bs);
+  load_weights<E, V, W>(weight, bias, c, nc, w, bs);
   const T* xr = x + static_cast<int64_t>(b) * Tn * D + c;
   T* yr = y + static_cast<int64_t>(b) * Tn * D + c;
   for_pieces(cu, N, Tn, b, m0, m1, [&](int n, int s, int e, int m, int mend) {
@@ -149,20 +145,19 @@ __global__ __launch_bounds__(kConvBlock) void conv_fwd_kernel(
     float win[W][E];
     load_history<T, E, V, W>(xr, st, D, s, m, nc, win);
     for (; m < mend; m += kConvAhead) {
-      float in[kConvAhead][E];
+      typename Pack<T, E, V>::Words in[kConvAhead];
 #pragma unroll
-      for (int u = 0; u < kConvAhead; ++u) Pack<T, E, V>::load(xr + min(m + u, mend - 1) * D, in[u], nc);
+      for (int u = 0; u < kConvAhead; ++u) in[u] = Pack<T, E, V>::fetch(xr + min(m + u, mend - 1) * D, nc);
 #pragma unroll
       for (int u = 0; u < kConvAhead; ++u) {
         if (m + u < mend) {
           float o[E];
-#pragma unroll
-          for (int i = 0; i < E; ++i) win[W - 1][i] = in[u][i];
+          Pack<T, E, V>::unpack(in[u], win[W - 1]);
           conv_dot<E, W>(win, w, bs, o);
           if (silu)
 #pragma unroll
             for (int i = 0; i < E; ++i) o[i] *= sigmoid_fast(o[i]);
-          Pack<T, E, V>::store(yr + (m + u) * D, o, nc);
+          Pack<T, E, V>::template store<true>(yr + (m + u) * D, o, nc);
           shift_window<E, W>(win);
         }
       }
@@ -189,7 +184,7 @@ __global__ __launch_bounds__(kConvBlock) void conv_step_kernel(
 #pragma unroll
       for (int i = 0; i < E; ++i) win[k][i] = 0.f;
   }
-  load_weights<E, W>(weight, bias, c, nc, w, bs);
+  load_weights<E, V, W>(weight, bias, c, nc, w, bs);
   conv_dot<E, W>(win, w, bs, o);
   if (silu)
 #pragma unroll
@@ -213,7 +208,7 @@ __device__ __forceinline__ void silu_grad(const float (&p)[E], float (&d)[E]) {
 // Backward: dp as above from the recomputed p; dx[t] = sum_k weight[k] dp[t + W - 1 - k] (tokens of
 // the same sequence), dweight[c, k] = sum_t dp[t] x[t - (W - 1) + k], dbias = sum_t dp. A thread
 // walks its tile and the W - 1 tokens after it, whose dp it recomputes for its own dx. Parameter
-// gradients: one float32 partial sum per tile, added up in a fixed order by a second kernel.
+// gradients: one float32 partial sum per four tiles, added up in a fixed order by a second kernel.
 // The last N items form the gradients of the initial states from the first W - 1 tokens.
 template <typename T, typename G, int E, bool V, int W>
 __global__ __launch_bounds__(kConvBlock) void conv_bwd_kernel(
@@ -221,13 +216,19 @@ __global__ __launch_bounds__(kConvBlock) void conv_bwd_kernel(
     const T* __restrict__ init, const int32_t* __restrict__ cu, int N, int Tn, int64_t D, int TT, int tiles, bool silu,
     const G* __restrict__ dy, const T* __restrict__ dfin, T* __restrict__ dx, T* __restrict__ dinit,
     float* __restrict__ part) {
-  const ConvPos pp = conv_pos<E>(static_cast<int>(D), tiles + (dinit ? N : 0));
-  if (pp.done) return;
-  const int c = pp.c, nc = pp.nc;
+  // a workgroup: four tiles (or states) of 64 channel groups; one partial sum per four tiles
+  __shared__ float sums[3][W + 1][E][kWave];
+  const int groups = static_cast<int>((D + E - 1) / E), gblocks = (groups + kWave - 1) / kWave;
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  const int four = blockIdx.x / gblocks, g = (blockIdx.x - four * gblocks) * kWave + lane;
+  const int sets = (tiles + 3) / 4, tile = four * 4 + wave;
+  const bool here = g < groups;
+  const int c = here ? g * E : 0, nc = here ? min(E, static_cast<int>(D) - c) : 0;
   float w[W][E], bs[E];
-  load_weights<E, W>(weight, bias, c, nc, w, bs);
-  if (pp.tile >= tiles) {
-    const int n = pp.tile - tiles;
+  if (here) load_weights<E, V, W>(weight, bias, c, nc, w, bs);
+  if (four >= sets) {
+    const int n = (four - sets) * 4 + wave;
+    if (!here || n >= N) return;
     int s = 0, e = Tn;
     if (cu) packed_range(cu, n, Tn, s, e);
     const int64_t row = cu ? 0 : static_cast<int64_t>(n) * Tn * D;
@@ -266,14 +267,14 @@ __global__ __launch_bounds__(kConvBlock) void conv_bwd_kernel(
     return;
   }
   const int per = (Tn + TT - 1) / TT;
-  const int b = pp.tile / per, m0 = (pp.tile - b * per) * TT, m1 = min(m0 + TT, Tn);
+  const int b = tile / per, m0 = (tile - b * per) * TT, m1 = min(m0 + TT, Tn);
   const int64_t row = static_cast<int64_t>(b) * Tn * D + c;
   float dw[W + 1][E];
 #pragma unroll
   for (int k = 0; k <= W; ++k)
 #pragma unroll
     for (int i = 0; i < E; ++i) dw[k][i] = 0.f;
-  for_pieces(cu, N, Tn, b, m0, m1, [&](int n, int s, int e, int m, int mend) {
+  if (here && tile < tiles) for_pieces(cu, N, Tn, b, m0, m1, [&](int n, int s, int e, int m, int mend) {
     const int64_t so = static_cast<int64_t>(n) * (W - 1) * D + c;
     float win[W][E], ring[W][E];  // ring: dp of the last W tokens
     load_history<T, E, V, W>(x + row, init ? init + so : nullptr, D, s, m, nc, win);
@@ -284,33 +285,35 @@ __global__ __launch_bounds__(kConvBlock) void conv_bwd_kernel(
     const int first = m, stop = mend + W - 1, have = min(stop, e);
     constexpr int U = 4;
     for (; m < stop; m += U) {
-      float in[U][E], d[U][E];
+      typename Pack<T, E, V>::Words in[U];
+      typename Pack<G, E, V>::Words din[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int t = min(m + u, have - 1);
-        Pack<T, E, V>::load(x + row + t * D, in[u], nc);
-        Pack<G, E, V>::load(dy + row + t * D, d[u], nc);
+        in[u] = Pack<T, E, V>::fetch(x + row + t * D, nc);
+        din[u] = Pack<G, E, V>::fetch(dy + row + t * D, nc);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int t = m + u;
         if (t < stop) {
-#pragma unroll
-          for (int i = 0; i < E; ++i) win[W - 1][i] = in[u][i];
+          float d[E];
+          Pack<T, E, V>::unpack(in[u], win[W - 1]);
+          Pack<G, E, V>::unpack(din[u], d);
           if (t >= have) {
 #pragma unroll
-            for (int i = 0; i < E; ++i) d[u][i] = 0.f;
+            for (int i = 0; i < E; ++i) d[i] = 0.f;
           } else if (silu) {
             float p[E];
             conv_dot<E, W>(win, w, bs, p);
-            silu_grad<E>(p, d[u]);
+            silu_grad<E>(p, d);
           }
           if (t < mend) {
 #pragma unroll
             for (int i = 0; i < E; ++i) {
 #pragma unroll
-              for (int k = 0; k < W; ++k) dw[k][i] = fmaf(d[u][i], win[k][i], dw[k][i]);
-              dw[W][i] += d[u][i];
+              for (int k = 0; k < W; ++k) dw[k][i] = fmaf(d[i], win[k][i], dw[k][i]);
+              dw[W][i] += d[i];
             }
           }
           shift_window<E, W>(win);
@@ -318,7 +321,7 @@ __global__ __launch_bounds__(kConvBlock) void conv_bwd_kernel(
           for (int i = 0; i < E; ++i) {
 #pragma unroll
             for (int k = 0; k < W - 1; ++k) ring[k][i] = ring[k + 1][i];
-            ring[W - 1][i] = d[u][i];
+            ring[W - 1][i] = d[i];
           }
           const int to = t - (W - 1);  // its dx is complete: ring[o] is dp[to + o]
           if (to >= first) {
@@ -336,17 +339,26 @@ __global__ __launch_bounds__(kConvBlock) void conv_bwd_kernel(
 #pragma unroll
               for (int i = 0; i < E; ++i) g[i] += f[i];
             }
-            Pack<T, E, V>::store(dx + row + to * D, g, nc);
+            Pack<T, E, V>::template store<true>(dx + row + to * D, g, nc);
           }
         }
       }
     }
   });
+  if (wave > 0)
 #pragma unroll
-  for (int k = 0; k <= W; ++k)
+    for (int k = 0; k <= W; ++k)
 #pragma unroll
-    for (int i = 0; i < E; ++i)
-      if (i < nc) part[(static_cast<int64_t>(pp.tile) * (W + 1) + k) * D + c + i] = dw[k][i];
+      for (int i = 0; i < E; ++i) sums[wave - 1][k][i][lane] = dw[k][i];
+  __syncthreads();
+  if (wave == 0 && here)
+#pragma unroll
+    for (int k = 0; k <= W; ++k)
+#pragma unroll
+      for (int i = 0; i < E; ++i)
+        if (i < nc)
+          part[(static_cast<int64_t>(four) * (W + 1) + k) * D + c + i] =
+              ((dw[k][i] + sums[0][k][i][lane]) + sums[1][k][i][lane]) + sums[2][k][i][lane];
 }
 
 // --- launches -----------------------------------------------------------------------------------
@@ -377,23 +389,35 @@ static hipError_t conv_step_t(const ConvArgs& a, hipStream_t st) {
 }
 
 int64_t conv_tiles(int64_t B, int64_t T, int64_t D, bool packed) {
-  return tiles_of(B, T, packed, conv_tile(B * T, D));
+  return tiles_of(B, T, packed, conv_tile(B * T, (D + 7) / 8));
 }
 
-// Tiles of the backward: by eight channels per thread whatever the alignment, so that the
-// workspace's size follows from the sizes alone.
-static int conv_bwd_tile(int64_t B, int64_t T, int64_t D) { return conv_tile(B * T, (D + 7) / 8); }
+constexpr int kConvBwdPiece = 4;  // channels per thread: with 8 a thread needs more than 200 registers
 
-int64_t conv_bwd_tiles(int64_t B, int64_t T, int64_t D, bool packed) {
+// Tokens per tile of the backward: 32 once that gives two wavefronts per SIMD.
+static int conv_bwd_tile(int64_t B, int64_t T, int64_t D) {
+  const int64_t groups = (D + kConvBwdPiece - 1) / kConvBwdPiece;
+  int t = 32;
+  while (t > 4 && B * T / t * groups < 131072) t >>= 1;
+  return t;
+}
+
+static int64_t conv_bwd_all_tiles(int64_t B, int64_t T, int64_t D, bool packed) {
   return tiles_of(B, T, packed, conv_bwd_tile(B, T, D));
+}
+
+int64_t conv_bwd_sets(int64_t B, int64_t T, int64_t D, bool packed) {
+  return (conv_bwd_all_tiles(B, T, D, packed) + 3) / 4;
 }
 
 template <typename T, typename G, int E, bool V, int W>
 static hipError_t conv_bwd_t(const ConvBwdArgs& a, hipStream_t st) {
   const ConvArgs& f = a.f;
   const int TT = conv_bwd_tile(f.B, f.T, f.D);
-  const int64_t tiles = conv_bwd_tiles(f.B, f.T, f.D, f.cu_seqlens != nullptr);
-  const unsigned grid = conv_grid(tiles + (a.dinit ? f.N : 0), (f.D + E - 1) / E);
+  const bool packed = f.cu_seqlens != nullptr;
+  const int64_t tiles = conv_bwd_all_tiles(f.B, f.T, f.D, packed), sets = conv_bwd_sets(f.B, f.T, f.D, packed);
+  const int64_t gblocks = ((f.D + E - 1) / E + kWave - 1) / kWave;
+  const unsigned grid = static_cast<unsigned>((sets + (a.dinit ? (f.N + 3) / 4 : 0)) * gblocks);
   if (grid > 0) {
     conv_bwd_kernel<T, G, E, V, W><<<grid, kConvBlock, 0, st>>>(
         static_cast<const T*>(f.x), f.weight, f.bias, static_cast<const T*>(f.init), f.cu_seqlens, f.N, f.T, f.D, TT,
@@ -406,7 +430,7 @@ static hipError_t conv_bwd_t(const ConvBwdArgs& a, hipStream_t st) {
   float* dw = a.dweight;
   float* db = a.dbias;
   const int D = f.D;
-  return column_sums(a.part, tiles, static_cast<int64_t>(W + 1) * D, (W + (db ? 1 : 0)) * D, st,
+  return column_sums(a.part, sets, static_cast<int64_t>(W + 1) * D, (W + (db ? 1 : 0)) * D, st,
                      [=] __device__(int col, float s) {
                        const int k = col / D, ch = col - k * D;
                        if (k < W) dw[static_cast<int64_t>(ch) * W + k] = s;
@@ -424,30 +448,27 @@ static hipError_t conv_w(const ConvArgs& a, bool step, hipStream_t st) {
 }
 
 static hipError_t conv_any(const ConvArgs& a, bool step, hipStream_t st) {
-  const bool v = a.D % piece_of(a.dtype) == 0 && aligned16(a.x) && aligned16(a.y) && aligned16(a.init) && aligned16(a.fin);
-  if (a.dtype == COMBA_BF16) return v ? conv_w<u16, 8, true>(a, step, st) : conv_w<u16, 1, false>(a, step, st);
-  return v ? conv_w<float, 4, true>(a, step, st) : conv_w<float, 1, false>(a, step, st);
+  if (a.dtype == COMBA_BF16) return a.D % 8 == 0 ? conv_w<u16, 8, true>(a, step, st) : conv_w<u16, 8, false>(a, step, st);
+  return a.D % 4 == 0 ? conv_w<float, 4, true>(a, step, st) : conv_w<float, 4, false>(a, step, st);
 }
 
 hipError_t launch_conv(const ConvArgs& a, hipStream_t st) { return conv_any(a, false, st); }
 hipError_t launch_conv_step(const ConvArgs& a, hipStream_t st) { return conv_any(a, true, st); }
 
-template <typename T, typename G, int E, bool V>
+template <typename T, typename G, bool V>
 static hipError_t conv_bwd_w(const ConvBwdArgs& a, hipStream_t st) {
   switch (a.f.W) {
-    case 2: return conv_bwd_t<T, G, E, V, 2>(a, st);
-    case 3: return conv_bwd_t<T, G, E, V, 3>(a, st);
-    default: return conv_bwd_t<T, G, E, V, 4>(a, st);
+    case 2: return conv_bwd_t<T, G, kConvBwdPiece, V, 2>(a, st);
+    case 3: return conv_bwd_t<T, G, kConvBwdPiece, V, 3>(a, st);
+    default: return conv_bwd_t<T, G, kConvBwdPiece, V, 4>(a, st);
   }
 }
 
 hipError_t launch_conv_bwd(const ConvBwdArgs& a, hipStream_t st) {
-  const ConvArgs& f = a.f;
-  const bool v = f.D % piece_of(f.dtype) == 0 && aligned16(f.x) && aligned16(f.init) && aligned16(a.dy) &&
-                 aligned16(a.dfin) && aligned16(a.dx) && aligned16(a.dinit);
-  if (f.dtype == COMBA_FP32) return v ? conv_bwd_w<float, float, 4, true>(a, st) : conv_bwd_w<float, float, 1, false>(a, st);
-  if (a.dy_dtype == COMBA_FP32) return v ? conv_bwd_w<u16, float, 8, true>(a, st) : conv_bwd_w<u16, float, 1, false>(a, st);
-  return v ? conv_bwd_w<u16, u16, 8, true>(a, st) : conv_bwd_w<u16, u16, 1, false>(a, st);
+  const bool v = a.f.D % kConvBwdPiece == 0;
+  if (a.f.dtype == COMBA_FP32) return v ? conv_bwd_w<float, float, true>(a, st) : conv_bwd_w<float, float, false>(a, st);
+  if (a.dy_dtype == COMBA_FP32) return v ? conv_bwd_w<u16, float, true>(a, st) : conv_bwd_w<u16, float, false>(a, st);
+  return v ? conv_bwd_w<u16, u16, true>(a, st) : conv_bwd_w<u16, u16, false>(a, st);
 }
 
 }  // namespace comba
