@@ -319,49 +319,64 @@ __global__ __launch_bounds__(kScanBlock) void scan_step_kernel(
   for (int i = 0; i < NPL; ++i) A2[i] *= kLog2E;
   const float bias = dt_bias ? dt_bias[c] : 0.f, sk = skip ? skip[c] : 0.f;
   const int64_t first = static_cast<int64_t>(blockIdx.x / cblocks) * per;
-  for (int64_t n = first; n < first + per && n < N; ++n) {
-    float h[NPL];
-    const int64_t at = (n * D + c) * S;
-    if (!init) {
+  constexpr int U = 2;  // sequences whose loads are in flight together
+  for (int64_t n0 = first; n0 < first + per && n0 < N; n0 += U) {
+    float h[U][NPL], b[U][NPL], cc[U][NPL], xv[U], dl[U], zv[U];
 #pragma unroll
-      for (int i = 0; i < NPL; ++i) h[i] = 0.f;
-    } else if constexpr (V) {
+    for (int u = 0; u < U; ++u) {
+      const int64_t n = min(n0 + u, static_cast<int64_t>(N) - 1), at = (n * D + c) * S;
+      if (!init) {
 #pragma unroll
-      for (int i = 0; i < NPL; i += 4) {
-        const f32x4 v = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(init + at + s0 + i));
-        h[i] = v[0]; h[i + 1] = v[1]; h[i + 2] = v[2]; h[i + 3] = v[3];
-      }
-    } else {
-      load_states<NPL>(init + at, s0, S, h);
-    }
-    const float xv = Elem<T>::load(x, n * D + c);
-    float dl = Elem<T>::load(dt, n * D + c) + bias;
-    if (softplus) dl = softplus_f32(dl);
-    const float dx = dl * xv;
-    const T* B = Bm + (n * G + p.g) * S;
-    const T* C = Cm + (n * G + p.g) * S;
-    float o = 0.f;
+        for (int i = 0; i < NPL; ++i) h[u][i] = 0.f;
+      } else if constexpr (V) {
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-      const bool have = V || s0 + i < S;
-      const float b = have ? Elem<T>::load(B, s0 + i) : 0.f, cc = have ? Elem<T>::load(C, s0 + i) : 0.f;
-      h[i] = fmaf(__builtin_amdgcn_exp2f(dl * A2[i]), h[i], dx * b);
-      o = fmaf(h[i], cc, o);
-    }
-    o = fmaf(sk, xv, lane_total<4>(o));
-    if (z) {
-      const float zv = Elem<T>::load(z, n * D + c);
-      o *= zv * sigmoid_fast(zv);
-    }
-    if (q == 0) Elem<T>::store(y, n * D + c, o);
-    if (fin) {
-      if constexpr (V) {
-#pragma unroll
-        for (int i = 0; i < NPL; i += 4)
-          __builtin_nontemporal_store(f32x4{h[i], h[i + 1], h[i + 2], h[i + 3]},
-                                      reinterpret_cast<f32x4*>(fin + at + s0 + i));
+        for (int i = 0; i < NPL; i += 4) {
+          const f32x4 v = *reinterpret_cast<const f32x4*>(init + at + s0 + i);
+          h[u][i] = v[0]; h[u][i + 1] = v[1]; h[u][i + 2] = v[2]; h[u][i + 3] = v[3];
+        }
       } else {
-        store_states<NPL>(fin + at, s0, S, h);
+        load_states<NPL>(init + at, s0, S, h[u]);
+      }
+      xv[u] = Elem<T>::load(x, n * D + c);
+      dl[u] = Elem<T>::load(dt, n * D + c) + bias;
+      zv[u] = z ? Elem<T>::load(z, n * D + c) : 0.f;
+      const T* B = Bm + (n * G + p.g) * S + s0;
+      const T* C = Cm + (n * G + p.g) * S + s0;
+      if constexpr (V) {
+        Pack<T, NPL, true>::load(B, b[u], NPL);
+        Pack<T, NPL, true>::load(C, cc[u], NPL);
+      } else {
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+          b[u][i] = s0 + i < S ? Elem<T>::load(B, i) : 0.f;
+          cc[u][i] = s0 + i < S ? Elem<T>::load(C, i) : 0.f;
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t n = n0 + u;
+      if (n >= first + per || n >= N) break;
+      const float d = softplus ? softplus_f32(dl[u]) : dl[u], dx = d * xv[u];
+      float o = 0.f;
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) {
+        h[u][i] = fmaf(__builtin_amdgcn_exp2f(d * A2[i]), h[u][i], dx * b[u][i]);
+        o = fmaf(h[u][i], cc[u][i], o);
+      }
+      o = fmaf(sk, xv[u], lane_total<4>(o));
+      if (z) o *= zv[u] * sigmoid_fast(zv[u]);
+      if (q == 0) Elem<T>::store(y, n * D + c, o);
+      if (fin) {
+        const int64_t at = (n * D + c) * S;
+        if constexpr (V) {
+#pragma unroll
+          for (int i = 0; i < NPL; i += 4)
+            __builtin_nontemporal_store(f32x4{h[u][i], h[u][i + 1], h[u][i + 2], h[u][i + 3]},
+                                        reinterpret_cast<f32x4*>(fin + at + s0 + i));
+        } else {
+          store_states<NPL>(fin + at, s0, S, h[u]);
+        }
       }
     }
   }

@@ -120,41 +120,95 @@ __device__ __forceinline__ void channel_sums(float* v, int lane) {
   }
 }
 
-// Index of the first value that channel_sums<N> leaves in this lane, and whether the lane is the one
-// that writes it (where lanes hold the same value).
+// Index of the first value that channel_sums<N> leaves in this lane. Lanes that differ in the bits
+// behind the last halving hold the same value.
 template <int N>
-__device__ __forceinline__ int channel_sum_index(int lane, bool& writer) {
+__device__ __forceinline__ int channel_sum_index(int lane) {
   int at = 0, n = N;
-  writer = true;
 #pragma unroll
   for (int b = 5; b >= 2; --b) {
-    const int bit = (lane >> b) & 1;
-    if (n >= 2) {
-      n /= 2;
-      at += bit * n;
-    } else if (bit) {
-      writer = false;
-    }
+    if (n < 2) break;
+    n /= 2;
+    at += ((lane >> b) & 1) * n;
   }
   return at;
 }
 
-template <typename T>
-__device__ __forceinline__ float step_size(const ScanBwdK<T>& a, float raw, float bias) {
-  const float u = raw + bias;
-  return a.softplus ? softplus_f32(u) : u;
-}
+// A piece of TT tokens for the 64 channels of a workgroup, worked on per (token, channel) with a lane
+// per channel: thread (tk, ch) has tokens tk, tk + 4, ... of channel ch. Tokens behind the segment
+// and channels behind the group's last read 0 and store nowhere.
+template <typename T, int TT> struct Piece {
+  static constexpr int R = TT / 4;
+  uint32_t own[R];
+  uint32_t rx[R], rd[R], rz[R], ry[R];
+  float bias;
+  int tk, ch;
+  bool live;
+
+  __device__ __forceinline__ void place(const ScanBwdK<T>& a, const ScanPlace& p) {
+    ch = threadIdx.x % kScanChannels;
+    tk = threadIdx.x / kScanChannels;
+    live = ch < p.cl;
+    const int c = p.c0 + (live ? ch : p.cl - 1);
+    bias = a.dt_bias ? a.dt_bias[c] : 0.f;
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+      own[j] = live ? (static_cast<uint32_t>(tk + 4 * j) * a.D + c) * static_cast<uint32_t>(sizeof(T)) : kNowhere;
+  }
+  // The rows of the piece that starts at token t of the segment, as a range of `base`.
+  static __device__ __forceinline__ Range<T> rows(const T* base, const ScanBwdK<T>& a, const ScanPlace& p, int t) {
+    const int n = max(0, min(TT, p.t1 - p.t0 - t));
+    return Range<T>(base + (base ? (static_cast<int64_t>(p.b) * a.T_ + p.t0 + t) * a.D : 0),
+                    base ? static_cast<int64_t>(n) * a.D * sizeof(T) : 0);
+  }
+  template <bool ALL> __device__ __forceinline__ void fetch(const ScanBwdK<T>& a, const ScanPlace& p, int t) {
+    const Range<T> x = rows(a.x, a, p, t), d = rows(a.dt, a, p, t);
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      rx[j] = x.load(own[j]);
+      rd[j] = d.load(own[j]);
+    }
+    if constexpr (ALL) {
+      const Range<T> z = rows(a.z, a, p, t), y = rows(a.dy, a, p, t);
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        rz[j] = z.load(own[j]);
+        ry[j] = y.load(own[j]);
+      }
+    }
+  }
+  __device__ __forceinline__ float step(const ScanBwdK<T>& a, const ScanPlace& p, int t, int j) const {
+    const float u = Range<T>::value(rd[j]) + bias;
+    float d = softplus_f32(u);
+    pin(d);
+    d = a.softplus ? d : u;
+    return live && t + tk + 4 * j < p.t1 - p.t0 ? d : 0.f;  // elsewhere: decay 1, no input
+  }
+  // dy z sigmoid(z), the gradient of the ungated y; s: sigmoid(z)
+  __device__ __forceinline__ float grad(const ScanBwdK<T>& a, int j, float& s) const {
+    const float y = Range<T>::value(ry[j]), z = Range<T>::value(rz[j]);
+    s = sigmoid_fast(z);
+    float g = z * s;
+    pin(g);
+    return a.z ? y * g : y;
+  }
+};
 
 template <typename T, int NPL>
 __global__ __launch_bounds__(kScanBlock) void scan_bwd_ends_kernel(ScanBwdK<T> a) {
-  constexpr int SP = 4 * NPL, L = BwdTile<NPL>::L;
+  constexpr int SP = 4 * NPL, L = BwdTile<NPL>::L, TT = BwdTile<NPL>::CT;
   __shared__ __align__(16) float bc[L][4][2 * NPL];
+  __shared__ __align__(16) f32x4 st[2][TT][kScanChannels];  // step size, input, gradient of y
+  __shared__ float tot[4][kScanChannels];
   const int tid = threadIdx.x, lane = tid & 63, q = lane & 3;
   const int cblocks = a.G * ((a.D / a.G + kScanChannels - 1) / kScanChannels);
   const ScanPlace p = scan_place<kScanChannels>(blockIdx.x / cblocks, blockIdx.x % cblocks, a.cu, a.N, a.T_, a.D, a.G, L);
   if (!p.ok) return;
+  Piece<T, TT> pc;
+  pc.place(a, p);
+  pc.template fetch<true>(a, p, 0);
   stage_bc<T, NPL, L>(a, p, bc);
-  const int in = (tid >> 6) * 16 + (lane >> 2);
+  const int in = tid / 4;
   const bool live = in < p.cl;
   const int c = p.c0 + (live ? in : p.cl - 1);
   float A2[NPL], h[NPL], gs[NPL], pr[NPL];
@@ -165,49 +219,41 @@ __global__ __launch_bounds__(kScanBlock) void scan_bwd_ends_kernel(ScanBwdK<T> a
     h[i] = gs[i] = 0.f;
     pr[i] = 1.f;
   }
-  const float bias = a.dt_bias ? a.dt_bias[c] : 0.f;
-  __syncthreads();
-  const int64_t row0 = static_cast<int64_t>(p.b) * a.T_ + p.t0;
   const int len = p.t1 - p.t0;
   float dtot = 0.f;
-  constexpr int U = 4;  // groups of four tokens fetched together
-  for (int t = 0; t < len; t += 4 * U) {
-    float rx[U], rd[U], rz[U], ry[U];
+  for (int t = 0, buf = 0; t < len; t += TT, buf ^= 1) {
 #pragma unroll
-    for (int j = 0; j < U; ++j) {
-      const int64_t o = (row0 + min(t + 4 * j + q, len - 1)) * a.D + c;
-      rx[j] = Elem<T>::load(a.x, o);
-      rd[j] = Elem<T>::load(a.dt, o);
-      ry[j] = Elem<T>::load(a.dy, o);
-      rz[j] = a.z ? Elem<T>::load(a.z, o) : 0.f;
+    for (int j = 0; j < pc.R; ++j) {
+      float s;
+      const float d = pc.step(a, p, t, j), g = pc.grad(a, j, s);
+      dtot += d;
+      st[buf][pc.tk + 4 * j][pc.ch] = f32x4{d, d * Range<T>::value(pc.rx[j]), g, 0.f};
     }
+    pc.template fetch<true>(a, p, t + TT);
+    __syncthreads();  // the other buffer is written only behind the next one
 #pragma unroll
-    for (int j = 0; j < U; ++j) {
-      if (t + 4 * j >= len) break;
-      const bool have = t + 4 * j + q < len;
-      const float dl = have ? step_size(a, rd[j], bias) : 0.f;
-      const float dx = have ? dl * rx[j] : 0.f;
-      float dyp = have ? ry[j] : 0.f;
-      if (a.z && have) dyp *= rz[j] * sigmoid_fast(rz[j]);
-      dtot += dl;
-      auto token = [&](auto kc) {
-        constexpr int K = decltype(kc)::value;
-        const float dk = quad_bcast<K>(dl), xk = quad_bcast<K>(dx), yk = quad_bcast<K>(dyp);
-        const float* r = bc[t + 4 * j + K][q];
+    for (int k = 0; k < TT; ++k) {
+      const f32x4 e4 = st[buf][k][in];
+      const float* r = bc[t + k][q];
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) {
+        const float e = __builtin_amdgcn_exp2f(e4[0] * A2[i]);
+        h[i] = fmaf(e, h[i], e4[1] * r[i]);
+        pr[i] *= e;
+        gs[i] = fmaf(pr[i], e4[2] * r[NPL + i], gs[i]);
+      }
+      if (k % 4 == 3)
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
-          const float e = __builtin_amdgcn_exp2f(dk * A2[i]);
-          h[i] = fmaf(e, h[i], xk * r[i]);
-          pr[i] *= e;
-          gs[i] = fmaf(pr[i], yk * r[NPL + i], gs[i]);
+          pin(h[i]);
+          pin(gs[i]);
         }
-      };
-      token(std::integral_constant<int, 0>{});
-      token(std::integral_constant<int, 1>{});
-      token(std::integral_constant<int, 2>{});
-      token(std::integral_constant<int, 3>{});
     }
   }
+  tot[pc.tk][pc.ch] = dtot;
+  __syncthreads();
+  if (tid < kScanChannels && pc.live)
+    a.dsum[p.slot * a.D + p.c0 + tid] = (tot[0][tid] + tot[1][tid]) + (tot[2][tid] + tot[3][tid]);
   if (!live) return;
   const int64_t at = (p.slot * a.D + c) * SP + q * NPL;
 #pragma unroll
@@ -215,8 +261,6 @@ __global__ __launch_bounds__(kScanBlock) void scan_bwd_ends_kernel(ScanBwdK<T> a
     a.hseg[at + i] = h[i];
     a.gseg[at + i] = gs[i];
   }
-  dtot = lane_total<4>(dtot);
-  if (q == 0) a.dsum[p.slot * a.D + c] = dtot;
 }
 
 // One thread per (direction, sequence, channel, state): hseg becomes the segments' incoming states,
@@ -264,28 +308,33 @@ __global__ __launch_bounds__(kScanBlock) void scan_bwd_carry_kernel(
 
 template <typename T, int NPL>
 __global__ __launch_bounds__(kScanBlock) void scan_bwd_kernel(ScanBwdK<T> a) {
-  constexpr int SP = 4 * NPL, CT = BwdTile<NPL>::CT, NSUB = BwdTile<NPL>::NSUB, L = BwdTile<NPL>::L, Q = CT / 4;
+  constexpr int SP = 4 * NPL, CT = BwdTile<NPL>::CT, NSUB = BwdTile<NPL>::NSUB, L = BwdTile<NPL>::L;
   constexpr int NV = 2 * NPL, LEFT = NV >= 16 ? NV / 16 : 1;
   __shared__ __align__(16) float bc[L][4][NV];
   __shared__ __align__(16) float held[NSUB][kScanBlock][NPL];   // states at the start of every piece
-  __shared__ __align__(16) float red[2][4][CT][4][NV];          // dB, dC of a piece, per wavefront
+  __shared__ __align__(16) float red[4][CT][4][NV];             // dB, dC of a piece, per wavefront
+  // Per (token, channel) of a piece: step size, input, gradient of y. The channel's quad replaces
+  // them by what the token's thread needs: (sum g B, sum A k, , y).
+  __shared__ __align__(16) f32x4 st[CT][kScanChannels];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, q = lane & 3;
   const int dg = a.D / a.G, per = (dg + kScanChannels - 1) / kScanChannels, cblocks = a.G * per;
   const int cb = blockIdx.x % cblocks;
   const ScanPlace p = scan_place<kScanChannels>(blockIdx.x / cblocks, cb, a.cu, a.N, a.T_, a.D, a.G, L);
-  const int in = wave * 16 + (lane >> 2);
+  const int in = tid / 4;
   const bool live = in < p.cl;
   const int c = p.c0 + (live ? in : p.cl - 1);
   const int64_t at = (p.slot * a.D + c) * SP + q * NPL;
-  const int64_t dpart = p.slot * 2 * a.D + c;
   if (!p.ok) {  // a slot between sequences adds nothing
     if (live) {
 #pragma unroll
       for (int i = 0; i < NPL; ++i) a.dApart[at + i] = 0.f;
-      if (q == 0) a.dDpart[dpart] = a.dDpart[dpart + a.D] = 0.f;
+      if (q == 0) a.dDpart[p.slot * 2 * a.D + c] = a.dDpart[(p.slot * 2 + 1) * a.D + c] = 0.f;
     }
     return;
   }
+  Piece<T, CT> pc;
+  pc.place(a, p);
+  pc.template fetch<false>(a, p, 0);
   stage_bc<T, NPL, L>(a, p, bc);
   float A2[NPL], h[NPL], gc[NPL], dA[NPL];  // gc: gradient that reaches the state before token t + 1
 #pragma unroll
@@ -296,154 +345,157 @@ __global__ __launch_bounds__(kScanBlock) void scan_bwd_kernel(ScanBwdK<T> a) {
     gc[i] = live ? a.gseg[at + i] : 0.f;
     dA[i] = 0.f;
   }
-  const float bias = a.dt_bias ? a.dt_bias[c] : 0.f, skip = a.skip ? a.skip[c] : 0.f;
+  const int lc = p.c0 + (pc.live ? pc.ch : p.cl - 1);
+  const float skip = a.skip ? a.skip[lc] : 0.f;
   const int64_t row0 = static_cast<int64_t>(p.b) * a.T_ + p.t0;
   const int len = p.t1 - p.t0, nsub = (len + CT - 1) / CT;
   float dskip = 0.f, dbias = 0.f;
-  __syncthreads();
 
-  // states at the start of every piece
+  // states at the start of every piece; the step sizes and inputs of two pieces share st
+  f32x2(*sd)[CT][kScanChannels] = reinterpret_cast<f32x2(*)[CT][kScanChannels]>(&st[0][0]);
   for (int k = 0; k < nsub; ++k) {
 #pragma unroll
     for (int i = 0; i < NPL; ++i) held[k][tid][i] = h[i];
     if (k == nsub - 1) break;
-    float rx[Q], rd[Q];
 #pragma unroll
-    for (int j = 0; j < Q; ++j) {
-      const int64_t o = (row0 + k * CT + 4 * j + q) * a.D + c;
-      rx[j] = Elem<T>::load(a.x, o);
-      rd[j] = Elem<T>::load(a.dt, o);
+    for (int j = 0; j < pc.R; ++j) {
+      const float d = pc.step(a, p, k * CT, j);
+      sd[k & 1][pc.tk + 4 * j][pc.ch] = f32x2{d, d * Range<T>::value(pc.rx[j])};
     }
+    pc.template fetch<false>(a, p, (k + 1) * CT);
+    __syncthreads();
 #pragma unroll
-    for (int j = 0; j < Q; ++j) {
-      const float dl = live ? step_size(a, rd[j], bias) : 0.f;
-      const float dx = live ? dl * rx[j] : 0.f;
-      auto token = [&](auto kc) {
-        constexpr int K = decltype(kc)::value;
-        const float dk = quad_bcast<K>(dl), xk = quad_bcast<K>(dx);
-        const float* r = bc[k * CT + 4 * j + K][q];
+    for (int t = 0; t < CT; ++t) {
+      const f32x2 e2 = sd[k & 1][t][in];
+      const float* r = bc[k * CT + t][q];
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) h[i] = fmaf(__builtin_amdgcn_exp2f(dk * A2[i]), h[i], xk * r[i]);
-      };
-      token(std::integral_constant<int, 0>{});
-      token(std::integral_constant<int, 1>{});
-      token(std::integral_constant<int, 2>{});
-      token(std::integral_constant<int, 3>{});
+      for (int i = 0; i < NPL; ++i) h[i] = fmaf(__builtin_amdgcn_exp2f(e2[0] * A2[i]), h[i], e2[1] * r[i]);
+      if (t % 4 == 3)
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) pin(h[i]);
     }
   }
 
-  bool writer;
-  const int vat = channel_sum_index<NV>(lane, writer);
-  const int cbg = cb - p.g * per;
-  for (int k = nsub - 1, buf = 0; k >= 0; --k, buf ^= 1) {
-    float xv[Q], ud[Q], zv[Q], yv[Q], dl[Q], dx[Q], dyp[Q], yr[Q];
+  const int vat = channel_sum_index<NV>(lane), cbg = cb - p.g * per;
+  const int64_t rows = static_cast<int64_t>(a.cu ? 1 : a.N) * a.T_;
+  pc.template fetch<true>(a, p, max(nsub - 1, 0) * CT);
+  for (int k = nsub - 1; k >= 0; --k) {
+    __syncthreads();  // everything of the piece before is read
+    float xv[pc.R], uv[pc.R], zv[pc.R], yv[pc.R], dl[pc.R], dyp[pc.R], gz[pc.R];
 #pragma unroll
-    for (int j = 0; j < Q; ++j) {
-      const int t = k * CT + 4 * j + q;
-      const int64_t o = (row0 + min(t, len - 1)) * a.D + c;
-      xv[j] = Elem<T>::load(a.x, o);
-      ud[j] = Elem<T>::load(a.dt, o) + bias;
-      yv[j] = Elem<T>::load(a.dy, o);
-      zv[j] = a.z ? Elem<T>::load(a.z, o) : 0.f;
+    for (int j = 0; j < pc.R; ++j) {
+      xv[j] = Range<T>::value(pc.rx[j]);
+      uv[j] = Range<T>::value(pc.rd[j]) + pc.bias;
+      zv[j] = Range<T>::value(pc.rz[j]);
+      yv[j] = Range<T>::value(pc.ry[j]);
+      dl[j] = pc.step(a, p, k * CT, j);
+      dyp[j] = pc.grad(a, j, gz[j]);
+      st[pc.tk + 4 * j][pc.ch] = f32x4{dl[j], dl[j] * xv[j], dyp[j], 0.f};
     }
+    if (k > 0) pc.template fetch<true>(a, p, (k - 1) * CT);
 #pragma unroll
     for (int i = 0; i < NPL; ++i) h[i] = held[k][tid][i];
+    __syncthreads();
     float hs[CT][NPL], as[CT][NPL];
 #pragma unroll
-    for (int j = 0; j < Q; ++j) {
-      const bool have = live && k * CT + 4 * j + q < len;
-      dl[j] = have ? (a.softplus ? softplus_f32(ud[j]) : ud[j]) : 0.f;
-      dx[j] = have ? dl[j] * xv[j] : 0.f;
-      dyp[j] = have ? (a.z ? yv[j] * (zv[j] * sigmoid_fast(zv[j])) : yv[j]) : 0.f;
+    for (int j = 0; j < CT / 4; ++j) {
       float ys[4];
-      auto token = [&](auto kc) {
-        constexpr int K = decltype(kc)::value;
-        const float dk = quad_bcast<K>(dl[j]), xk = quad_bcast<K>(dx[j]);
-        const float* r = bc[k * CT + 4 * j + K][q];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const f32x4 e4 = st[4 * j + t][in];
+        const float* r = bc[k * CT + 4 * j + t][q];
         float y = 0.f;
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
-          const float e = __builtin_amdgcn_exp2f(dk * A2[i]);
-          const float prev = (4 * j + K) ? hs[(4 * j + K) ? 4 * j + K - 1 : 0][i] : h[i];
-          as[4 * j + K][i] = e;
-          hs[4 * j + K][i] = fmaf(e, prev, xk * r[i]);
-          y = fmaf(hs[4 * j + K][i], r[NPL + i], y);
+          const float e = __builtin_amdgcn_exp2f(e4[0] * A2[i]);
+          const float prev = (j || t) ? hs[4 * j + t - (j || t)][i] : h[i];
+          as[4 * j + t][i] = e;
+          hs[4 * j + t][i] = fmaf(e, prev, e4[1] * r[i]);
+          y = i ? fmaf(hs[4 * j + t][i], r[NPL + i], y) : hs[4 * j + t][i] * r[NPL];
         }
-        ys[K] = y;
-      };
-      token(std::integral_constant<int, 0>{});
-      token(std::integral_constant<int, 1>{});
-      token(std::integral_constant<int, 2>{});
-      token(std::integral_constant<int, 3>{});
-      yr[j] = lane_sums<4>(ys, lane);
+        ys[t] = y;
+      }
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) pin(hs[4 * j + t][i]);
+      st[4 * j + q][in][3] = lane_sums<4>(ys, lane);
     }
 #pragma unroll
-    for (int j = Q - 1; j >= 0; --j) {
+    for (int j = CT / 4 - 1; j >= 0; --j) {
       float sb[4], sa[4];
-      auto token = [&](auto kc) {
-        constexpr int K = decltype(kc)::value, t = K;
-        const float dk = quad_bcast<K>(dl[j]), xk = quad_bcast<K>(dx[j]), yk = quad_bcast<K>(dyp[j]);
-        const float* r = bc[k * CT + 4 * j + K][q];
+#pragma unroll
+      for (int t = 3; t >= 0; --t) {
+        const f32x4 e4 = st[4 * j + t][in];
+        const float* r = bc[k * CT + 4 * j + t][q];
         float v[NV], b = 0.f, d = 0.f;
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
-          const float g = fmaf(yk, r[NPL + i], gc[i]);
-          const float prev = (4 * j + t) ? hs[(4 * j + t) ? 4 * j + t - 1 : 0][i] : h[i];
-          v[i] = g * xk;
-          v[NPL + i] = hs[4 * j + t][i] * yk;
-          b = fmaf(g, r[i], b);
+          const float g = fmaf(e4[2], r[NPL + i], gc[i]);
+          const float prev = (j || t) ? hs[4 * j + t - (j || t)][i] : h[i];
+          v[i] = g * e4[1];
+          v[NPL + i] = hs[4 * j + t][i] * e4[2];
+          b = i ? fmaf(g, r[i], b) : g * r[i];
           gc[i] = g * as[4 * j + t][i];
           const float kk = gc[i] * prev;
-          dA[i] = fmaf(kk, dk, dA[i]);
-          d = fmaf(kk, A2[i], d);
+          dA[i] = fmaf(kk, e4[0], dA[i]);
+          d = i ? fmaf(kk, A2[i], d) : kk * A2[i];
         }
-        sb[K] = b;
-        sa[K] = d;
+        sb[t] = b;
+        sa[t] = d;
         channel_sums<NV>(v, lane);
-        if (writer)
 #pragma unroll
-          for (int i = 0; i < LEFT; ++i) red[buf][wave][4 * j + K][q][vat + i] = v[i];
-      };
-      token(std::integral_constant<int, 3>{});
-      token(std::integral_constant<int, 2>{});
-      token(std::integral_constant<int, 1>{});
-      token(std::integral_constant<int, 0>{});
+        for (int i = 0; i < LEFT; ++i) red[wave][4 * j + t][q][vat + i] = v[i];
+      }
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) {
+        pin(gc[i]);
+        pin(dA[i]);
+      }
       const float b = lane_sums<4>(sb, lane), d = lane_sums<4>(sa, lane) * (1.f / kLog2E);
-      if (live && k * CT + 4 * j + q < len) {
-        const int64_t o = (row0 + k * CT + 4 * j + q) * a.D + c;
-        Elem<T>::store(a.dx, o, fmaf(dl[j], b, skip * dyp[j]));
-        float dd = fmaf(xv[j], b, d);
-        if (a.softplus) dd *= sigmoid_fast(ud[j]);
-        Elem<T>::store(a.ddt, o, dd);
+      *reinterpret_cast<f32x2*>(&st[4 * j + q][in]) = f32x2{b, d};
+    }
+    __syncthreads();
+    const Range<T> ox = Piece<T, CT>::rows(a.dx, a, p, k * CT), od = Piece<T, CT>::rows(a.ddt, a, p, k * CT),
+                   oz = Piece<T, CT>::rows(a.dz, a, p, k * CT);
+#pragma unroll
+    for (int j = 0; j < pc.R; ++j) {
+      const f32x4 e4 = st[pc.tk + 4 * j][pc.ch];
+      ox.store(pc.own[j], fmaf(dl[j], e4[0], skip * dyp[j]));
+      float dd = fmaf(xv[j], e4[0], e4[1]), s = sigmoid_fast(uv[j]);
+      pin(s);
+      dd = a.softplus ? dd * s : dd;
+      od.store(pc.own[j], dd);
+      oz.store(pc.own[j], yv[j] * fmaf(skip, xv[j], e4[3]) * (gz[j] * fmaf(zv[j], 1.f - gz[j], 1.f)));
+      if (pc.live && k * CT + pc.tk + 4 * j < len) {
         dbias += dd;
         dskip = fmaf(dyp[j], xv[j], dskip);
-        if (a.z) {
-          const float s = sigmoid_fast(zv[j]);
-          Elem<T>::store(a.dz, o, yv[j] * fmaf(skip, xv[j], yr[j]) * (s * fmaf(zv[j], 1.f - s, 1.f)));
-        }
       }
     }
-    __syncthreads();  // the other buffer is written again only behind the next one
     for (int e = tid; e < CT * 2 * SP; e += kScanBlock) {
       const int t = e / (2 * SP), which = (e / SP) & 1, s = e % SP;
       if (k * CT + t < len) {
         float v = 0.f;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) v += red[buf][w][t][s / NPL][which * NPL + s % NPL];
-        const int64_t row = row0 + k * CT + t, rows = static_cast<int64_t>(a.cu ? 1 : a.N) * a.T_;
-        a.dBCpart[((cbg * rows + row) * a.G + p.g) * (2 * SP) + which * SP + s] = v;
+        for (int w = 0; w < 4; ++w) v += red[w][t][s / NPL][which * NPL + s % NPL];
+        a.dBCpart[((cbg * rows + row0 + k * CT + t) * a.G + p.g) * (2 * SP) + which * SP + s] = v;
       }
     }
+  }
+  // the four token groups' sums of a channel
+  __syncthreads();
+  st[pc.tk][pc.ch] = f32x4{dskip, dbias, 0.f, 0.f};
+  __syncthreads();
+  if (tid < kScanChannels && pc.live) {
+    f32x4 t = st[0][tid];
+#pragma unroll
+    for (int w = 1; w < 4; ++w) t += st[w][tid];
+    a.dDpart[p.slot * 2 * a.D + lc] = t[0];
+    a.dDpart[(p.slot * 2 + 1) * a.D + lc] = t[1];
   }
   if (!live) return;
 #pragma unroll
   for (int i = 0; i < NPL; ++i) a.dApart[at + i] = dA[i];
-  dskip = lane_total<4>(dskip);
-  dbias = lane_total<4>(dbias);
-  if (q == 0) {
-    a.dDpart[dpart] = dskip;
-    a.dDpart[dpart + a.D] = dbias;
-  }
 }
 
 // dB and dC: the partial sums of the group's channel blocks, added in order and rounded once.
