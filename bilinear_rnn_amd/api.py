@@ -514,6 +514,12 @@ def _may(t: Optional[torch.Tensor], name: str, dtype, shape, index: int):
 
 def _activation(t: torch.Tensor, name: str, dims: int) -> int:
     """Checks the tensor that the others are measured by; returns its device's index."""
+    try:
+        index = t.get_device()
+        if index >= 0 and t.dtype in _DT and t.dim() == dims and t.is_contiguous():
+            return index
+    except AttributeError:
+        pass
     _require(t, name)
     if t.dtype not in _DT:
         raise ValueError(f"{name} must be bfloat16 or float32 (got {t.dtype})")
@@ -603,7 +609,7 @@ def short_conv(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
     if final_state is not None or not output_final_state:
         _may(final_state, "final_state", x.dtype, (N, W - 1, D), index)
     else:
-        final_state = torch.empty((N, W - 1, D), dtype=x.dtype, device=x.device)
+        final_state = x.new_empty((N, W - 1, D))
     _run(lib().comba_short_conv_fwd, index,
          _at(x), _at(weight), _at(bias), _at(initial_state), _at(cu_seqlens),
          N if cu_seqlens is not None else 0, B, T, D, W, _DT[x.dtype], int(bool(silu)), _at(out),
@@ -624,21 +630,20 @@ def short_conv_step(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.
         out = torch.empty_like(x)
     else:
         _need(out, "out", x.dtype, (N, D), index)
-    final_state = _step_state(initial_state, final_state, in_place, output_final_state, (N, W - 1, D), x.dtype,
-                              x.device, index)
+    final_state = _step_state(x, initial_state, final_state, in_place, output_final_state, (N, W - 1, D), x.dtype, index)
     _run(lib().comba_short_conv_step, index,
          _at(x), _at(weight), _at(bias), _at(initial_state), N, D, W, _DT[x.dtype], int(bool(silu)), _at(out),
          _at(final_state))
     return out, final_state
 
 
-def _step_state(initial_state, final_state, in_place, output_final_state, shape, dtype, device, index):
+def _step_state(x, initial_state, final_state, in_place, output_final_state, shape, dtype, index):
     if in_place:
         if initial_state is None:
             raise ValueError("in_place requires initial_state")
         return initial_state
     if final_state is None and output_final_state:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return x.new_empty(shape, dtype=dtype)
     _may(final_state, "final_state", dtype, shape, index)
     return final_state
 
@@ -720,7 +725,7 @@ def selective_scan(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, Bm: torch
     if final_state is not None or not output_final_state:
         _may(final_state, "final_state", torch.float32, (N, D, S), index)
     else:
-        final_state = torch.empty((N, D, S), dtype=torch.float32, device=x.device)
+        final_state = x.new_empty((N, D, S), dtype=torch.float32)
     nseq = N if cu_seqlens is not None else 0
     workspace = _workspace(workspace, selective_scan_workspace_size(B, T, D, S, G, nseq), x.device)
     _run(lib().comba_selective_scan_fwd, index,
@@ -745,8 +750,7 @@ def selective_step(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, Bm: torch
         out = torch.empty_like(x)
     else:
         _need(out, "out", x.dtype, (N, D), index)
-    final_state = _step_state(initial_state, final_state, in_place, output_final_state, (N, D, S), torch.float32,
-                              x.device, index)
+    final_state = _step_state(x, initial_state, final_state, in_place, output_final_state, (N, D, S), torch.float32, index)
     _run(lib().comba_selective_step, index,
          _at(x), _at(dt), _at(A), _at(Bm), _at(Cm), _at(skip), _at(z), _at(dt_bias), int(bool(softplus)),
          _at(initial_state), N, D, S, G, _DT[x.dtype], _at(out), _at(final_state))
@@ -785,13 +789,11 @@ def selective_scan_bwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, Bm: t
 
 
 def _norm_args(y, gate, residual, scale, post_weight, pre_weight):
-    _require(y, "y")
-    if y.dtype not in _DT:
-        raise ValueError(f"y must be bfloat16 or float32 (got {y.dtype})")
-    if y.dim() < 1 or y.shape[-1] < 1:
+    dims = y.dim() if isinstance(y, torch.Tensor) else 1
+    index = _activation(y, "y", dims)
+    if dims < 1 or y.shape[-1] < 1:
         raise ValueError("y must be [..., D]")
     D = y.shape[-1]
-    index = y.get_device()
     _may(gate, "gate", y.dtype, y.shape, index)
     _may(residual, "residual", y.dtype, y.shape, index)
     _may(scale, "scale", torch.float32, (D,), index)
