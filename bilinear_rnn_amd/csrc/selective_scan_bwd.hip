@@ -16,7 +16,9 @@
 //   4. the sums over segments (dA, dskip, ddt_bias) and over channel blocks (dB, dC), in a fixed order.
 // Nothing is kept from the forward. Bound by the vector ALU like the forward: three exponentials and
 // about 25 instructions per (token, channel, state). The sums over the 16 channels of a wavefront
-// halve the values at every step (permlane swaps: two instructions per pair of values).
+// halve the values at every step (permlane swaps: two instructions per pair of values). Through LDS
+// instead (terms written, one sum per lane read back) the vector ALU has 12 % less to do, but the
+// kernel waits for LDS longer than that: 316 us against 300 at B = 4, T = 2048, D = 2048, S = 16.
 #include "column_sums.h"
 #include "comba.h"
 #include "scan_common.h"
@@ -55,21 +57,6 @@ template <typename T> struct ScanBwdK {
   int N, T_, D, S, G, L;
   bool softplus;
 };
-
-// B and C of the segment's tokens as float32 in LDS, [token][quad lane][NPL of B, NPL of C]; 0 where
-// there is no token or state.
-template <typename T, int NPL, int L>
-__device__ __forceinline__ void stage_bc(const ScanBwdK<T>& a, const ScanPlace& p, float (*bc)[4][2 * NPL]) {
-  constexpr int SP = 4 * NPL;
-  const int64_t row0 = static_cast<int64_t>(p.b) * a.T_ + p.t0;
-  for (int e = threadIdx.x; e < L * SP; e += kScanBlock) {
-    const int t = e / SP, s = e % SP;
-    const bool have = p.t0 + t < p.t1 && s < a.S;
-    const int64_t o = ((row0 + t) * a.G + p.g) * a.S + s;
-    bc[t][s / NPL][s % NPL] = have ? Elem<T>::load(a.Bm, o) : 0.f;
-    bc[t][s / NPL][NPL + s % NPL] = have ? Elem<T>::load(a.Cm, o) : 0.f;
-  }
-}
 
 // Sums v over the 16 channels of the wavefront (lane bits 2 .. 5). At lane bit 5, 4, 3, 2 a lane keeps
 // the lower half of its values if the bit is clear, the upper half if it is set, while there are two
@@ -194,10 +181,45 @@ template <typename T, int TT> struct Piece {
   }
 };
 
+// The piece's B and C: the thread's elements (token, state), 0 where there is none.
+template <typename T, int TT, int SP> struct PieceBC {
+  static constexpr int PT = (TT * SP + kScanBlock - 1) / kScanBlock;
+  uint32_t off[PT], rb[PT], rc[PT];
+  __device__ __forceinline__ void place(const ScanBwdK<T>& a) {
+#pragma unroll
+    for (int k = 0; k < PT; ++k) {
+      const int e = threadIdx.x + k * kScanBlock, t = e / SP, s = e % SP;
+      off[k] = t < TT && s < a.S ? (static_cast<uint32_t>(t) * a.G * a.S + s) * static_cast<uint32_t>(sizeof(T)) : kNowhere;
+    }
+  }
+  __device__ __forceinline__ void fetch(const ScanBwdK<T>& a, const ScanPlace& p, int t) {
+    const int n = max(0, min(TT, p.t1 - p.t0 - t));
+    const int64_t at = ((static_cast<int64_t>(p.b) * a.T_ + p.t0 + t) * a.G + p.g) * a.S;
+    const int64_t bytes = n ? (static_cast<int64_t>(n - 1) * a.G * a.S + a.S) * sizeof(T) : 0;
+    const Range<T> B(a.Bm + at, bytes), C(a.Cm + at, bytes);
+#pragma unroll
+    for (int k = 0; k < PT; ++k) {
+      rb[k] = B.load(off[k]);
+      rc[k] = C.load(off[k]);
+    }
+  }
+  // [token][quad lane][NPL of B, NPL of C]
+  template <int NPL> __device__ __forceinline__ void put(float (*bc)[4][2 * NPL]) const {
+#pragma unroll
+    for (int k = 0; k < PT; ++k) {
+      const int e = threadIdx.x + k * kScanBlock, t = e / SP, s = e % SP;
+      if (PT * kScanBlock == TT * SP || t < TT) {
+        bc[t][s / NPL][s % NPL] = Range<T>::value(rb[k]);
+        bc[t][s / NPL][NPL + s % NPL] = Range<T>::value(rc[k]);
+      }
+    }
+  }
+};
+
 template <typename T, int NPL>
 __global__ __launch_bounds__(kScanBlock) void scan_bwd_ends_kernel(ScanBwdK<T> a) {
   constexpr int SP = 4 * NPL, L = BwdTile<NPL>::L, TT = BwdTile<NPL>::CT;
-  __shared__ __align__(16) float bc[L][4][2 * NPL];
+  __shared__ __align__(16) float bc[2][TT][4][2 * NPL];
   __shared__ __align__(16) f32x4 st[2][TT][kScanChannels];  // step size, input, gradient of y
   __shared__ float tot[4][kScanChannels];
   const int tid = threadIdx.x, lane = tid & 63, q = lane & 3;
@@ -206,8 +228,10 @@ __global__ __launch_bounds__(kScanBlock) void scan_bwd_ends_kernel(ScanBwdK<T> a
   if (!p.ok) return;
   Piece<T, TT> pc;
   pc.place(a, p);
+  PieceBC<T, TT, SP> pb;
+  pb.place(a);
   pc.template fetch<true>(a, p, 0);
-  stage_bc<T, NPL, L>(a, p, bc);
+  pb.fetch(a, p, 0);
   const int in = tid / 4;
   const bool live = in < p.cl;
   const int c = p.c0 + (live ? in : p.cl - 1);
@@ -229,12 +253,14 @@ __global__ __launch_bounds__(kScanBlock) void scan_bwd_ends_kernel(ScanBwdK<T> a
       dtot += d;
       st[buf][pc.tk + 4 * j][pc.ch] = f32x4{d, d * Range<T>::value(pc.rx[j]), g, 0.f};
     }
+    pb.template put<NPL>(bc[buf]);
     pc.template fetch<true>(a, p, t + TT);
+    pb.fetch(a, p, t + TT);
     __syncthreads();  // the other buffer is written only behind the next one
 #pragma unroll
     for (int k = 0; k < TT; ++k) {
       const f32x4 e4 = st[buf][k][in];
-      const float* r = bc[t + k][q];
+      const float* r = bc[buf][k][q];
 #pragma unroll
       for (int i = 0; i < NPL; ++i) {
         const float e = __builtin_amdgcn_exp2f(e4[0] * A2[i]);
@@ -309,8 +335,9 @@ __global__ __launch_bounds__(kScanBlock) void scan_bwd_carry_kernel(
 template <typename T, int NPL>
 __global__ __launch_bounds__(kScanBlock) void scan_bwd_kernel(ScanBwdK<T> a) {
   constexpr int SP = 4 * NPL, CT = BwdTile<NPL>::CT, NSUB = BwdTile<NPL>::NSUB, L = BwdTile<NPL>::L;
-  constexpr int NV = 2 * NPL, LEFT = NV >= 16 ? NV / 16 : 1;
-  __shared__ __align__(16) float bc[L][4][NV];
+  constexpr int NV = 2 * NPL;
+  constexpr int LEFT = NV >= 16 ? NV / 16 : 1;
+  __shared__ __align__(16) float bc[2][CT][4][NV];              // two pieces, then one
   __shared__ __align__(16) float held[NSUB][kScanBlock][NPL];   // states at the start of every piece
   __shared__ __align__(16) float red[4][CT][4][NV];             // dB, dC of a piece, per wavefront
   // Per (token, channel) of a piece: step size, input, gradient of y. The channel's quad replaces
@@ -334,8 +361,10 @@ __global__ __launch_bounds__(kScanBlock) void scan_bwd_kernel(ScanBwdK<T> a) {
   }
   Piece<T, CT> pc;
   pc.place(a, p);
+  PieceBC<T, CT, SP> pb;
+  pb.place(a);
   pc.template fetch<false>(a, p, 0);
-  stage_bc<T, NPL, L>(a, p, bc);
+  pb.fetch(a, p, 0);
   float A2[NPL], h[NPL], gc[NPL], dA[NPL];  // gc: gradient that reaches the state before token t + 1
 #pragma unroll
   for (int i = 0; i < NPL; ++i) {
@@ -362,12 +391,14 @@ __global__ __launch_bounds__(kScanBlock) void scan_bwd_kernel(ScanBwdK<T> a) {
       const float d = pc.step(a, p, k * CT, j);
       sd[k & 1][pc.tk + 4 * j][pc.ch] = f32x2{d, d * Range<T>::value(pc.rx[j])};
     }
+    pb.template put<NPL>(bc[k & 1]);
     pc.template fetch<false>(a, p, (k + 1) * CT);
+    pb.fetch(a, p, (k + 1) * CT);
     __syncthreads();
 #pragma unroll
     for (int t = 0; t < CT; ++t) {
       const f32x2 e2 = sd[k & 1][t][in];
-      const float* r = bc[k * CT + t][q];
+      const float* r = bc[k & 1][t][q];
 #pragma unroll
       for (int i = 0; i < NPL; ++i) h[i] = fmaf(__builtin_amdgcn_exp2f(e2[0] * A2[i]), h[i], e2[1] * r[i]);
       if (t % 4 == 3)
@@ -379,8 +410,10 @@ __global__ __launch_bounds__(kScanBlock) void scan_bwd_kernel(ScanBwdK<T> a) {
   const int vat = channel_sum_index<NV>(lane), cbg = cb - p.g * per;
   const int64_t rows = static_cast<int64_t>(a.cu ? 1 : a.N) * a.T_;
   pc.template fetch<true>(a, p, max(nsub - 1, 0) * CT);
+  pb.fetch(a, p, max(nsub - 1, 0) * CT);
   for (int k = nsub - 1; k >= 0; --k) {
     __syncthreads();  // everything of the piece before is read
+    pb.template put<NPL>(bc[0]);
     float xv[pc.R], uv[pc.R], zv[pc.R], yv[pc.R], dl[pc.R], dyp[pc.R], gz[pc.R];
 #pragma unroll
     for (int j = 0; j < pc.R; ++j) {
@@ -392,7 +425,10 @@ __global__ __launch_bounds__(kScanBlock) void scan_bwd_kernel(ScanBwdK<T> a) {
       dyp[j] = pc.grad(a, j, gz[j]);
       st[pc.tk + 4 * j][pc.ch] = f32x4{dl[j], dl[j] * xv[j], dyp[j], 0.f};
     }
-    if (k > 0) pc.template fetch<true>(a, p, (k - 1) * CT);
+    if (k > 0) {
+      pc.template fetch<true>(a, p, (k - 1) * CT);
+      pb.fetch(a, p, (k - 1) * CT);
+    }
 #pragma unroll
     for (int i = 0; i < NPL; ++i) h[i] = held[k][tid][i];
     __syncthreads();
@@ -403,7 +439,7 @@ __global__ __launch_bounds__(kScanBlock) void scan_bwd_kernel(ScanBwdK<T> a) {
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         const f32x4 e4 = st[4 * j + t][in];
-        const float* r = bc[k * CT + 4 * j + t][q];
+        const float* r = bc[0][4 * j + t][q];
         float y = 0.f;
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
@@ -427,7 +463,7 @@ __global__ __launch_bounds__(kScanBlock) void scan_bwd_kernel(ScanBwdK<T> a) {
 #pragma unroll
       for (int t = 3; t >= 0; --t) {
         const f32x4 e4 = st[4 * j + t][in];
-        const float* r = bc[k * CT + 4 * j + t][q];
+        const float* r = bc[0][4 * j + t][q];
         float v[NV], b = 0.f, d = 0.f;
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
