@@ -532,8 +532,8 @@ def _sequences(B: int, T: int, cu_seqlens: Optional[torch.Tensor], index: int) -
     if cu_seqlens is None:
         return B
     _require(cu_seqlens, "cu_seqlens", torch.int32)
-    if cu_seqlens.dim() != 1:
-        raise ValueError("cu_seqlens must have one dimension")
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError(f"cu_seqlens must be [N + 1] for N >= 1 sequences (got {tuple(cu_seqlens.shape)})")
     _need(cu_seqlens, "cu_seqlens", torch.int32, cu_seqlens.shape, index)
     if DEBUG_CHECKS:
         none = torch.empty((1,), dtype=torch.float32, device=cu_seqlens.device)
@@ -641,6 +641,8 @@ def _step_state(x, initial_state, final_state, in_place, output_final_state, sha
     if in_place:
         if initial_state is None:
             raise ValueError("in_place requires initial_state")
+        if final_state is not None and final_state is not initial_state:
+            raise ValueError("in_place updates initial_state: final_state must not be given")
         return initial_state
     if final_state is None and output_final_state:
         return x.new_empty(shape, dtype=dtype)

@@ -106,6 +106,7 @@ ScanPlan scan_bwd_plan(int64_t B, int64_t T, int64_t N, int S, bool packed);
 int scan_padded_states(int S);           // states per channel in the workspaces
 int64_t scan_channel_blocks(int64_t D, int64_t G);      // workgroups per slot
 int64_t scan_bwd_channel_blocks(int64_t D, int64_t G);
+int64_t scan_step_blocks(int64_t N, int64_t D, int64_t G);  // workgroups of the step
 
 struct ScanBwdArgs {
   ScanArgs f;                 // the forward's inputs; y and fin unused

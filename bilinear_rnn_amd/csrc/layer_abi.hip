@@ -2,6 +2,7 @@
 // workspace carving and launches on the caller's stream.
 #include <climits>
 #include <cmath>
+#include <initializer_list>
 
 #include "comba.h"
 #include "layer.h"
@@ -14,6 +15,11 @@ using comba::report;
 using comba::report_launch;
 
 constexpr int32_t kMaxWidth = 1 << 22;
+// The kernels step through tokens in tiles with 32-bit counters, which run past the last token by
+// less than two tiles.
+constexpr int64_t kMaxTokens = INT_MAX - 0xffff;
+constexpr int64_t kMaxThreads = UINT_MAX;               // of one launch
+constexpr int64_t kMaxBlocks = kMaxThreads / 256 - 8;   // workgroups of 256, their number rounded up to 8
 
 size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
@@ -38,7 +44,7 @@ int32_t check_batch(const int32_t* cu, int32_t num_seqs, int32_t B, int32_t T, i
     return report(COMBA_ERR_INVALID_ARG, "T must be >= 1 without cu_seqlens");
   }
   N = cu ? num_seqs : B;
-  if (static_cast<int64_t>(B) * T > INT_MAX) return report(COMBA_ERR_UNSUPPORTED, "more than 2^31 - 1 tokens");
+  if (static_cast<int64_t>(B) * T > kMaxTokens) return report(COMBA_ERR_UNSUPPORTED, "more than 2^31 - 2^16 tokens");
   return COMBA_OK;
 }
 
@@ -46,6 +52,22 @@ int32_t check_workspace(const void* ws, size_t have, size_t need, const char* wh
   if (need == 0) return COMBA_OK;
   if (!ws || have < need) return report(COMBA_ERR_WORKSPACE, what);
   if (misaligned(ws, 256)) return report(COMBA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  return COMBA_OK;
+}
+
+struct Span {  // a tensor, or nothing
+  const void* p;
+  int64_t bytes;
+};
+
+// Outputs lie apart from the inputs and from each other.
+int32_t check_apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  for (auto o = outs.begin(); o != outs.end(); ++o) {
+    for (const Span& i : ins)
+      if (overlaps(o->p, o->bytes, i.p, i.bytes)) return report(COMBA_ERR_INVALID_ARG, "an output overlaps an input");
+    for (auto u = o + 1; u != outs.end(); ++u)
+      if (overlaps(o->p, o->bytes, u->p, u->bytes)) return report(COMBA_ERR_INVALID_ARG, "two outputs overlap");
+  }
   return COMBA_OK;
 }
 
@@ -83,6 +105,11 @@ COMBA_API int32_t comba_short_conv_fwd(const void* x, const float* weight, const
   const int64_t state = N * (W - 1) * D * size_of(dtype);
   if (overlaps(initial_state, state, final_state, state))
     return report(COMBA_ERR_INVALID_ARG, "final_state overlaps initial_state (only the single-token form works in place)");
+  const int64_t act = static_cast<int64_t>(B) * T * D * size_of(dtype);
+  rc = check_apart({{y, act}, {final_state, state}},
+                   {{x, act}, {weight, 4ll * D * W}, {bias, 4ll * D}, {initial_state, state},
+                    {cu_seqlens, 4 * (N + 1)}});
+  if (rc != COMBA_OK) return rc;
   const comba::ConvArgs a{x, weight, bias, initial_state, cu_seqlens, static_cast<int>(N), B, T, D, W, dtype,
                           silu != 0, y, final_state};
   return report_launch(comba::launch_conv(a, static_cast<hipStream_t>(stream)));
@@ -100,6 +127,10 @@ COMBA_API int32_t comba_short_conv_step(const void* x, const float* weight, cons
   const int64_t state = static_cast<int64_t>(N) * (W - 1) * D * size_of(dtype);
   if (initial_state != final_state && overlaps(initial_state, state, final_state, state))
     return report(COMBA_ERR_INVALID_ARG, "final_state partially overlaps initial_state");
+  const Span in{x, static_cast<int64_t>(N) * D * size_of(dtype)}, w{weight, 4ll * D * W}, b{bias, 4ll * D};
+  if ((rc = check_apart({{y, in.bytes}}, {in, w, b, {initial_state, state}, {final_state, state}})) != COMBA_OK ||
+      (rc = check_apart({{final_state, state}}, {in, w, b})) != COMBA_OK)
+    return rc;
   const comba::ConvArgs a{x, weight, bias, initial_state, nullptr, N, N, 1, D, W, dtype, silu != 0, y, final_state};
   return report_launch(comba::launch_conv_step(a, static_cast<hipStream_t>(stream)));
 }
@@ -123,9 +154,16 @@ COMBA_API int32_t comba_short_conv_bwd(const void* x, const float* weight, const
   int64_t N = 0;
   if ((rc = check_batch(cu_seqlens, num_seqs, B, T, N)) != COMBA_OK) return rc;
   if ((rc = check_conv_items(B, T, D, N, cu_seqlens != nullptr)) != COMBA_OK) return rc;
-  rc = check_workspace(workspace, workspace_bytes,
-                       comba_short_conv_bwd_workspace_size(B, T, D, W, cu_seqlens ? num_seqs : 0),
+  const size_t need = comba_short_conv_bwd_workspace_size(B, T, D, W, cu_seqlens ? num_seqs : 0);
+  rc = check_workspace(workspace, workspace_bytes, need,
                        "workspace is NULL or smaller than comba_short_conv_bwd_workspace_size()");
+  if (rc != COMBA_OK) return rc;
+  const int64_t elems = static_cast<int64_t>(B) * T * D, act = elems * size_of(dtype);
+  const int64_t state = N * (W - 1) * D * size_of(dtype);
+  rc = check_apart({{dx, act}, {dweight, 4ll * D * W}, {dbias, 4ll * D}, {d_initial_state, state},
+                    {workspace, static_cast<int64_t>(need)}},
+                   {{x, act}, {weight, 4ll * D * W}, {bias, 4ll * D}, {initial_state, state},
+                    {cu_seqlens, 4 * (N + 1)}, {dy, elems * size_of(dy_dtype)}, {d_final_state, state}});
   if (rc != COMBA_OK) return rc;
   const comba::ConvBwdArgs a{{x, weight, bias, initial_state, cu_seqlens, static_cast<int>(N), B, T, D, W, dtype,
                               silu != 0, nullptr, nullptr},
@@ -146,11 +184,14 @@ int32_t check_scan(const void* x, const void* dt, const float* A, const void* Bm
   if (G < 1 || D % G != 0) return report(COMBA_ERR_INVALID_ARG, "G must be >= 1 and divide D");
   if (S > comba::kScanMaxStates) return report(COMBA_ERR_UNSUPPORTED, "more than 64 states per channel");
   if (D > kMaxWidth) return report(COMBA_ERR_UNSUPPORTED, "D above 2^22");
+  if (static_cast<int64_t>(G) * S > 1 << 23)  // a tile of B or C is addressed with 32-bit offsets
+    return report(COMBA_ERR_UNSUPPORTED, "G * S above 2^23");
   return COMBA_OK;
 }
 
-int32_t check_scan_grid(int64_t slots, int64_t D, int64_t G, int64_t N, int64_t SP) {
-  if (slots * comba::scan_channel_blocks(D, G) > INT_MAX || (N * D * SP) / 256 > INT_MAX)
+// `carried`: the states that a launch with a thread each carries across segments.
+int32_t check_scan_grid(int64_t slots, int64_t blocks, int64_t carried) {
+  if (slots * blocks > kMaxBlocks || carried > kMaxThreads - 255)
     return report(COMBA_ERR_UNSUPPORTED, "too many (segment, channel) pairs for one launch");
   return COMBA_OK;
 }
@@ -189,7 +230,7 @@ ScanBwdWorkspace scan_bwd_workspace(const comba::ScanPlan& p, int64_t rows, int6
 
 bool scan_sizes_ok(int32_t B, int32_t T, int32_t D, int32_t S, int32_t G) {
   return B >= 1 && T >= 0 && D >= 1 && D <= kMaxWidth && S >= 1 && S <= comba::kScanMaxStates && G >= 1 &&
-         D % G == 0 && static_cast<int64_t>(B) * T <= INT_MAX;
+         D % G == 0 && static_cast<int64_t>(B) * T <= kMaxTokens;
 }
 
 }  // namespace
@@ -215,11 +256,19 @@ COMBA_API int32_t comba_selective_scan_fwd(const void* x, const void* dt, const 
   if ((rc = check_states(initial_state, final_state, N * D * S * 4)) != COMBA_OK) return rc;
   const int64_t SP = comba::scan_padded_states(S);
   const comba::ScanPlan p = comba::scan_plan(B, T, D, G, N, cu_seqlens != nullptr);
-  if ((rc = check_scan_grid(p.slots, D, G, N, SP)) != COMBA_OK) return rc;
+  if ((rc = check_scan_grid(p.slots, comba::scan_channel_blocks(D, G), p.L ? N * D * SP : 0)) != COMBA_OK) return rc;
   const ScanWorkspace w = scan_workspace(p, D, SP);
   rc = check_workspace(workspace, workspace_bytes, w.total,
                        "workspace is NULL or smaller than comba_selective_scan_workspace_size()");
   if (rc != COMBA_OK) return rc;
+  const int64_t rows = static_cast<int64_t>(B) * T, act = rows * D * size_of(dtype);
+  const int64_t bc = rows * G * S * size_of(dtype), state = N * D * S * 4;
+  const Span sx{x, act}, sd{dt, act}, sA{A, 4ll * D * S}, sB{Bm, bc}, sC{Cm, bc}, ss{skip, 4ll * D}, sz{z, act},
+      sb{dt_bias, 4ll * D}, sc{cu_seqlens, 4 * (N + 1)}, sw{workspace, static_cast<int64_t>(w.total)};
+  if ((rc = check_apart({{y, act}, sw}, {sx, sd, sA, sB, sC, ss, sz, sb, sc, {initial_state, state},
+                                         {final_state, state}})) != COMBA_OK ||
+      (rc = check_apart({{final_state, state}}, {sx, sd, sA, sB, sC, ss, sz, sb, sc})) != COMBA_OK)
+    return rc;
   char* ws = static_cast<char*>(workspace);
   const comba::ScanArgs a{x, dt, A, Bm, Cm, skip, z, dt_bias, softplus != 0, initial_state, cu_seqlens,
                           static_cast<int>(N), B, T, D, S, G, dtype, y, final_state};
@@ -237,7 +286,15 @@ COMBA_API int32_t comba_selective_step(const void* x, const void* dt, const floa
   if (!y) return report(COMBA_ERR_INVALID_ARG, "y must be non-NULL");
   if (N < 1) return report(COMBA_ERR_INVALID_ARG, "N must be >= 1");
   if ((rc = check_states(initial_state, final_state, static_cast<int64_t>(N) * D * S * 4)) != COMBA_OK) return rc;
-  if ((rc = check_scan_grid(N, D, G, N, comba::scan_padded_states(S))) != COMBA_OK) return rc;
+  if ((rc = check_scan_grid(comba::scan_step_blocks(N, D, G), 1, 0)) != COMBA_OK) return rc;
+  const int64_t act = static_cast<int64_t>(N) * D * size_of(dtype), state = static_cast<int64_t>(N) * D * S * 4;
+  const int64_t bc = static_cast<int64_t>(N) * G * S * size_of(dtype);
+  const Span sx{x, act}, sd{dt, act}, sA{A, 4ll * D * S}, sB{Bm, bc}, sC{Cm, bc}, ss{skip, 4ll * D}, sz{z, act},
+      sb{dt_bias, 4ll * D};
+  if ((rc = check_apart({{y, act}}, {sx, sd, sA, sB, sC, ss, sz, sb, {initial_state, state}, {final_state, state}})) !=
+          COMBA_OK ||
+      (rc = check_apart({{final_state, state}}, {sx, sd, sA, sB, sC, ss, sz, sb})) != COMBA_OK)
+    return rc;
   const comba::ScanArgs a{x, dt, A, Bm, Cm, skip, z, dt_bias, softplus != 0, initial_state, nullptr, N, N, 1, D, S, G,
                           dtype, y, final_state};
   return report_launch(comba::launch_scan_step(a, static_cast<hipStream_t>(stream)));
@@ -267,12 +324,19 @@ COMBA_API int32_t comba_selective_scan_bwd(const void* x, const void* dt, const 
   if ((rc = check_batch(cu_seqlens, num_seqs, B, T, N)) != COMBA_OK) return rc;
   const int64_t SP = comba::scan_padded_states(S), rows = static_cast<int64_t>(B) * T;
   const comba::ScanPlan p = comba::scan_bwd_plan(B, T, N, S, cu_seqlens != nullptr);
-  if ((rc = check_scan_grid(p.slots, D, G, N, SP)) != COMBA_OK) return rc;
-  if (rows * G * 2 * SP / 256 > INT_MAX || D * SP > INT_MAX)
+  if ((rc = check_scan_grid(p.slots, comba::scan_bwd_channel_blocks(D, G), N * D * SP)) != COMBA_OK) return rc;
+  if (rows * G * 2 * SP > kMaxThreads - 255 || D * SP > kMaxThreads / 16 - 64)  // column sums: 16 threads each
     return report(COMBA_ERR_UNSUPPORTED, "too many (token, group, state) triples for one launch");
   const ScanBwdWorkspace w = scan_bwd_workspace(p, rows, D, SP, G);
   rc = check_workspace(workspace, workspace_bytes, w.total,
                        "workspace is NULL or smaller than comba_selective_scan_bwd_workspace_size()");
+  if (rc != COMBA_OK) return rc;
+  const int64_t act = rows * D * size_of(dtype), bc = rows * G * S * size_of(dtype), state = N * D * S * 4;
+  rc = check_apart({{dx, act}, {ddt, act}, {dA, 4ll * D * S}, {dBm, bc}, {dCm, bc}, {dskip, 4ll * D}, {dz, act},
+                    {ddt_bias, 4ll * D}, {d_initial_state, state}, {workspace, static_cast<int64_t>(w.total)}},
+                   {{x, act}, {dt, act}, {A, 4ll * D * S}, {Bm, bc}, {Cm, bc}, {skip, 4ll * D}, {z, act},
+                    {dt_bias, 4ll * D}, {initial_state, state}, {cu_seqlens, 4 * (N + 1)}, {dy, act},
+                    {d_final_state, state}});
   if (rc != COMBA_OK) return rc;
   char* ws = static_cast<char*>(workspace);
   auto at = [&](size_t o) { return reinterpret_cast<float*>(ws + o); };
@@ -310,6 +374,10 @@ COMBA_API int32_t comba_block_norm_fwd(const void* y, const void* gate, const vo
   if (!r) return report(COMBA_ERR_INVALID_ARG, "r must be non-NULL");
   if ((n == nullptr) != (pre_weight == nullptr))
     return report(COMBA_ERR_INVALID_ARG, "n is given exactly when pre_weight is");
+  const int64_t act = rows * D * size_of(dtype), par = 4ll * D;
+  const int32_t apart = check_apart({{r, act}, {n, act}}, {{y, act}, {gate, act}, {residual, act}, {scale, par},
+                                                           {post_weight, par}, {pre_weight, par}});
+  if (apart != COMBA_OK) return apart;
   const comba::NormArgs a{y, gate, residual, scale, post_weight, pre_weight, rows, D, dtype, eps, r, n};
   return report_launch(comba::launch_norm(a, static_cast<hipStream_t>(stream)));
 }
@@ -333,8 +401,15 @@ COMBA_API int32_t comba_block_norm_bwd(const void* y, const void* gate, const vo
       (scale == nullptr) != (dscale == nullptr) || (post_weight == nullptr) != (dpost_weight == nullptr) ||
       (pre_weight == nullptr) != (dpre_weight == nullptr))
     return report(COMBA_ERR_INVALID_ARG, "a gradient is given exactly when its input is");
-  rc = check_workspace(workspace, workspace_bytes, comba_block_norm_bwd_workspace_size(rows, D),
+  const size_t need = comba_block_norm_bwd_workspace_size(rows, D);
+  rc = check_workspace(workspace, workspace_bytes, need,
                        "workspace is NULL or smaller than comba_block_norm_bwd_workspace_size()");
+  if (rc != COMBA_OK) return rc;
+  const int64_t act = rows * D * size_of(dtype), par = 4ll * D;
+  rc = check_apart({{dy, act}, {dgate, act}, {dresidual, act}, {dscale, par}, {dpost_weight, par}, {dpre_weight, par},
+                    {workspace, static_cast<int64_t>(need)}},
+                   {{y, act}, {gate, act}, {residual, act}, {scale, par}, {post_weight, par}, {pre_weight, par},
+                    {dr, act}, {dn, act}});
   if (rc != COMBA_OK) return rc;
   const comba::NormBwdArgs a{{y, gate, residual, scale, post_weight, pre_weight, rows, D, dtype, eps, nullptr, nullptr},
                              dr, dn, dy, dgate, dresidual, dscale, dpost_weight, dpre_weight,

@@ -66,6 +66,13 @@ __device__ __forceinline__ float softplus_f32(float u) {
   return fmaf(s, p, fmaxf(u, 0.f));
 }
 
+// A for the base-2 exponential, kept finite: a step size of 0 (tokens behind a segment have it) leaves
+// the state as it is also where A is -infinity, which forgets it at every other token.
+__device__ __forceinline__ float decay_rate(float A) {
+  const float r = A * kLog2E;
+  return r < -3.4028235e38f ? -3.4028235e38f : r;
+}
+
 // A workgroup's place: segment [t0, t1) of sequence n in batch row b, channels from c0 on.
 struct ScanPlace {
   int n, b, seg, t0, t1, s0, s1;   // s0, s1: the whole sequence

@@ -98,7 +98,7 @@ __global__ __launch_bounds__(kFwdChannels* kFwdLanes) void scan_fwd_kernel(ScanK
   load_states<NPL>(a.A + static_cast<int64_t>(c) * a.S, q * NPL, a.S, A2);
 #pragma unroll
   for (int i = 0; i < NPL; ++i) {
-    A2[i] *= kLog2E;
+    A2[i] = decay_rate(A2[i]);
     h[i] = 0.f;
   }
   if (!STATE) {
@@ -279,7 +279,7 @@ __global__ __launch_bounds__(kScanBlock) void scan_carry_kernel(const float* __r
   const int segs = segments_of(s1 - s0, L);
   const int64_t slot0 = cu ? static_cast<int64_t>(s0 / L) + n : static_cast<int64_t>(n) * ((T + L - 1) / L);
   const bool real = s < S;
-  const float A2 = real ? A[c * S + s] * kLog2E : 0.f;
+  const float A2 = real ? decay_rate(A[c * S + s]) : 0.f;
   float h = real && init ? init[(n * D + c) * S + s] : 0.f;
   float* hp = hseg + (slot0 * D + c) * SP + s;
   const float* dp = dsum + slot0 * D + c;
@@ -316,7 +316,7 @@ __global__ __launch_bounds__(kScanBlock) void scan_step_kernel(
   float A2[NPL];
   load_states<NPL>(A + static_cast<int64_t>(c) * S, s0, S, A2);
 #pragma unroll
-  for (int i = 0; i < NPL; ++i) A2[i] *= kLog2E;
+  for (int i = 0; i < NPL; ++i) A2[i] = decay_rate(A2[i]);
   const float bias = dt_bias ? dt_bias[c] : 0.f, sk = skip ? skip[c] : 0.f;
   const int64_t first = static_cast<int64_t>(blockIdx.x / cblocks) * per;
   constexpr int U = 2;  // sequences whose loads are in flight together
@@ -433,13 +433,25 @@ static hipError_t scan_t(const ScanArgs& a, const ScanPlan& p, float* hseg, floa
   return hipGetLastError();
 }
 
+static int64_t scan_step_channel_blocks(int64_t D, int64_t G) {
+  return G * ((D / G + kScanChannels - 1) / kScanChannels);
+}
+
+// Sequences per workgroup: up to 8 while eight workgroups per compute unit remain.
+static int64_t scan_step_per(int64_t N, int64_t cb) {
+  const int64_t per = N * cb / 2048;
+  return per < 1 ? 1 : (per > 8 ? 8 : per);
+}
+
+int64_t scan_step_blocks(int64_t N, int64_t D, int64_t G) {
+  const int64_t cb = scan_step_channel_blocks(D, G), per = scan_step_per(N, cb);
+  return (N + per - 1) / per * cb;
+}
+
 template <typename T, int NPL>
 static hipError_t scan_step_t(const ScanArgs& a, hipStream_t st) {
-  const int64_t cb = a.G * ((a.D / a.G + kScanChannels - 1) / kScanChannels);
-  // sequences per workgroup: up to 8 while eight workgroups per compute unit remain
-  int64_t per = a.N * cb / 2048;
-  per = per < 1 ? 1 : (per > 8 ? 8 : per);
-  const unsigned grid = static_cast<unsigned>((a.N + per - 1) / per * cb);
+  const int64_t per = scan_step_per(a.N, scan_step_channel_blocks(a.D, a.G));
+  const unsigned grid = static_cast<unsigned>(scan_step_blocks(a.N, a.D, a.G));
   auto run = [&](auto v) {
     scan_step_kernel<T, NPL, decltype(v)::value><<<grid, kScanBlock, 0, st>>>(
         static_cast<const T*>(a.x), static_cast<const T*>(a.dt), a.A, static_cast<const T*>(a.Bm),

@@ -239,7 +239,7 @@ __global__ __launch_bounds__(kScanBlock) void scan_bwd_ends_kernel(ScanBwdK<T> a
 #pragma unroll
   for (int i = 0; i < NPL; ++i) {
     const int s = q * NPL + i;
-    A2[i] = s < a.S ? a.A[static_cast<int64_t>(c) * a.S + s] * kLog2E : 0.f;
+    A2[i] = s < a.S ? decay_rate(a.A[static_cast<int64_t>(c) * a.S + s]) : 0.f;
     h[i] = gs[i] = 0.f;
     pr[i] = 1.f;
   }
@@ -307,7 +307,7 @@ __global__ __launch_bounds__(kScanBlock) void scan_bwd_carry_kernel(
   const int segs = segments_of(s1 - s0, L);
   const int64_t slot0 = cu ? static_cast<int64_t>(s0 / L) + n : static_cast<int64_t>(n) * ((T + L - 1) / L);
   const bool real = s < S;
-  const float A2 = real ? A[c * S + s] * kLog2E : 0.f;
+  const float A2 = real ? decay_rate(A[c * S + s]) : 0.f;
   const float* from = back ? dfin : init;
   float h = real && from ? from[(n * D + c) * S + s] : 0.f;
   float* hp = (back ? gseg : hseg) + (slot0 * D + c) * SP + s;
@@ -369,7 +369,7 @@ __global__ __launch_bounds__(kScanBlock) void scan_bwd_kernel(ScanBwdK<T> a) {
 #pragma unroll
   for (int i = 0; i < NPL; ++i) {
     const int s = q * NPL + i;
-    A2[i] = s < a.S ? a.A[static_cast<int64_t>(c) * a.S + s] * kLog2E : 0.f;
+    A2[i] = s < a.S ? decay_rate(a.A[static_cast<int64_t>(c) * a.S + s]) : 0.f;
     h[i] = live ? a.hseg[at + i] : 0.f;
     gc[i] = live ? a.gseg[at + i] : 0.f;
     dA[i] = 0.f;

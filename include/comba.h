@@ -445,8 +445,8 @@ int32_t comba_lds_probe(int32_t kind, const int32_t* lane_offsets, int32_t iters
  * - With cu_seqlens, tokens before cu_seqlens[0] or from cu_seqlens[N] on
  *   belong to no sequence: they are not read, and their rows of an output are
  *   left as they were.
- * - Outputs must not overlap inputs or each other, except where a state may be
- *   updated in place as stated.
+ * - Outputs and the workspace must not overlap inputs or each other, except
+ *   where a state may be updated in place as stated (COMBA_ERR_INVALID_ARG).
  * COMBA_ABI_VERSION stays while existing entry points keep their signature
  * and meaning; a caller that needs an added one looks it up by name.
  */
@@ -476,7 +476,7 @@ int32_t comba_lds_probe(int32_t kind, const int32_t* lane_offsets, int32_t iters
  * (num_seqs is N with cu_seqlens and 0 without), 256-byte aligned, and gives
  * the same bits on every run.
  * Errors: COMBA_ERR_UNSUPPORTED for other W, and for tensors of more than 2^31
- * (token tile, channel) pairs or 2^31 - 1 tokens.
+ * (token tile, channel) pairs or 2^31 - 2^16 tokens.
  */
 int32_t comba_short_conv_fwd(const void* x, const float* weight, const float* bias, const void* initial_state,
                              const int32_t* cu_seqlens, int32_t num_seqs, int32_t B, int32_t T, int32_t D, int32_t W,
@@ -502,7 +502,9 @@ int32_t comba_short_conv_bwd(const void* x, const float* weight, const float* bi
  *     h_t[s] = exp(d_t A[c, s]) h_{t-1}[s] + d_t x_t Bm_t[g, s]
  *     y_t    = (sum_s Cm_t[g, s] h_t[s] + skip x_t) * z_t sigmoid(z_t)
  *   x, dt, z, y    [B, T, D]        dtype; z may be NULL (no gate)
- *   A              [D, S]           float32 (negative for a decay; not checked)
+ *   A              [D, S]           float32 (negative for a decay; not checked.
+ *                                   -infinity keeps nothing of the state, but
+ *                                   all of it where d is 0)
  *   Bm, Cm         [B, T, G, S]     dtype; G divides D
  *   skip, dt_bias  [D]              float32, either may be NULL (0)
  *   initial_state  [N, D, S]        float32, or NULL for zeros
@@ -522,8 +524,8 @@ int32_t comba_short_conv_bwd(const void* x, const float* weight, const float* bi
  *   d_initial_state [N, D, S] float32 (each may be NULL: not written).
  * It needs comba_selective_scan_bwd_workspace_size(...) bytes, 256-byte
  * aligned, and gives the same bits on every run.
- * Errors: COMBA_ERR_UNSUPPORTED for S > 64, D > 2^22, more than 2^31 - 1
- * tokens or workgroups.
+ * Errors: COMBA_ERR_UNSUPPORTED for S > 64, D > 2^22, G S > 2^23, more than
+ * 2^31 - 2^16 tokens, and for launches of more than 2^32 - 1 threads.
  */
 size_t comba_selective_scan_workspace_size(int32_t B, int32_t T, int32_t D, int32_t S, int32_t G, int32_t num_seqs);
 

@@ -251,6 +251,23 @@ def test_refusals_of_the_binding():
         comba.block_norm(x, post_weight=p["a"], out_norm=x)
 
 
+def test_calls_that_would_overwrite_their_inputs_are_refused():
+    p, a = make_layer(12), activations(1, 8, 13)
+    x, w = a["x"], p["wv"]
+    with pytest.raises(comba.CombaError, match="an output overlaps an input"):
+        comba.short_conv(x, w, out=x)
+    with pytest.raises(comba.CombaError, match="an output overlaps an input"):
+        comba.selective_scan(x, a["dt"], p["A"], a["Bm"], a["Cm"], out=a["dt"])
+    with pytest.raises(comba.CombaError, match="an output overlaps an input"):
+        comba.block_norm(x, post_weight=p["a"], out=x)
+    s = torch.zeros((1, 3, D), dtype=BF16, device="cuda")
+    with pytest.raises(ValueError, match="final_state must not be given"):
+        comba.short_conv_step(x[:, 0].contiguous(), w, initial_state=s, in_place=True, final_state=torch.empty_like(s))
+    for cu in ([], [0]):
+        with pytest.raises(ValueError, match="N >= 1 sequences"):
+            comba.short_conv(x, w, cu_seqlens=torch.tensor(cu, dtype=torch.int32, device="cuda"))
+
+
 def test_debug_checks_cover_packed_offsets(monkeypatch):
     from bilinear_rnn_amd import api
     p, a = make_layer(13), activations(1, 20, 14)

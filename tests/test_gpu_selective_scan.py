@@ -197,3 +197,31 @@ def test_growing_states_are_allowed():
     gamma = scan_gamma(20, umax(ref)) * (1 + x)
     check("y", y, ry, my, gamma)
     check("state", f, rf, mf, gamma)
+
+
+@pytest.mark.parametrize("B,T,D,S,lens", [(2, 45, 20, 16, None), (1, 300, 66, 5, None), (1, 700, 40, 16, [3, 590, 0, 107])])
+def test_states_that_forget_at_every_token(B, T, D, S, lens):
+    """A = -infinity: the state is d x B alone, up to the last token of a sequence whose length is no
+    multiple of a tile, and an empty sequence's state passes through. The oracle has -1e30, whose
+    exponential is 0 for every step size that occurs (at least log(1 + e^-9))."""
+    on, ref = make(B, T, D, S, 1, F32, lens, seed=21)
+    gone = rnd(22).random(size=(D, S)) < 0.4
+    ref["A"][gone] = -1e30
+    on["A"] = torch.where(torch.from_numpy(gone).cuda(), -torch.inf, on["A"])
+    cu = cu_of(lens)
+    call = dict(**opts(on), cu_seqlens=cu_dev(cu))
+    y, f = comba.selective_scan(*args_of(on), **call)
+    o = oracle_args(ref, True, cu)
+    ry, rf = layer.selective_scan(*args_of(ref), **o)
+    my, mf = layer.selective_scan(*args_of(half_A(ref)), **o, magnitude=True)
+    gamma = scan_gamma(T if lens is None else max(lens), umax(ref))
+    check("y", y, ry, my, gamma)
+    check("state", f, rf, mf, gamma)
+    g = comba.selective_scan_bwd(*args_of(on), on["dy"], **call, d_final_state=on["dfin"])
+    o = dict(**o, dy=ref["dy"], dfin=ref["dfin"])
+    r = layer.selective_scan(*args_of(ref), **o)
+    m = layer.selective_scan(*args_of(half_A(ref)), **o, magnitude=True)
+    for k in r:
+        adds = D if k in ("dB", "dC") else B * T if k in ("dA", "dskip", "ddt_bias") else 0
+        check(k, g[k], r[k], m[k] * (2 if k in ("ddt", "ddt_bias") else 1),
+              scan_gamma(T if lens is None else max(lens), umax(ref), adds, ways=2))

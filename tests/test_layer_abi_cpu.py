@@ -172,3 +172,53 @@ def test_binding_refuses_host_tensors():
             call()
     with pytest.raises(TypeError):
         comba.block_norm(None)
+
+
+# Distinct addresses for the tensors of a call, far enough apart for the sizes used below.
+def apart(names):
+    return {k: (i + 1) << 32 for i, k in enumerate(names)}
+
+
+CONV_T, STEP_T = apart(("x", "w", "b", "y")), apart(("x", "w", "b", "s0", "sf", "y"))
+CONV_B = apart(("x", "w", "b", "dy", "dx", "dw", "ws"))
+SCAN_T, SCAN_S = apart(("x", "d", "A", "Bm", "C", "y")), apart(("x", "d", "A", "Bm", "C", "s0", "sf", "y"))
+SCAN_B = apart(("x", "d", "A", "Bm", "C", "dy", "dx", "dd", "dA", "dB", "dC", "ws"))
+NORM_T, NORM_B = apart(("y", "post", "pre", "r", "n")), apart(("y", "post", "pre", "dr", "dn", "dy", "dpost", "dpre", "ws"))
+
+
+@pytest.mark.parametrize("fn,base,kw", [
+    (conv, CONV_T, dict(y=CONV_T["x"])), (conv, CONV_T, dict(y=CONV_T["x"] + 2 * 8 * 16 * 2 - 2)),
+    (conv, CONV_T, dict(y=CONV_T["b"] + 60)), (conv, CONV_T, dict(sf=CONV_T["x"])), (conv, CONV_T, dict(sf=CONV_T["y"])),
+    (conv_step, STEP_T, dict(y=STEP_T["x"])), (conv_step, STEP_T, dict(y=STEP_T["s0"])),
+    (conv_step, STEP_T, dict(sf=STEP_T["x"])),
+    (conv_bwd, CONV_B, dict(dx=CONV_B["dy"])), (conv_bwd, CONV_B, dict(dw=CONV_B["w"])),
+    (conv_bwd, CONV_B, dict(ws=CONV_B["x"])), (conv_bwd, CONV_B, dict(dw=CONV_B["dx"])),
+    (scan, SCAN_T, dict(y=SCAN_T["x"])), (scan, SCAN_T, dict(y=SCAN_T["d"])), (scan, SCAN_T, dict(sf=SCAN_T["A"])),
+    (scan, SCAN_T, dict(sf=SCAN_T["y"])), (scan, SCAN_T, dict(B=1, T=4096, D=64, ws=SCAN_T["C"], wsb=BIG)),
+    (scan_step, SCAN_S, dict(y=SCAN_S["x"])), (scan_step, SCAN_S, dict(y=SCAN_S["sf"])),
+    (scan_step, SCAN_S, dict(sf=SCAN_S["Bm"])),
+    (scan_bwd, SCAN_B, dict(dx=SCAN_B["x"])), (scan_bwd, SCAN_B, dict(dd=SCAN_B["dy"])),
+    (scan_bwd, SCAN_B, dict(dB=SCAN_B["dC"])), (scan_bwd, SCAN_B, dict(ws=SCAN_B["dy"])),
+    (norm, NORM_T, dict(r=NORM_T["y"])), (norm, NORM_T, dict(n=NORM_T["r"] + 4 * 64 * 2 - 16)),
+    (norm_bwd, NORM_B, dict(dy=NORM_B["dr"])), (norm_bwd, NORM_B, dict(dpost=NORM_B["dpre"])),
+], ids=lambda v: getattr(v, "__name__", "-".join(v) if isinstance(v, dict) else str(v)))
+def test_overlapping_tensors_are_refused(fn, base, kw):
+    assert fn(**{**base, **kw}) == INVALID
+    assert "overlap" in api.last_error()
+
+
+@pytest.mark.parametrize("fn,kw", [
+    # token counters of 32 bits run past the last token by less than two tiles
+    (conv, dict(B=1, T=(1 << 31) - 40, D=1)), (conv_bwd, dict(B=1, T=(1 << 31) - 40, D=1)),
+    (scan, dict(B=1, T=(1 << 31) - 40, D=1)), (scan_bwd, dict(B=1, T=(1 << 31) - 40, D=1, S=1)),
+    # a tile of B and C: 32-bit offsets
+    (scan, dict(D=1 << 20, G=1 << 20, S=16)), (scan_step, dict(D=1 << 20, G=1 << 20, S=16)),
+    (scan_bwd, dict(D=1 << 20, G=1 << 20, S=16)),
+    # a launch of 2^32 threads or more: workgroups, and threads per carried state
+    (scan, dict(cu=P, n=1 << 20, B=1, T=1 << 20, D=1 << 12)), (scan_step, dict(N=1 << 27, D=1 << 12)),
+    (scan_bwd, dict(cu=P, n=1 << 18, B=1, T=1 << 18, D=1 << 13)), (scan_bwd, dict(B=1 << 16, T=1 << 10, D=4, S=64)),
+    (scan_bwd, dict(B=1, T=128, D=1 << 22, S=64)),
+], ids=str)
+def test_sizes_past_the_kernels_counters_are_refused(fn, kw):
+    assert fn(**kw) == UNSUPPORTED
+    assert api.last_error() != ""
