@@ -1,7 +1,7 @@
 // Device code shared by the selective scan's forward and backward.
 //
-// A channel's SP states (S padded with states that stay 0) are spread over LPC neighbouring lanes, NPL
-// consecutive states each; a workgroup holds channels of one B / C group.
+// A channel's SP states (S padded with states that stay 0) are spread over LPC lanes, NPL consecutive
+// states each; a workgroup holds channels of one B / C group.
 #pragma once
 
 #include <type_traits>
@@ -34,22 +34,47 @@ __device__ __forceinline__ void each(F f) {
   }
 }
 
-// v[k] summed over the LPC lanes, for the lane's own k.
-template <int LPC>
-__device__ __forceinline__ float lane_sums(float (&v)[LPC], int lane) {
-  if constexpr (LPC >= 8) halve_dpp<2, 4>(v, lane);
+// Halves over lane bits 3 and 2: of 4 N values, the lane keeps numbers k + N (2 b3 + b2), k < N, in
+// v[0 .. N - 1], each summed over lane ^ 4, ^ 8 and ^ 12. A DPP addition that writes only some banks of
+// four lanes makes a halving two instructions per result; selecting what to keep and what to send
+// makes it three, and the compiler has no form for the other. Inside the asm: two wait states (an
+// instruction is one) between a register's write and its DPP read, before the first, between the
+// two halvings and behind the last.
+#define COMBA_BIT3(A, B)                                                      \
+  "v_add_f32_dpp " A ", " A ", " A " row_ror:8 row_mask:0xf bank_mask:0xf\n\t" \
+  "v_add_f32_dpp " A ", " B ", " B " row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+#define COMBA_BIT2(A, B, WAIT)                                                       \
+  "v_add_f32_dpp " A ", " A ", " A " row_shl:4 row_mask:0xf bank_mask:0x5\n\t" WAIT   \
+  "v_add_f32_dpp " A ", " B ", " B " row_shr:4 row_mask:0xf bank_mask:0xa\n\t"
+template <int N> __device__ __forceinline__ void halve_bits_3_2(float* v) {
+  if constexpr (N == 1) {
+    asm("s_nop 1\n\t" COMBA_BIT3("%0", "%2") COMBA_BIT3("%1", "%3") COMBA_BIT2("%0", "%1", "s_nop 0\n\t") "s_nop 1"
+        : "+v"(v[0]), "+v"(v[1])
+        : "v"(v[2]), "v"(v[3]));
+  } else {
+    static_assert(N % 2 == 0, "1 or pairs");
+#pragma unroll
+    for (int i = 0; i < N; i += 2)
+      asm("s_nop 1\n\t" COMBA_BIT3("%0", "%4") COMBA_BIT3("%1", "%5") COMBA_BIT3("%2", "%6") COMBA_BIT3("%3", "%7")
+              COMBA_BIT2("%0", "%2", "") COMBA_BIT2("%1", "%3", "") "s_nop 1"
+          : "+v"(v[i]), "+v"(v[i + 1]), "+v"(v[i + N]), "+v"(v[i + 1 + N])
+          : "v"(v[i + 2 * N]), "v"(v[i + 1 + 2 * N]), "v"(v[i + 3 * N]), "v"(v[i + 1 + 3 * N]));
+  }
+}
+#undef COMBA_BIT2
+#undef COMBA_BIT3
+
+// v[k] summed over the quad, for the lane's own k.
+__device__ __forceinline__ float quad_sums(float (&v)[4], int lane) {
   halve_dpp<1, 2>(v, lane);
   halve_dpp<0, 1>(v, lane);
   return v[0];
 }
 
-// x summed over the LPC lanes.
-template <int LPC>
-__device__ __forceinline__ float lane_total(float x) {
+// x summed over the quad.
+__device__ __forceinline__ float quad_total(float x) {
   x += dpp_flip<0>(x);
-  x += dpp_flip<1>(x);
-  if constexpr (LPC >= 8) x += dpp_flip<2>(x);
-  return x;
+  return x + dpp_flip<1>(x);
 }
 
 // log(1 + e^u), to float32's accuracy also where the result is small. With e = e^-|u| in (0, 1],

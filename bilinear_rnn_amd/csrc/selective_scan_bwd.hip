@@ -61,11 +61,13 @@ template <typename T> struct ScanBwdK {
   bool softplus;
 };
 
-// Sums v over the 16 channels of the wavefront (lane bits 2 .. 5). At lane bit 5, 4, 3, 2 a lane keeps
+// Sums v over the 16 channels of the wavefront (lane bits 2 .. 5). At lane bit 3, 2, 5, 4 a lane keeps
 // the lower half of its values if the bit is clear, the upper half if it is set, while there are two
-// or more; then all lanes add. Left: v[0 .. max(1, N/16) - 1].
+// or more; then all lanes add. Left: v[0 .. max(1, N/16) - 1]. The most values go through bits 3 and
+// 2: 8 cycles a result there, 13 with a swap (4 x 2048 x 2048 x 16, all kernels: 373 -> 357 us).
 template <int N>
-__device__ __forceinline__ void channel_sums(float* v, int lane) {
+__device__ __forceinline__ void channel_sums(float* v) {
+  static_assert(N >= 4, "two states per lane at the least");
   auto swap_add = [](float u, float w, auto wide) {
     const unsigned a = __float_as_uint(u), b = __float_as_uint(w);
     if constexpr (decltype(wide)::value) {
@@ -76,50 +78,25 @@ __device__ __forceinline__ void channel_sums(float* v, int lane) {
       return __uint_as_float(r[0]) + __uint_as_float(r[1]);
     }
   };
-  auto ror8 = [](float x) {
-    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x128, 0xf, 0xf, true));
-  };
-  // lane ^ 4: mirror the 8-lane half, then reverse the quad
-  auto flip4 = [](float x) {
-    const int m = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x141, 0xf, 0xf, true);
-    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, m, 0x1b, 0xf, 0xf, true));
-  };
-  constexpr int H5 = N >= 2 ? N / 2 : 1, H4 = H5 >= 2 ? H5 / 2 : 1, H3 = H4 >= 2 ? H4 / 2 : 1, H2 = H3 >= 2 ? H3 / 2 : 1;
+  constexpr int H2 = N / 4, H5 = H2 >= 2 ? H2 / 2 : 1, H4 = H5 >= 2 ? H5 / 2 : 1;
+  halve_bits_3_2<H2>(v);
 #pragma unroll
-  for (int i = 0; i < H5; ++i) v[i] = swap_add(v[i], v[N >= 2 ? i + H5 : i], std::true_type{});
+  for (int i = 0; i < H5; ++i) v[i] = swap_add(v[i], v[H2 >= 2 ? i + H5 : i], std::true_type{});
 #pragma unroll
   for (int i = 0; i < H4; ++i) v[i] = swap_add(v[i], v[H5 >= 2 ? i + H4 : i], std::false_type{});
-  const bool b3 = lane & 8, b2 = lane & 4;
-#pragma unroll
-  for (int i = 0; i < H3; ++i) {
-    if constexpr (H4 >= 2) {
-      const float keep = b3 ? v[i + H3] : v[i], send = b3 ? v[i] : v[i + H3];
-      v[i] = keep + ror8(send);
-    } else {
-      v[i] += ror8(v[i]);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < H2; ++i) {
-    if constexpr (H3 >= 2) {
-      const float keep = b2 ? v[i + H2] : v[i], send = b2 ? v[i] : v[i + H2];
-      v[i] = keep + flip4(send);
-    } else {
-      v[i] += flip4(v[i]);
-    }
-  }
 }
 
 // Index of the first value that channel_sums<N> leaves in this lane. Lanes that differ in the bits
 // behind the last halving hold the same value.
 template <int N>
 __device__ __forceinline__ int channel_sum_index(int lane) {
+  constexpr int order[4] = {3, 2, 5, 4};
   int at = 0, n = N;
 #pragma unroll
-  for (int b = 5; b >= 2; --b) {
+  for (int k = 0; k < 4; ++k) {
     if (n < 2) break;
     n /= 2;
-    at += ((lane >> b) & 1) * n;
+    at += ((lane >> order[k]) & 1) * n;
   }
   return at;
 }
@@ -458,7 +435,7 @@ __global__ __launch_bounds__(kScanBlock) void scan_bwd_kernel(ScanBwdK<T> a) {
       for (int t = 0; t < 4; ++t)
 #pragma unroll
         for (int i = 0; i < NPL; ++i) pin(hs[4 * j + t][i]);
-      st[4 * j + q][in][3] = lane_sums<4>(ys, lane);
+      st[4 * j + q][in][3] = quad_sums(ys, lane);
     }
 #pragma unroll
     for (int j = CT / 4 - 1; j >= 0; --j) {
@@ -482,7 +459,7 @@ __global__ __launch_bounds__(kScanBlock) void scan_bwd_kernel(ScanBwdK<T> a) {
         }
         sb[t] = b;
         sa[t] = d;
-        channel_sums<NV>(v, lane);
+        channel_sums<NV>(v);
 #pragma unroll
         for (int i = 0; i < LEFT; ++i) red[wave][4 * j + t][q][vat + i] = v[i];
       }
@@ -491,7 +468,7 @@ __global__ __launch_bounds__(kScanBlock) void scan_bwd_kernel(ScanBwdK<T> a) {
         pin(gc[i]);
         pin(dA[i]);
       }
-      const float b = lane_sums<4>(sb, lane), d = lane_sums<4>(sa, lane) * (1.f / kLog2E);
+      const float b = quad_sums(sb, lane), d = quad_sums(sa, lane) * (1.f / kLog2E);
       *reinterpret_cast<f32x2*>(&st[4 * j + q][in]) = f32x2{b, d};
     }
     __syncthreads();
