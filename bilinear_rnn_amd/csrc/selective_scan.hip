@@ -12,12 +12,13 @@
 // inputs as float32 in LDS, formed once; sums over the states halved over the channel's lanes, eight
 // tokens at a time.
 //
-// Measured, bf16, S = 16, D = 2048: 8 x 4096 tokens 380 to 400 us (2.8e12 states per second; HBM alone
-// would take 87). Two wavefronts per SIMD are all that sequence and channels give; the vector ALU is
-// busy 75 % of the time, with 17.8 instructions per token and wavefront: 10 of the recurrence, 2.6 of
+// Measured, bf16, S = 16, D = 2048: 8 x 4096 tokens 360 to 375 us (2.9e12 states per second; HBM alone
+// would take 87), 1 x 65536 tokens, cut, 890 to 920 us. The uncut scan has the two wavefronts per SIMD
+// that sequences and channels give, and the vector ALU is busy 75 % of the time; the cut one has four
+// and runs at the rate of its instructions, 17.2 per token and wavefront: 10 of the recurrence, 2.1 of
 // the sum over the lanes, 5 of the work per token. Not better: y summed by the matrix cores (16x16x4
-// fp32 blocks hold the SIMD for 32 cycles each, 515 us), the work per token spread between the
-// recurrence's tokens instead of before and behind them (flat).
+// fp32 blocks hold the SIMD for 32 cycles each: 515 us against 421 then), the work per token spread
+// between the recurrence's tokens, branches instead of selections in it (both flat).
 //
 // Parallel over sequences and channels; a batch with too few of them for the chip is cut along time
 // into segments of L tokens (scan_plan): every segment's end state from 0, a pass that carries the
@@ -30,8 +31,8 @@ namespace comba {
 
 // Tokens per LDS tile, channels per workgroup and lanes per channel of the forward. 32 channels make
 // workgroups of four wavefronts whose phases do not line up, so that one's barrier and loads hide
-// behind another's arithmetic; 8 lanes make twice the wavefronts of 4 for the same channels. Measured
-// at B = 8, T = 4096, D = 2048, S = 16, bf16 (8 lanes): 16 / 32 / 64 tokens 449 / 406 / 392 us at 32
+// behind another's arithmetic; 8 lanes make twice the wavefronts of 4 for the same channels. Measured,
+// all before the present sum over the lanes, at B = 8, T = 4096, D = 2048, S = 16, bf16 (8 lanes): 16 / 32 / 64 tokens 449 / 406 / 392 us at 32
 // channels, 32 tokens at 16 / 64 channels 413 / 417 us; 4 lanes 595 us, 16 lanes (16 channels)
 // 439 us. At B = 1, T = 65536, cut: 966 / 949 / 1028 us, 1055 / 952, 1140, 1089.
 constexpr int kScanTile = 32, kFwdChannels = 32, kFwdLanes = 8;
