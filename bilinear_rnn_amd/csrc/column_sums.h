@@ -10,14 +10,14 @@ namespace comba {
 
 constexpr int kSumCols = 64, kSumGroups = 16;  // columns and row groups per workgroup
 
-// A wavefront reads 64 neighbouring columns (256 bytes) of one row; the 16 row groups keep enough
-// loads in flight for the few thousand columns that a layer's parameters have.
+// One workgroup's columns. A wavefront reads 64 neighbouring columns (256 bytes) of one row; the 16 row
+// groups keep enough loads in flight for the few thousand columns that a layer's parameters have.
 template <typename F>
-__global__ __launch_bounds__(kSumCols* kSumGroups) void column_sums_kernel(const float* __restrict__ part, int64_t rows,
-                                                                           int64_t stride, int cols, F out) {
+__device__ __forceinline__ void column_sums_block(const float* __restrict__ part, int64_t rows, int64_t stride, int cols,
+                                                  int block, F out) {
   __shared__ float sums[kSumGroups][kSumCols];
   const int l = threadIdx.x % kSumCols, g = threadIdx.x / kSumCols;
-  const int c = blockIdx.x * kSumCols + l;
+  const int c = block * kSumCols + l;
   float s = 0.f;
   if (c < cols) {
 #pragma unroll 4
@@ -30,6 +30,12 @@ __global__ __launch_bounds__(kSumCols* kSumGroups) void column_sums_kernel(const
     for (int i = 1; i < kSumGroups; ++i) s += sums[i][l];
     out(c, s);
   }
+}
+
+template <typename F>
+__global__ __launch_bounds__(kSumCols* kSumGroups) void column_sums_kernel(const float* __restrict__ part, int64_t rows,
+                                                                           int64_t stride, int cols, F out) {
+  column_sums_block(part, rows, stride, cols, blockIdx.x, out);
 }
 
 template <typename F>

@@ -325,7 +325,7 @@ COMBA_API int32_t comba_selective_scan_bwd(const void* x, const void* dt, const 
   const int64_t SP = comba::scan_padded_states(S), rows = static_cast<int64_t>(B) * T;
   const comba::ScanPlan p = comba::scan_bwd_plan(B, T, N, S, cu_seqlens != nullptr);
   if ((rc = check_scan_grid(p.slots, comba::scan_bwd_channel_blocks(D, G), N * D * SP)) != COMBA_OK) return rc;
-  if (rows * G * 2 * SP > kMaxThreads - 255 || D * SP > kMaxThreads / 16 - 64)  // column sums: 16 threads each
+  if (rows * G * 2 * SP + 16 * (D * SP + 2 * D) > kMaxThreads - 4096)  // the sums: 16 threads per column
     return report(COMBA_ERR_UNSUPPORTED, "too many (token, group, state) triples for one launch");
   const ScanBwdWorkspace w = scan_bwd_workspace(p, rows, D, SP, G);
   rc = check_workspace(workspace, workspace_bytes, w.total,

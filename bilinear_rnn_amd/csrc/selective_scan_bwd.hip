@@ -13,7 +13,10 @@
 //   2. scan_bwd_carry: the true incoming states and outgoing gradients, along the segments;
 //   3. scan_bwd: per segment the states at every CT-th token forward, then from its end the CT tokens
 //      of each piece: states and decays recomputed into registers, then the reverse recurrence;
-//   4. the sums over segments (dA, dskip, ddt_bias) and over channel blocks (dB, dC), in a fixed order.
+//   4. scan_bwd_sums: over segments (dA, dskip, ddt_bias) and over channel blocks (dB, dC), in a fixed
+//      order.
+// Where no sequence can be longer than a segment (T <= L), 3 starts from the given states itself and
+// writes d_initial_state: two launches instead of four, which is what a short batch's time is made of.
 // Nothing is kept from the forward. Bound by the vector ALU like the forward: three exponentials and
 // about 25 instructions per (token, channel, state). The sums over the 16 channels of a wavefront
 // halve the values at every step (permlane swaps: two instructions per pair of values). Through LDS
@@ -59,6 +62,7 @@ template <typename T> struct ScanBwdK {
   float* dBCpart;
   int N, T_, D, S, G, L;
   bool softplus;
+  bool whole;  // no sequence is cut
 };
 
 // Sums v over the 16 channels of the wavefront (lane bits 2 .. 5). At lane bit 3, 2, 5, 4 a lane keeps
@@ -312,8 +316,9 @@ __global__ __launch_bounds__(kScanBlock) void scan_bwd_carry_kernel(
   if (back && dinit && real) dinit[(n * D + c) * S + s] = h;
 }
 
+// Up to 8 states the registers are held to what three wavefronts per SIMD have.
 template <typename T, int NPL>
-__global__ __launch_bounds__(kScanBlock) void scan_bwd_kernel(ScanBwdK<T> a) {
+__global__ __launch_bounds__(kScanBlock, NPL == 2 ? 3 : 1) void scan_bwd_kernel(ScanBwdK<T> a) {
   constexpr int SP = 4 * NPL, CT = BwdTile<NPL>::CT, NSUB = BwdTile<NPL>::NSUB, L = BwdTile<NPL>::L;
   constexpr int NV = 2 * NPL;
   constexpr int LEFT = NV >= 16 ? NV / 16 : 1;
@@ -350,8 +355,14 @@ __global__ __launch_bounds__(kScanBlock) void scan_bwd_kernel(ScanBwdK<T> a) {
   for (int i = 0; i < NPL; ++i) {
     const int s = q * NPL + i;
     A2[i] = s < a.S ? decay_rate(a.A[static_cast<int64_t>(c) * a.S + s]) : 0.f;
-    h[i] = live ? a.hseg[at + i] : 0.f;
-    gc[i] = live ? a.gseg[at + i] : 0.f;
+    const int64_t given = (static_cast<int64_t>(p.n) * a.D + c) * a.S + s;
+    if (a.whole) {
+      h[i] = live && a.init && s < a.S ? a.init[given] : 0.f;
+      gc[i] = live && a.dfin && s < a.S ? a.dfin[given] : 0.f;
+    } else {
+      h[i] = live ? a.hseg[at + i] : 0.f;
+      gc[i] = live ? a.gseg[at + i] : 0.f;
+    }
     dA[i] = 0.f;
   }
   const int lc = p.c0 + (pc.live ? pc.ch : p.cl - 1);
@@ -511,28 +522,63 @@ __global__ __launch_bounds__(kScanBlock) void scan_bwd_kernel(ScanBwdK<T> a) {
   }
   if (!live) return;
 #pragma unroll
-  for (int i = 0; i < NPL; ++i) a.dApart[at + i] = dA[i];
+  for (int i = 0; i < NPL; ++i) {
+    const int s = q * NPL + i;
+    a.dApart[at + i] = dA[i];
+    if (a.whole && a.dinit && s < a.S) a.dinit[(static_cast<int64_t>(p.n) * a.D + c) * a.S + s] = gc[i];
+  }
 }
 
-// dB and dC: the partial sums of the group's channel blocks, added in order and rounded once.
-// Tokens of no sequence are left alone.
+struct ScanSums {
+  const float* dApart;
+  const float* dDpart;
+  const float* dBCpart;
+  const int32_t* cu;
+  float* dA;
+  float* dskip;
+  float* dbias;
+  int64_t slots, rows;
+  int N, D, S, SP, G, blocks;  // blocks: channel blocks of a group
+};
+
+constexpr int kSumThreads = kSumCols * kSumGroups;
+static int64_t sum_blocks(int64_t columns) { return (columns + kSumCols - 1) / kSumCols; }
+
+// One launch for all sums: the first workgroups take dA's columns, the next dskip's and ddt_bias's,
+// the rest dB and dC, whose partial sums (one per channel block of the group) are added in order and
+// rounded once. Tokens of no sequence are left alone.
 template <typename T>
-__global__ __launch_bounds__(kScanBlock) void scan_bwd_bc_kernel(const float* __restrict__ part, const int32_t* __restrict__ cu,
-                                                                 int N, int64_t rows, int G, int S, int SP, int blocks,
-                                                                 T* __restrict__ dB, T* __restrict__ dC) {
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * kScanBlock + threadIdx.x, per = rows * G * 2 * SP;
+__global__ __launch_bounds__(kSumThreads) void scan_bwd_sums_kernel(ScanSums a, int ablocks, int dblocks, T* __restrict__ dB,
+                                                                    T* __restrict__ dC) {
+  int b = blockIdx.x;
+  if (b < ablocks) {
+    column_sums_block(a.dApart, a.slots, static_cast<int64_t>(a.D) * a.SP, a.D * a.SP, b, [&](int col, float v) {
+      if (col % a.SP < a.S) a.dA[static_cast<int64_t>(col / a.SP) * a.S + col % a.SP] = v;
+    });
+    return;
+  }
+  b -= ablocks;
+  if (b < dblocks) {
+    column_sums_block(a.dDpart, a.slots, 2 * static_cast<int64_t>(a.D), 2 * a.D, b, [&](int col, float v) {
+      float* to = col < a.D ? a.dskip : a.dbias;
+      if (to) to[col < a.D ? col : col - a.D] = v;
+    });
+    return;
+  }
+  b -= dblocks;
+  const int64_t id = static_cast<int64_t>(b) * kSumThreads + threadIdx.x, per = a.rows * a.G * 2 * a.SP;
   if (id >= per) return;
-  const int s = static_cast<int>(id % SP), which = static_cast<int>(id / SP) & 1;
-  const int64_t rg = id / (2 * SP);
-  if (s >= S) return;
-  if (cu) {
-    const int64_t t = rg / G;
-    if (t < cu[0] || t >= cu[N]) return;
+  const int s = static_cast<int>(id % a.SP), which = static_cast<int>(id / a.SP) & 1;
+  const int64_t rg = id / (2 * a.SP);
+  if (s >= a.S) return;
+  if (a.cu) {
+    const int64_t t = rg / a.G;
+    if (t < a.cu[0] || t >= a.cu[a.N]) return;
   }
   float v = 0.f;
 #pragma unroll 4
-  for (int b = 0; b < blocks; ++b) v += part[b * per + id];
-  Elem<T>::store(which ? dC : dB, rg * S + s, v);
+  for (int k = 0; k < a.blocks; ++k) v += a.dBCpart[k * per + id];
+  Elem<T>::store(which ? dC : dB, rg * a.S + s, v);
 }
 
 int64_t scan_bwd_channel_blocks(int64_t D, int64_t G) { return G * ((D / G + kScanChannels - 1) / kScanChannels); }
@@ -552,42 +598,27 @@ static hipError_t scan_bwd_t(const ScanBwdArgs& a, const ScanPlan& p, hipStream_
                       static_cast<const T*>(f.Cm), f.skip, static_cast<const T*>(f.z), f.dt_bias, f.init, f.cu_seqlens,
                       static_cast<const T*>(a.dy), a.dfin, static_cast<T*>(a.dx), static_cast<T*>(a.ddt),
                       static_cast<T*>(a.dz), a.dinit, a.hseg, a.gseg, a.dsum, a.dApart, a.dDpart, a.dBCpart,
-                      f.N, f.T, f.D, f.S, f.G, p.L, f.softplus};
+                      f.N, f.T, f.D, f.S, f.G, p.L, f.softplus, f.T <= p.L};
   const int64_t cb = scan_bwd_channel_blocks(f.D, f.G), rows = static_cast<int64_t>(f.B) * f.T;
   const unsigned grid = static_cast<unsigned>(p.slots * cb);
   hipError_t e;
-  scan_bwd_ends_kernel<T, NPL><<<grid, kScanBlock, 0, st>>>(k);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  const int64_t threads = static_cast<int64_t>(f.N) * f.D * SP;
-  scan_bwd_carry_kernel<<<dim3(static_cast<unsigned>((threads + kScanBlock - 1) / kScanBlock), 2), kScanBlock, 0, st>>>(
-      f.A, f.init, a.dfin, f.cu_seqlens, f.N, f.T, f.D, f.S, SP, p.L, a.hseg, a.gseg, a.dsum, a.dinit);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  scan_bwd_kernel<T, NPL><<<grid, kScanBlock, 0, st>>>(k);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  if (rows > 0) {
-    const int64_t n = rows * f.G * 2 * SP;
-    scan_bwd_bc_kernel<T><<<static_cast<unsigned>((n + kScanBlock - 1) / kScanBlock), kScanBlock, 0, st>>>(
-        a.dBCpart, f.cu_seqlens, f.N, rows, f.G, f.S, SP, static_cast<int>(cb / f.G), static_cast<T*>(a.dBm),
-        static_cast<T*>(a.dCm));
+  if (!k.whole) {
+    scan_bwd_ends_kernel<T, NPL><<<grid, kScanBlock, 0, st>>>(k);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    const int64_t threads = static_cast<int64_t>(f.N) * f.D * SP;
+    scan_bwd_carry_kernel<<<dim3(static_cast<unsigned>((threads + kScanBlock - 1) / kScanBlock), 2), kScanBlock, 0, st>>>(
+        f.A, f.init, a.dfin, f.cu_seqlens, f.N, f.T, f.D, f.S, SP, p.L, a.hseg, a.gseg, a.dsum, a.dinit);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  float* dA = a.dA;
-  const int S = f.S;
-  e = column_sums(a.dApart, p.slots, static_cast<int64_t>(f.D) * SP, f.D * SP, st, [=] __device__(int col, float v) {
-    if (col % SP < S) dA[static_cast<int64_t>(col / SP) * S + col % SP] = v;
-  });
-  if (e != hipSuccess) return e;
-  float* dk = a.dskip;
-  float* db = a.ddt_bias;
-  if (!dk && !db) return hipSuccess;
-  const int D = f.D;
-  return column_sums(a.dDpart, p.slots, 2 * static_cast<int64_t>(D), 2 * D, st, [=] __device__(int col, float v) {
-    if (col < D) {
-      if (dk) dk[col] = v;
-    } else if (db) {
-      db[col - D] = v;
-    }
-  });
+  scan_bwd_kernel<T, NPL><<<grid, kScanBlock, 0, st>>>(k);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  const ScanSums sums{a.dApart, a.dDpart, a.dBCpart, f.cu_seqlens, a.dA, a.dskip, a.ddt_bias, p.slots, rows,
+                      f.N, f.D, f.S, SP, f.G, static_cast<int>(cb / f.G)};
+  const int64_t ablocks = sum_blocks(static_cast<int64_t>(f.D) * SP), dblocks = sum_blocks(2ll * f.D);
+  const int64_t bcblocks = (rows * f.G * 2 * SP + kSumThreads - 1) / kSumThreads;
+  scan_bwd_sums_kernel<T><<<static_cast<unsigned>(ablocks + dblocks + bcblocks), kSumThreads, 0, st>>>(
+      sums, static_cast<int>(ablocks), static_cast<int>(dblocks), static_cast<T*>(a.dBm), static_cast<T*>(a.dCm));
+  return hipGetLastError();
 }
 
 hipError_t launch_scan_bwd(const ScanBwdArgs& a, const ScanPlan& p, hipStream_t st) {
