@@ -102,7 +102,7 @@ struct ScanPlan {
   int64_t slots;
 };
 ScanPlan scan_plan(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N, bool packed);
-ScanPlan scan_bwd_plan(int64_t B, int64_t T, int64_t N, int S, bool packed);
+ScanPlan scan_bwd_plan(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N, int S, bool packed);
 int scan_padded_states(int S);           // states per channel in the workspaces
 int64_t scan_channel_blocks(int64_t D, int64_t G);      // workgroups per slot
 int64_t scan_bwd_channel_blocks(int64_t D, int64_t G);

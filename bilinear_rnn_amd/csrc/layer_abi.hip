@@ -303,7 +303,7 @@ COMBA_API int32_t comba_selective_step(const void* x, const void* dt, const floa
 COMBA_API size_t comba_selective_scan_bwd_workspace_size(int32_t B, int32_t T, int32_t D, int32_t S, int32_t G,
                                                          int32_t num_seqs) {
   if (!scan_sizes_ok(B, T, D, S, G)) return 0;
-  const comba::ScanPlan p = comba::scan_bwd_plan(B, T, num_seqs > 0 ? num_seqs : B, S, num_seqs > 0);
+  const comba::ScanPlan p = comba::scan_bwd_plan(B, T, D, G, num_seqs > 0 ? num_seqs : B, S, num_seqs > 0);
   return scan_bwd_workspace(p, static_cast<int64_t>(B) * T, D, comba::scan_padded_states(S), G).total;
 }
 
@@ -323,7 +323,7 @@ COMBA_API int32_t comba_selective_scan_bwd(const void* x, const void* dt, const 
   int64_t N = 0;
   if ((rc = check_batch(cu_seqlens, num_seqs, B, T, N)) != COMBA_OK) return rc;
   const int64_t SP = comba::scan_padded_states(S), rows = static_cast<int64_t>(B) * T;
-  const comba::ScanPlan p = comba::scan_bwd_plan(B, T, N, S, cu_seqlens != nullptr);
+  const comba::ScanPlan p = comba::scan_bwd_plan(B, T, D, G, N, S, cu_seqlens != nullptr);
   if ((rc = check_scan_grid(p.slots, comba::scan_bwd_channel_blocks(D, G), N * D * SP)) != COMBA_OK) return rc;
   if (rows * G * 2 * SP + 16 * (D * SP + 2 * D) > kMaxThreads - 4096)  // the sums: 16 threads per column
     return report(COMBA_ERR_UNSUPPORTED, "too many (token, group, state) triples for one launch");

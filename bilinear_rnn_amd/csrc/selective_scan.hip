@@ -415,16 +415,17 @@ int64_t scan_channel_blocks(int64_t D, int64_t G) { return G * ((D / G + kFwdCha
 // where the uncut scan leaves SIMDs with one wavefront or none, 256 workgroups of four wavefronts.
 // Measured at D = 2048, S = 16, T = 4096, bf16, uncut / cut: 261 / 79 us for B = 1, 265 / 136 for 2,
 // 261 / 183 for 3, 271 / 237 for 4, 359 / 343 for 6; at B = 1, T = 65536 4640 / 874. Segments make
-// 1024 workgroups, within 128 tokens (B = 1, T = 1024: 32 us against 42 with 256) and 1024 tokens
-// (T = 65536: 874 us, 951 with 4096).
+// 1024 workgroups, within 64 tokens (D = 512: T = 300 18 us, 22 with 128; T = 2048 23 us, 24 with 128,
+// 27 with 32) and 1024 tokens (T = 65536: 874 us, 951 with 4096). Fewer than 256 tokens stay whole: two
+// more launches cost as much (T = 200: 16 us whole, 18.5 cut; 256 with 32 states: 25 whole, 20 cut).
 // A packed batch's lengths are not known here. Its long sequences are cut, to 512 tokens at the most
 // (64 lognormal sequences, 47204 tokens: 742 us, 966 uncut), but where there are enough sequences to
 // fill the chip not below their mean length, so that sequences of one length stay whole.
 ScanPlan scan_plan(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N, bool packed) {
   const int64_t cb = scan_channel_blocks(D, G), most = packed ? 512 : 1024;
-  if (!packed && B * cb > 256) return ScanPlan{0, N};
+  if (T < 256 || (!packed && B * cb > 256)) return ScanPlan{0, N};
   int64_t L = B * T * cb / 2048;
-  L = L < 128 ? 128 : (L > most ? most : L);
+  L = L < 64 ? 64 : (L > most ? most : L);
   if (packed && N * cb >= 512 && L < (T + N - 1) / N) L = (T + N - 1) / N;
   L = (L + kScanTile - 1) / kScanTile * kScanTile;
   if (L >= T) return ScanPlan{0, N};

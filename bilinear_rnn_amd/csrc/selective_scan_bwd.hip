@@ -25,6 +25,8 @@
 // Measured there, bf16: 357 to 367 us in all: 78 (1), 10 (2), 285 (3), 7 and 9 (4), without the gaps.
 // The vector ALU is busy 75 % of 3's time, at two wavefronts per SIMD (240 registers: 16 tokens'
 // states and decays; 61 KB of LDS). HBM moves 0.33 GB in 3.
+#include <utility>
+
 #include "column_sums.h"
 #include "comba.h"
 #include "scan_common.h"
@@ -33,8 +35,7 @@ namespace comba {
 
 template <int NPL> struct BwdTile {
   static constexpr int CT = NPL <= 4 ? 16 : 64 / NPL;        // tokens whose states are held in registers
-  static constexpr int NSUB = NPL <= 8 ? 8 : 4;              // pieces of CT tokens per segment
-  static constexpr int L = CT * NSUB;
+  static constexpr int NSUB = NPL <= 8 ? 8 : 4;              // pieces of CT tokens in the longest segment
 };
 
 template <typename T> struct ScanBwdK {
@@ -202,13 +203,13 @@ template <typename T, int TT, int SP> struct PieceBC {
 
 template <typename T, int NPL>
 __global__ __launch_bounds__(kScanBlock) void scan_bwd_ends_kernel(ScanBwdK<T> a) {
-  constexpr int SP = 4 * NPL, L = BwdTile<NPL>::L, TT = BwdTile<NPL>::CT;
+  constexpr int SP = 4 * NPL, TT = BwdTile<NPL>::CT;
   __shared__ __align__(16) float bc[2][TT][4][2 * NPL];
   __shared__ __align__(16) f32x4 st[2][TT][kScanChannels];  // step size, input, gradient of y
   __shared__ float tot[4][kScanChannels];
   const int tid = threadIdx.x, lane = tid & 63, q = lane & 3;
   const int cblocks = a.G * ((a.D / a.G + kScanChannels - 1) / kScanChannels);
-  const ScanPlace p = scan_place<kScanChannels>(blockIdx.x / cblocks, blockIdx.x % cblocks, a.cu, a.N, a.T_, a.D, a.G, L);
+  const ScanPlace p = scan_place<kScanChannels>(blockIdx.x / cblocks, blockIdx.x % cblocks, a.cu, a.N, a.T_, a.D, a.G, a.L);
   if (!p.ok) return;
   Piece<T, TT> pc;
   pc.place(a, p);
@@ -319,7 +320,7 @@ __global__ __launch_bounds__(kScanBlock) void scan_bwd_carry_kernel(
 // Up to 8 states the registers are held to what three wavefronts per SIMD have.
 template <typename T, int NPL>
 __global__ __launch_bounds__(kScanBlock, NPL == 2 ? 3 : 1) void scan_bwd_kernel(ScanBwdK<T> a) {
-  constexpr int SP = 4 * NPL, CT = BwdTile<NPL>::CT, NSUB = BwdTile<NPL>::NSUB, L = BwdTile<NPL>::L;
+  constexpr int SP = 4 * NPL, CT = BwdTile<NPL>::CT, NSUB = BwdTile<NPL>::NSUB;
   constexpr int NV = 2 * NPL;
   constexpr int LEFT = NV >= 16 ? NV / 16 : 1;
   __shared__ __align__(16) float bc[2][CT][4][NV];              // two pieces, then one
@@ -331,7 +332,7 @@ __global__ __launch_bounds__(kScanBlock, NPL == 2 ? 3 : 1) void scan_bwd_kernel(
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, q = lane & 3;
   const int dg = a.D / a.G, per = (dg + kScanChannels - 1) / kScanChannels, cblocks = a.G * per;
   const int cb = blockIdx.x % cblocks;
-  const ScanPlace p = scan_place<kScanChannels>(blockIdx.x / cblocks, cb, a.cu, a.N, a.T_, a.D, a.G, L);
+  const ScanPlace p = scan_place<kScanChannels>(blockIdx.x / cblocks, cb, a.cu, a.N, a.T_, a.D, a.G, a.L);
   const int in = tid / 4;
   const bool live = in < p.cl;
   const int c = p.c0 + (live ? in : p.cl - 1);
@@ -583,11 +584,19 @@ __global__ __launch_bounds__(kSumThreads) void scan_bwd_sums_kernel(ScanSums a, 
 
 int64_t scan_bwd_channel_blocks(int64_t D, int64_t G) { return G * ((D / G + kScanChannels - 1) / kScanChannels); }
 
-ScanPlan scan_bwd_plan(int64_t B, int64_t T, int64_t N, int S, bool packed) {
+// Segments are as long as LDS holds pieces of (128 tokens up to 16 states), shorter, down to one piece,
+// where that leaves fewer than two workgroups per compute unit. At D = 2048, S = 16, bf16, with 128 /
+// 64 / 32 / 16 tokens: 1 x 128 tokens 61 / 50 / 35 / 30 us, 1 x 1024 87 / 67 / 70 / 79, 1 x 4096
+// 192 / 198 / 214 / 255; 1 x 500 of 512 channels 81 / 48 / 34 / 30.
+ScanPlan scan_bwd_plan(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N, int S, bool packed) {
   const int npl = scan_padded_states(S) / 4;
-  const int L = npl <= 4 ? BwdTile<4>::L : npl == 8 ? BwdTile<8>::L : BwdTile<16>::L;
-  static_assert(BwdTile<2>::L == BwdTile<4>::L, "one segment length up to 16 states");
-  return ScanPlan{L, packed ? T / L + N + 1 : B * ((T + L - 1) / L)};
+  auto tile = [](auto t) { return std::pair<int64_t, int64_t>(decltype(t)::CT, decltype(t)::NSUB); };
+  const auto [ct, most] = npl <= 4 ? tile(BwdTile<4>{}) : npl == 8 ? tile(BwdTile<8>{}) : tile(BwdTile<16>{});
+  static_assert(BwdTile<2>::CT == BwdTile<4>::CT && BwdTile<2>::NSUB == BwdTile<4>::NSUB, "one length up to 16 states");
+  const int64_t cb = scan_bwd_channel_blocks(D, G);
+  int64_t L = ct * most;
+  while (L > ct && (B * T / L + N) * cb < 512) L /= 2;
+  return ScanPlan{static_cast<int>(L), packed ? T / L + N + 1 : B * ((T + L - 1) / L)};
 }
 
 template <typename T, int NPL>

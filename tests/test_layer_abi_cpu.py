@@ -147,14 +147,19 @@ def test_workspace_sizes():
     assert size(8, 4096, 2048, 16) == 0
     # 2048 channels are 64 workgroups: segments of 65536 * 64 / 2048, at most 1024 tokens
     assert size(1, 65536, 2048, 16) == up(64 * 2048 * 16 * 4) + up(64 * 2048 * 4)
-    # packed: T / L + N + 1 slots; few workgroups, so the shortest segments, 128 tokens
-    assert size(1, 5000, 64, 8, 1, 3) == up((5000 // 128 + 4) * 64 * 8 * 4) + up((5000 // 128 + 4) * 64 * 4)
+    # packed: T / L + N + 1 slots; few workgroups, so the shortest segments, 64 tokens
+    assert size(1, 5000, 64, 8, 1, 3) == up((5000 // 64 + 4) * 64 * 8 * 4) + up((5000 // 64 + 4) * 64 * 4)
+    assert size(1, 255, 64, 8) == 0 and size(1, 256, 64, 8) > 0      # short batches stay whole
     assert size(1, 100, 65, 16, 2) == 0          # G does not divide D
     # backward: 128 tokens per segment up to 16 states; three state arrays, four rows of D, B and C
     bwd = L.comba_selective_scan_bwd_workspace_size
     slots = 4 * 2048 // 128
     assert bwd(4, 2048, 2048, 16, 1, 0) == (3 * up(slots * 2048 * 16 * 4) + up(slots * 2048 * 4) + up(slots * 2 * 2048 * 4)
                                             + up(32 * 4 * 2048 * 2 * 16 * 4))
+    # a small batch: segments of one piece, 16 tokens
+    slots = 7
+    assert bwd(1, 100, 64, 16, 1, 0) == (3 * up(slots * 64 * 16 * 4) + up(slots * 64 * 4) + up(slots * 2 * 64 * 4)
+                                         + up(100 * 2 * 16 * 4))
     norm_ws = L.comba_block_norm_bwd_workspace_size
     assert norm_ws(8192, 2048) == 512 * 3 * 2048 * 4 and norm_ws(0, 64) == 0 and norm_ws(5, 16385) == 0
     assert norm_ws(3, 64) == 3 * 64 * 4 and norm_ws(33, 64) == up(2 * 3 * 64 * 4)   # 32 rows per workgroup
