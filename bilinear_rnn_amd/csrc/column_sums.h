@@ -14,7 +14,7 @@ constexpr int kSumCols = 64, kSumGroups = 16;  // columns and row groups per wor
 // groups keep enough loads in flight for the few thousand columns that a layer's parameters have.
 template <typename F>
 __device__ __forceinline__ void column_sums_block(const float* __restrict__ part, int64_t rows, int64_t stride, int cols,
-                                                  int block, F out) {
+                                                  int block, const F& out) {
   __shared__ float sums[kSumGroups][kSumCols];
   const int l = threadIdx.x % kSumCols, g = threadIdx.x / kSumCols;
   const int c = block * kSumCols + l;

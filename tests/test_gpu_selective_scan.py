@@ -89,7 +89,19 @@ def test_cases_cover_both_plans():
     assert sum(s > 0 for s in sizes) >= 4 and sum(s == 0 for s in sizes) >= 8
 
 
-@pytest.mark.parametrize("B,T,D,S,G,dtype,softplus,lens,without", CASES)
+BACKWARD = CASES + [  # enough sequences for segments of several pieces (16, 8 or 4 tokens each)
+    (70, 40, 512, 16, 1, F32, True, None, ()),                               # whole sequences of three pieces
+    (50, 140, 512, 16, 1, BF16, True, None, ()),                             # segments of 128 tokens
+    (24, 140, 512, 8, 2, F32, True, None, ("init",)),                        # of 64
+    (12, 140, 512, 16, 1, F32, True, None, ("z",)),                          # of 32
+    (1, 100, 512, 16, 1, F32, True, [5 * (k % 4 == 0) for k in range(80)], ()),          # packed, whole
+    (1, 1082, 512, 16, 1, F32, True, [k % 21 for k in range(70)] + [300, 131], ()),      # packed, two cut
+    (40, 70, 512, 32, 1, F32, True, None, ()), (70, 60, 512, 32, 1, F32, True, None, ("skip",)),
+    (60, 20, 512, 64, 1, F32, True, None, ()), (70, 14, 512, 64, 1, F32, False, None, ()),
+]
+
+
+@pytest.mark.parametrize("B,T,D,S,G,dtype,softplus,lens,without", BACKWARD)
 def test_backward(B, T, D, S, G, dtype, softplus, lens, without):
     on, ref = make(B, T, D, S, G, dtype, lens, without, seed=1, softplus=softplus)
     cu = cu_of(lens)
