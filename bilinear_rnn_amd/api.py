@@ -541,17 +541,18 @@ def _sequences(B: int, T: int, cu_seqlens: Optional[torch.Tensor], index: int) -
     return cu_seqlens.numel() - 1
 
 
-def _workspace(workspace: Optional[torch.Tensor], nbytes: int, device) -> Optional[torch.Tensor]:
-    """The caller's workspace if it is large enough, else a new one (None where none is needed)."""
+def _workspace(workspace: Optional[torch.Tensor], nbytes: int, like: torch.Tensor) -> Optional[torch.Tensor]:
+    """The caller's workspace if it is large enough, else a new one on like's device (None where none is
+    needed)."""
     if nbytes == 0:
         return None
     if workspace is not None:
         _require(workspace, "workspace", torch.uint8)
-        if workspace.device != device:
-            raise ValueError(f"workspace is on {workspace.device}, not on {device}")
+        if workspace.device != like.device:
+            raise ValueError(f"workspace is on {workspace.device}, not on {like.device}")
         if workspace.numel() >= nbytes:
             return workspace
-    return torch.empty((nbytes,), dtype=torch.uint8, device=device)
+    return like.new_empty((nbytes,), dtype=torch.uint8)
 
 
 def _at(t: Optional[torch.Tensor]):
@@ -674,11 +675,10 @@ def short_conv_bwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.T
     _may(d_final_state, "d_final_state", x.dtype, (N, W - 1, D), index)
     nseq = N if cu_seqlens is not None else 0
     L = lib()
-    f32 = dict(dtype=torch.float32, device=x.device)
-    g = dict(dx=torch.empty_like(x), dweight=torch.empty((D, W), **f32),
-             dbias=None if bias is None else torch.empty((D,), **f32),
+    g = dict(dx=torch.empty_like(x), dweight=torch.empty_like(weight),
+             dbias=None if bias is None else torch.empty_like(bias),
              dinitial_state=None if initial_state is None else torch.empty_like(initial_state))
-    workspace = _workspace(workspace, int(L.comba_short_conv_bwd_workspace_size(B, T, D, W, nseq)), x.device)
+    workspace = _workspace(workspace, int(L.comba_short_conv_bwd_workspace_size(B, T, D, W, nseq)), x)
     _run(L.comba_short_conv_bwd, index,
          _at(x), _at(weight), _at(bias), _at(initial_state), _at(cu_seqlens), nseq, B, T, D, W, _DT[x.dtype],
          int(bool(silu)), _at(dy), _DT[dy.dtype], _at(d_final_state), _at(g["dx"]), _at(g["dweight"]),
@@ -735,7 +735,7 @@ def selective_scan(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, Bm: torch
     else:
         final_state = _new_state(x, initial_state, (N, D, S), torch.float32)
     nseq = N if cu_seqlens is not None else 0
-    workspace = _workspace(workspace, selective_scan_workspace_size(B, T, D, S, G, nseq), x.device)
+    workspace = _workspace(workspace, selective_scan_workspace_size(B, T, D, S, G, nseq), x)
     _run(lib().comba_selective_scan_fwd, index,
          _at(x), _at(dt), _at(A), _at(Bm), _at(Cm), _at(skip), _at(z), _at(dt_bias), int(bool(softplus)),
          _at(initial_state), _at(cu_seqlens), nseq, B, T, D, S, G, _DT[x.dtype], _at(out), _at(final_state),
@@ -787,7 +787,7 @@ def selective_scan_bwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, Bm: t
         return None if t is None else torch.empty_like(t)
     g = dict(dx=like(x), ddt=like(dt), dA=like(A), dB=like(Bm), dC=like(Cm), dskip=like(skip), dz=like(z),
              ddt_bias=like(dt_bias), dinitial_state=like(initial_state))
-    workspace = _workspace(workspace, int(L.comba_selective_scan_bwd_workspace_size(B, T, D, S, G, nseq)), x.device)
+    workspace = _workspace(workspace, int(L.comba_selective_scan_bwd_workspace_size(B, T, D, S, G, nseq)), x)
     _run(L.comba_selective_scan_bwd, index,
          _at(x), _at(dt), _at(A), _at(Bm), _at(Cm), _at(skip), _at(z), _at(dt_bias), int(bool(softplus)),
          _at(initial_state), _at(cu_seqlens), nseq, B, T, D, S, G, _DT[x.dtype], _at(dy), _at(d_final_state),
@@ -853,7 +853,7 @@ def block_norm_bwd(y: torch.Tensor, dr: Optional[torch.Tensor] = None, dn: Optio
         return None if t is None else torch.empty_like(t)
     g = dict(dy=like(y), dgate=like(gate), dresidual=like(residual), dscale=like(scale),
              dpost_weight=like(post_weight), dpre_weight=like(pre_weight))
-    workspace = _workspace(workspace, int(L.comba_block_norm_bwd_workspace_size(rows, D)), y.device)
+    workspace = _workspace(workspace, int(L.comba_block_norm_bwd_workspace_size(rows, D)), y)
     _run(L.comba_block_norm_bwd, index,
          _at(y), _at(gate), _at(residual), _at(scale), _at(post_weight), _at(pre_weight), rows, D, float(eps),
          _DT[y.dtype], _at(dr), _at(dn), _at(g["dy"]), _at(g["dgate"]), _at(g["dresidual"]),

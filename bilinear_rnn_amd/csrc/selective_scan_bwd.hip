@@ -19,10 +19,10 @@
 // writes d_initial_state: two launches instead of four, which is what a short batch's time is made of.
 // Nothing is kept from the forward. Bound by the vector ALU like the forward: three exponentials and
 // about 25 instructions per (token, channel, state). The sums over the 16 channels of a wavefront
-// halve the values at every step (permlane swaps: two instructions per pair of values). Through LDS
-// instead (terms written, one sum per lane read back) the vector ALU has 12 % less to do, but the
-// kernel waits for LDS longer than that: 316 us against 300 at B = 4, T = 2048, D = 2048, S = 16.
-// Measured there, bf16: 357 to 367 us in all: 78 (1), 10 (2), 285 (3), 7 and 9 (4), without the gaps.
+// halve the values at every step. Through LDS instead (terms written, one sum per lane read back) the
+// vector ALU has 12 % less to do, but the kernel waits for LDS longer than that: 316 us against 300 at
+// B = 4, T = 2048, D = 2048, S = 16.
+// Measured there, bf16: 357 to 360 us in all: 78 (1), 10 (2), 283 (3), 9 (4), without the gaps.
 // The vector ALU is busy 75 % of 3's time, at two wavefronts per SIMD (240 registers: 16 tokens'
 // states and decays; 61 KB of LDS). HBM moves 0.33 GB in 3.
 #include <utility>
