@@ -8,7 +8,7 @@
 // Sums and the SiLU are float32, the output is rounded once. Measured, W = 4, bf16:
 //   8 x 4096 tokens of 2048 channels: 46 us, 5.8 TB/s of the 6.2 that an elementwise sum reaches
 //   (56 us with loads only at natural alignment and stores through the caches); fp32, W = 3,
-//   15001 packed tokens of 1001 channels, whose rows start anywhere: 28 us, 4.4 TB/s (35 us with
+//   15001 packed tokens of 1001 channels, whose rows start anywhere: 25 us, 4.8 TB/s (35 us with
 //   element loads);
 //   one token for 256 sequences: 4.8 us, of which a launch takes most.
 #include "comba.h"
@@ -52,6 +52,15 @@ __device__ __forceinline__ ConvPos conv_pos(int D, int tiles) {
   p.nc = min(E, D - p.c);
   p.done = p.tile >= tiles;
   return p;
+}
+
+// A ragged last group of channels moved back to whole pieces: some channels are then computed and
+// stored twice, with the same bits, instead of a wavefront's going through element accesses (15001
+// packed tokens of 1001 fp32 channels 28 -> 25 us; 8 x 2048 tokens of 1999 bf16 channels 67 -> 29, the
+// backward 133 -> 44). Not where a state may be updated in place.
+template <int E>
+__device__ __forceinline__ int whole_group(int c, int64_t D) {
+  return min(c, static_cast<int>(D) - E);
 }
 
 template <int E, bool V, int W>
@@ -127,7 +136,7 @@ __global__ __launch_bounds__(kConvBlock) void conv_fwd_kernel(
     bool silu, T* __restrict__ y, T* __restrict__ fin) {
   const ConvPos p = conv_pos<E>(static_cast<int>(D), tiles + (fin ? N : 0));
   if (p.done) return;
-  const int c = p.c, nc = p.nc;
+  const int c = V ? whole_group<E>(p.c, D) : p.c, nc = V ? E : p.nc;
   if (p.tile >= tiles) {  // the last W - 1 inputs of sequence n: exact copies
     const int n = p.tile - tiles;
     int s = 0, e = Tn;
@@ -234,7 +243,8 @@ __global__ __launch_bounds__(kConvBlock) void conv_bwd_kernel(
   const int four = blockIdx.x / gblocks, g = (blockIdx.x - four * gblocks) * kWave + lane;
   const int sets = (tiles + 3) / 4, tile = four * 4 + wave;
   const bool here = g < groups;
-  const int c = here ? g * E : 0, nc = here ? min(E, static_cast<int>(D) - c) : 0;
+  const int c = !here ? 0 : V ? whole_group<E>(g * E, D) : g * E;
+  const int nc = !here ? 0 : V ? E : min(E, static_cast<int>(D) - c);
   float w[W][E], bs[E];
   if (here) load_weights<E, V, W>(weight, bias, c, nc, w, bs);
   if (four >= sets) {
@@ -461,8 +471,10 @@ static hipError_t conv_w(const ConvArgs& a, bool step, hipStream_t st) {
 }
 
 static hipError_t conv_any(const ConvArgs& a, bool step, hipStream_t st) {
-  if (a.dtype == COMBA_BF16) return a.D % 8 == 0 ? conv_w<u16, 8, true>(a, step, st) : conv_w<u16, 8, false>(a, step, st);
-  return a.D % 4 == 0 ? conv_w<float, 4, true>(a, step, st) : conv_w<float, 4, false>(a, step, st);
+  const int E = a.dtype == COMBA_BF16 ? 8 : 4;
+  const bool v = step ? a.D % E == 0 : a.D >= E;  // every thread has a whole piece of channels
+  if (a.dtype == COMBA_BF16) return v ? conv_w<u16, 8, true>(a, step, st) : conv_w<u16, 8, false>(a, step, st);
+  return v ? conv_w<float, 4, true>(a, step, st) : conv_w<float, 4, false>(a, step, st);
 }
 
 hipError_t launch_conv(const ConvArgs& a, hipStream_t st) { return conv_any(a, false, st); }
@@ -478,7 +490,7 @@ static hipError_t conv_bwd_w(const ConvBwdArgs& a, hipStream_t st) {
 }
 
 hipError_t launch_conv_bwd(const ConvBwdArgs& a, hipStream_t st) {
-  const bool v = a.f.D % kConvBwdPiece == 0;
+  const bool v = a.f.D >= kConvBwdPiece;
   if (a.f.dtype == COMBA_FP32) return v ? conv_bwd_w<float, float, true>(a, st) : conv_bwd_w<float, float, false>(a, st);
   if (a.dy_dtype == COMBA_FP32) return v ? conv_bwd_w<u16, float, true>(a, st) : conv_bwd_w<u16, float, false>(a, st);
   return v ? conv_bwd_w<u16, u16, true>(a, st) : conv_bwd_w<u16, u16, false>(a, st);
