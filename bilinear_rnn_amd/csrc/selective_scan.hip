@@ -320,18 +320,21 @@ __global__ __launch_bounds__(kScanBlock) void scan_carry_kernel(const float* __r
 // HBM. Four lanes per channel, a workgroup takes several sequences with A in registers, two
 // sequences' loads in flight. Measured at D = 2048, S = 16, bf16, in place: 13.5 us for 256 sequences
 // (5.3 TB/s; 19.6 us with one sequence's loads in flight and B and C element by element), 101 us for
-// 2048 (5.5 TB/s). States stored past the caches; loads that skip them too cost 16.8 us for 256.
-template <typename T, int NPL, bool V>
+// 2048 (5.5 TB/s); 256 with 13 states, whose rows start anywhere, 16 us
+// (24 element by element). States stored past the caches; loads that skip them too cost 16.8 us for 256.
+template <typename T, int NPL>
 __global__ __launch_bounds__(kScanBlock) void scan_step_kernel(
     const T* __restrict__ x, const T* __restrict__ dt, const float* __restrict__ A, const T* __restrict__ Bm,
     const T* __restrict__ Cm, const float* __restrict__ skip, const T* __restrict__ z, const float* __restrict__ dt_bias,
     bool softplus, const float* init, int N, int64_t D, int S, int G, int per, T* __restrict__ y, float* fin) {
+  constexpr bool V = NPL % 4 == 0;  // a lane's states in 16-byte pieces, at any address of a float
   const int lane = threadIdx.x & 63, q = lane & 3;
   const int cblocks = G * ((static_cast<int>(D) / G + kScanChannels - 1) / kScanChannels);
   const ScanPlace p = scan_place<kScanChannels>(0, blockIdx.x % cblocks, nullptr, 1, 1, static_cast<int>(D), G, 0);
   const int in = (threadIdx.x >> 6) * 16 + (lane >> 2);
   if (in >= p.cl) return;
   const int c = p.c0 + in, s0 = q * NPL;
+  const bool full = V && s0 + NPL <= S;
   float A2[NPL];
   load_states<NPL>(A + static_cast<int64_t>(c) * S, s0, S, A2);
 #pragma unroll
@@ -347,12 +350,8 @@ __global__ __launch_bounds__(kScanBlock) void scan_step_kernel(
       if (!init) {
 #pragma unroll
         for (int i = 0; i < NPL; ++i) h[u][i] = 0.f;
-      } else if constexpr (V) {
-#pragma unroll
-        for (int i = 0; i < NPL; i += 4) {
-          const f32x4 v = *reinterpret_cast<const f32x4*>(init + at + s0 + i);
-          h[u][i] = v[0]; h[u][i + 1] = v[1]; h[u][i + 2] = v[2]; h[u][i + 3] = v[3];
-        }
+      } else if (full) {
+        if constexpr (V) Pack<float, NPL, true>::load(init + at + s0, h[u], NPL);
       } else {
         load_states<NPL>(init + at, s0, S, h[u]);
       }
@@ -361,9 +360,11 @@ __global__ __launch_bounds__(kScanBlock) void scan_step_kernel(
       zv[u] = z ? Elem<T>::load(z, n * D + c) : 0.f;
       const T* B = Bm + (n * G + p.g) * S + s0;
       const T* C = Cm + (n * G + p.g) * S + s0;
-      if constexpr (V) {
-        Pack<T, NPL, true>::load(B, b[u], NPL);
-        Pack<T, NPL, true>::load(C, cc[u], NPL);
+      if (full) {
+        if constexpr (V) {
+          Pack<T, NPL, true>::load(B, b[u], NPL);
+          Pack<T, NPL, true>::load(C, cc[u], NPL);
+        }
       } else {
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
@@ -388,11 +389,14 @@ __global__ __launch_bounds__(kScanBlock) void scan_step_kernel(
       if (q == 0) Elem<T>::store(y, n * D + c, o);
       if (fin) {
         const int64_t at = (n * D + c) * S;
-        if constexpr (V) {
+        if (full) {
+          if constexpr (V) {
 #pragma unroll
-          for (int i = 0; i < NPL; i += 4)
-            __builtin_nontemporal_store(f32x4{h[u][i], h[u][i + 1], h[u][i + 2], h[u][i + 3]},
-                                        reinterpret_cast<f32x4*>(fin + at + s0 + i));
+            for (int i = 0; i < NPL; i += 4) {
+              const float four[4] = {h[u][i], h[u][i + 1], h[u][i + 2], h[u][i + 3]};
+              Pack<float, 4, true>::template store<true>(fin + at + s0 + i, four, 4);
+            }
+          }
         } else {
           store_states<NPL>(fin + at, s0, S, h[u]);
         }
@@ -474,19 +478,11 @@ template <typename T, int NPL>
 static hipError_t scan_step_t(const ScanArgs& a, hipStream_t st) {
   const int64_t per = scan_step_per(a.N, scan_step_channel_blocks(a.D, a.G));
   const unsigned grid = static_cast<unsigned>(scan_step_blocks(a.N, a.D, a.G));
-  auto run = [&](auto v) {
-    scan_step_kernel<T, NPL, decltype(v)::value><<<grid, kScanBlock, 0, st>>>(
-        static_cast<const T*>(a.x), static_cast<const T*>(a.dt), a.A, static_cast<const T*>(a.Bm),
-        static_cast<const T*>(a.Cm), a.skip, static_cast<const T*>(a.z), a.dt_bias, a.softplus, a.init, a.N, a.D, a.S,
-        a.G, static_cast<int>(per), static_cast<T*>(a.y), a.fin);
-    return hipGetLastError();
-  };
-  if constexpr (NPL % 4 == 0) {
-    const bool v = a.S == 4 * NPL && (reinterpret_cast<uintptr_t>(a.init) & 15) == 0 &&
-                   (reinterpret_cast<uintptr_t>(a.fin) & 15) == 0;
-    if (v) return run(std::true_type{});
-  }
-  return run(std::false_type{});
+  scan_step_kernel<T, NPL><<<grid, kScanBlock, 0, st>>>(
+      static_cast<const T*>(a.x), static_cast<const T*>(a.dt), a.A, static_cast<const T*>(a.Bm),
+      static_cast<const T*>(a.Cm), a.skip, static_cast<const T*>(a.z), a.dt_bias, a.softplus, a.init, a.N, a.D, a.S, a.G,
+      static_cast<int>(per), static_cast<T*>(a.y), a.fin);
+  return hipGetLastError();
 }
 
 hipError_t launch_scan(const ScanArgs& a, const ScanPlan& p, float* hseg, float* dsum, hipStream_t st) {

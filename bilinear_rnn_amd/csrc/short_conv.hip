@@ -189,7 +189,7 @@ __global__ __launch_bounds__(kConvBlock) void conv_step_kernel(
     int64_t D, bool silu, T* __restrict__ y, T* fin) {
   const ConvPos p = conv_pos<E>(static_cast<int>(D), N);
   if (p.done) return;
-  const int c = p.c, nc = p.nc;
+  const int c = V ? whole_group<E>(p.c, D) : p.c, nc = V ? E : p.nc;
   const int64_t n = p.tile, so = n * (W - 1) * D + c;
   float win[W][E], w[W][E], bs[E], o[E];
   Pack<T, E, V>::load(x + n * D + c, win[W - 1], nc);
@@ -472,7 +472,8 @@ static hipError_t conv_w(const ConvArgs& a, bool step, hipStream_t st) {
 
 static hipError_t conv_any(const ConvArgs& a, bool step, hipStream_t st) {
   const int E = a.dtype == COMBA_BF16 ? 8 : 4;
-  const bool v = step ? a.D % E == 0 : a.D >= E;  // every thread has a whole piece of channels
+  // every thread has a whole piece of channels
+  const bool v = a.D % E == 0 || (a.D >= E && !(step && a.fin && a.init == a.fin));
   if (a.dtype == COMBA_BF16) return v ? conv_w<u16, 8, true>(a, step, st) : conv_w<u16, 8, false>(a, step, st);
   return v ? conv_w<float, 4, true>(a, step, st) : conv_w<float, 4, false>(a, step, st);
 }

@@ -87,7 +87,8 @@ def test_backward_without_state_or_its_gradient():
 
 
 @pytest.mark.parametrize("N,D,W,dtype,silu,init", [(1, 1, 2, BF16, True, True), (5, 64, 4, BF16, True, True),
-                                                  (33, 72, 3, F32, False, True), (7, 13, 4, BF16, True, False)])
+                                                  (33, 72, 3, F32, False, True), (7, 13, 4, BF16, True, False),
+                                                  (9, 13, 4, BF16, True, True), (6, 7, 2, F32, True, True)])
 def test_step(N, D, W, dtype, silu, init):
     on, ref = make(N, 1, D, W, dtype, True, init, seed=2)
     x = on["x"].view(N, D)
@@ -161,3 +162,21 @@ def test_values_at_the_edge():
     # tokens 2 .. 5 see the infinity, 4 and 5 through taps of weight 0: 0 * inf is NaN; 5 .. 8 see the NaN
     assert torch.all(torch.isinf(y[0, 2:4])) and torch.all(torch.isnan(y[0, 4:9]))
     assert torch.all(y[0, :2] == 0) and torch.all(y[0, 9:] == 0)
+
+
+@pytest.mark.parametrize("dtype,D", [(BF16, 8), (BF16, 9), (BF16, 23), (F32, 5), (F32, 7), (F32, 4)])
+def test_ragged_channels_equal_those_of_a_wider_tensor(dtype, D):
+    """Every channel is computed by itself: the same bits beside whatever channels."""
+    wide = 24
+    on, _ = make(2, 37, wide, 4, dtype, True, True, seed=31)
+    cut = {k: v if v is None else v[:D].contiguous() if k in ("weight", "bias") else v[..., :D].contiguous()
+           for k, v in on.items()}
+    a, b = (comba.short_conv(v["x"], v["weight"], v["bias"], v["init"]) for v in (on, cut))
+    assert all(torch.equal(p[..., :D], q) for p, q in zip(a, b))
+    a, b = (comba.short_conv_step(v["x"][:, 0].contiguous(), v["weight"], v["bias"], v["init"]) for v in (on, cut))
+    assert all(torch.equal(p[..., :D], q) for p, q in zip(a, b))
+    a, b = (comba.short_conv_bwd(v["x"], v["weight"], v["bias"], v["dy"], v["init"], d_final_state=v["dfin"])
+            for v in (on, cut))
+    for k in a:
+        p = a[k][:D] if k in ("dweight", "dbias") else a[k][..., :D]
+        assert torch.equal(p, b[k]), k
