@@ -13,7 +13,7 @@
 // tokens at a time.
 //
 // Measured, bf16, S = 16, D = 2048: 8 x 4096 tokens 354 to 375 us (2.9e12 states per second; HBM alone
-// would take 87), 1 x 65536 tokens, cut, 890 to 910 us. The uncut scan has the two wavefronts per SIMD
+// would take 87), 1 x 65536 tokens, cut, 890 to 925 us. The uncut scan has the two wavefronts per SIMD
 // that sequences and channels give, and the vector ALU is busy 75 % of the time; the cut one has four
 // and runs at the rate of its instructions, 17.2 per token and wavefront: 10 of the recurrence, 2.1 of
 // the sum over the lanes, 5 of the work per token. Not better: y summed by the matrix cores (16x16x4
