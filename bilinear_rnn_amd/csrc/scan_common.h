@@ -39,7 +39,8 @@ __device__ __forceinline__ void each(F f) {
 // four lanes makes a halving two instructions per result; selecting what to keep and what to send
 // makes it three, and the compiler has no form for the other. Inside the asm: two wait states (an
 // instruction is one) between a register's write and its DPP read, before the first, between the
-// two halvings and behind the last.
+// two halvings and behind the last. The registers written are early clobbers: they are written before
+// the last inputs are read, and without that the compiler gives equal values one register.
 #define COMBA_BIT3(A, B)                                                      \
   "v_add_f32_dpp " A ", " A ", " A " row_ror:8 row_mask:0xf bank_mask:0xf\n\t" \
   "v_add_f32_dpp " A ", " B ", " B " row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
@@ -49,7 +50,7 @@ __device__ __forceinline__ void each(F f) {
 template <int N> __device__ __forceinline__ void halve_bits_3_2(float* v) {
   if constexpr (N == 1) {
     asm("s_nop 1\n\t" COMBA_BIT3("%0", "%2") COMBA_BIT3("%1", "%3") COMBA_BIT2("%0", "%1", "s_nop 0\n\t") "s_nop 1"
-        : "+v"(v[0]), "+v"(v[1])
+        : "+&v"(v[0]), "+&v"(v[1])
         : "v"(v[2]), "v"(v[3]));
   } else {
     static_assert(N % 2 == 0, "1 or pairs");
@@ -57,7 +58,7 @@ template <int N> __device__ __forceinline__ void halve_bits_3_2(float* v) {
     for (int i = 0; i < N; i += 2)
       asm("s_nop 1\n\t" COMBA_BIT3("%0", "%4") COMBA_BIT3("%1", "%5") COMBA_BIT3("%2", "%6") COMBA_BIT3("%3", "%7")
               COMBA_BIT2("%0", "%2", "") COMBA_BIT2("%1", "%3", "") "s_nop 1"
-          : "+v"(v[i]), "+v"(v[i + 1]), "+v"(v[i + N]), "+v"(v[i + 1 + N])
+          : "+&v"(v[i]), "+&v"(v[i + 1]), "+&v"(v[i + N]), "+&v"(v[i + 1 + N])
           : "v"(v[i + 2 * N]), "v"(v[i + 1 + 2 * N]), "v"(v[i + 3 * N]), "v"(v[i + 1 + 3 * N]));
   }
 }
