@@ -99,6 +99,15 @@ __device__ __forceinline__ float decay_rate(float A) {
   return r < -3.4028235e38f ? -3.4028235e38f : r;
 }
 
+// own + 2^p h: a state carried over a segment whose decays multiply to 2^p. Where that factor leaves
+// float32's range, as it does for states that grow, h may be 0 or small enough for the product to be
+// finite: it is then scaled by the factor's mantissa and exponent one after the other.
+__device__ __forceinline__ float carried(float h, float p, float own) {
+  if (fabsf(p) < 126.f) return fmaf(__builtin_amdgcn_exp2f(p), h, own);
+  const float n = rintf(__builtin_amdgcn_fmed3f(p, -1e5f, 1e5f));
+  return own + __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f(p - n) * h, static_cast<int>(n));
+}
+
 // A workgroup's place: segment [t0, t1) of sequence n in batch row b, channels from c0 on.
 struct ScanPlace {
   int n, b, seg, t0, t1, s0, s1;   // s0, s1: the whole sequence

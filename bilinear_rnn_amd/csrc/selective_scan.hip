@@ -311,7 +311,7 @@ __global__ __launch_bounds__(kScanBlock) void scan_carry_kernel(const float* __r
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (k + u < segs) hp[(k + u) * D * SP] = h;
-      h = fmaf(__builtin_amdgcn_exp2f(A2 * d[u]), h, end[u]);
+      h = carried(h, A2 * d[u], end[u]);
     }
   }
 }

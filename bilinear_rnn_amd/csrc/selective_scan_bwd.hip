@@ -9,7 +9,8 @@
 //
 // Every sequence is cut into segments of L tokens that run in parallel:
 //   1. scan_bwd_ends: each segment's end state from 0, its gradient of its incoming state for no
-//      gradient behind it, and its sum of step sizes (the map of both is exp(A sum d));
+//      gradient behind it, and its sum of step sizes (the map of both is exp(A sum d)); a second time for
+//      the gradients where the decays' product overflowed, as growing states make it;
 //   2. scan_bwd_carry: the true incoming states and outgoing gradients, along the segments;
 //   3. scan_bwd: per segment the states at every CT-th token forward, then from its end the CT tokens
 //      of each piece: states and decays recomputed into registers, then the reverse recurrence;
@@ -230,18 +231,24 @@ __global__ __launch_bounds__(kScanBlock) void scan_bwd_ends_kernel(ScanBwdK<T> a
   }
   const int len = p.t1 - p.t0;
   float dtot = 0.f;
-  for (int t = 0, buf = 0; t < len; t += TT, buf ^= 1) {
+  // Stages the segment piece by piece, the first one fetched before, and calls tokens(buffer) for each.
+  auto pieces = [&](auto tokens) {
+    for (int t = 0, buf = 0; t < len; t += TT, buf ^= 1) {
 #pragma unroll
-    for (int j = 0; j < pc.R; ++j) {
-      float s;
-      const float d = pc.step(a, p, t, j), g = pc.grad(a, j, s);
-      dtot += d;
-      st[buf][pc.tk + 4 * j][pc.ch] = f32x4{d, d * Range<T>::value(pc.rx[j]), g, 0.f};
+      for (int j = 0; j < pc.R; ++j) {
+        float s;
+        const float d = pc.step(a, p, t, j), g = pc.grad(a, j, s);
+        dtot += d;
+        st[buf][pc.tk + 4 * j][pc.ch] = f32x4{d, d * Range<T>::value(pc.rx[j]), g, 0.f};
+      }
+      pb.template put<NPL>(bc[buf]);
+      pc.template fetch<true>(a, p, t + TT);
+      pb.fetch(a, p, t + TT);
+      __syncthreads();  // the other buffer is written only behind the next one
+      tokens(buf);
     }
-    pb.template put<NPL>(bc[buf]);
-    pc.template fetch<true>(a, p, t + TT);
-    pb.fetch(a, p, t + TT);
-    __syncthreads();  // the other buffer is written only behind the next one
+  };
+  pieces([&](int buf) {
 #pragma unroll
     for (int k = 0; k < TT; ++k) {
       const f32x4 e4 = st[buf][k][in];
@@ -260,18 +267,48 @@ __global__ __launch_bounds__(kScanBlock) void scan_bwd_ends_kernel(ScanBwdK<T> a
           pin(gs[i]);
         }
     }
-  }
+  });
   tot[pc.tk][pc.ch] = dtot;
-  __syncthreads();
+  bool over = false;
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) over |= !(pr[i] < INFINITY);
+  over = __syncthreads_or(over);
   if (tid < kScanChannels && pc.live)
     a.dsum[p.slot * a.D + p.c0 + tid] = (tot[0][tid] + tot[1][tid]) + (tot[2][tid] + tot[3][tid]);
-  if (!live) return;
   const int64_t at = (p.slot * a.D + c) * SP + q * NPL;
+  if (live)
 #pragma unroll
-  for (int i = 0; i < NPL; ++i) {
-    a.hseg[at + i] = h[i];
-    a.gseg[at + i] = gs[i];
+    for (int i = 0; i < NPL; ++i) a.hseg[at + i] = h[i];
+  if (over) {
+    // A product of decays overflowed: a growing state. What it multiplies may be 0 or small enough for
+    // a finite sum, so the sums are formed again with the products' exponents kept apart.
+    int ex[NPL];
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+      gs[i] = 0.f;
+      pr[i] = 1.f;
+      ex[i] = 0;
+    }
+    pc.template fetch<true>(a, p, 0);
+    pb.fetch(a, p, 0);
+    pieces([&](int buf) {
+#pragma unroll 1
+      for (int k = 0; k < TT; ++k) {
+        const f32x4 e4 = st[buf][k][in];
+        const float* r = bc[buf][k][q];
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+          pr[i] *= __builtin_amdgcn_exp2f(e4[0] * A2[i]);
+          ex[i] += __builtin_amdgcn_frexp_expf(pr[i]);
+          pr[i] = __builtin_amdgcn_frexp_mantf(pr[i]);
+          gs[i] += __builtin_amdgcn_ldexpf(pr[i] * (e4[2] * r[NPL + i]), ex[i]);
+        }
+      }
+    });
   }
+  if (live)
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) a.gseg[at + i] = gs[i];
 }
 
 // One thread per (direction, sequence, channel, state): hseg becomes the segments' incoming states,
@@ -310,7 +347,7 @@ __global__ __launch_bounds__(kScanBlock) void scan_bwd_carry_kernel(
     for (int u = 0; u < U; ++u) {
       if (k + u < segs) {
         hp[(back ? segs - 1 - k - u : k + u) * D * SP] = h;
-        h = fmaf(__builtin_amdgcn_exp2f(A2 * d[u]), h, own[u]);
+        h = carried(h, A2 * d[u], own[u]);
       }
     }
   }
