@@ -94,9 +94,12 @@ __device__ __forceinline__ void pin(float& x) { asm volatile("" : "+v"(x)); }
 
 constexpr float kLog2E = 1.44269504088896340736f;
 
-// 1 / (1 + e^-x) from the hardware exponential and reciprocal (about 1 ulp each): relative
-// error a few 2^-24, far below the rounding of a bf16 result and within float32's own.
-// e^-x overflows to infinity for x < -88, where the result is 0, as it should be to float32.
+// 1 / (1 + e^-x) from the hardware exponential and reciprocal (about 1 ulp, 2 2^-24, each). The
+// exponential's argument, x log2(e), is rounded to float32 with the constant's own 0.2 2^-24, which
+// e^-x shows as 1.3 |x| 2^-24: the relative error is up to (5 + 1.3 |x|) 2^-24 for negative x (31 2^-24 at
+// -20) and 6 2^-24 for positive x, where e^-x is small beside the 1. Below the rounding of a bf16 result
+// over the whole range, above that of a float32 one. e^-x overflows to infinity for x < -88, where
+// the result is 0 instead of something below 6e-39.
 __device__ __forceinline__ float sigmoid_fast(float x) {
   return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-kLog2E * x));
 }
