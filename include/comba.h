@@ -56,6 +56,12 @@
 extern "C" {
 #endif
 
+/*
+ * Rises when the signature or the meaning of an existing entry point changes.
+ * Entry points that are only added leave it (comba_check_inputs, which raised
+ * it to 6, was added before this rule): a caller that needs one of them looks
+ * it up by name.
+ */
 #define COMBA_ABI_VERSION 6
 
 /* Status codes returned by every entry point. */
@@ -439,16 +445,13 @@ int32_t comba_lds_probe(int32_t kind, const int32_t* lane_offsets, int32_t iters
  * - `dtype` (COMBA_BF16 or COMBA_FP32) is the type of every activation and of
  *   its gradient; parameters, their gradients and recurrent states are
  *   float32. All arithmetic is float32, each output is rounded once.
- * - Channel counts are free. 16-byte aligned tensors whose rows are multiples
- *   of 16 bytes take the fast path; any other address that is aligned to its
- *   elements works.
+ * - Channel counts are free, and so are addresses that are aligned to their
+ *   elements.
  * - With cu_seqlens, tokens before cu_seqlens[0] or from cu_seqlens[N] on
  *   belong to no sequence: they are not read, and their rows of an output are
  *   left as they were.
  * - Outputs and the workspace must not overlap inputs or each other, except
  *   where a state may be updated in place as stated (COMBA_ERR_INVALID_ARG).
- * COMBA_ABI_VERSION stays while existing entry points keep their signature
- * and meaning; a caller that needs an added one looks it up by name.
  */
 
 /*
