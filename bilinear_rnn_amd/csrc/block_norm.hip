@@ -11,9 +11,18 @@
 // up to 512 columns (several rows per wavefront, reductions without LDS), a workgroup above 1024.
 // Workgroups walk over many rows with the parameters in registers, and load the next row before they
 // work on the present one. Parts that are not given read 0 from an empty range, without a branch.
-// Measured, bf16: gated norm of 524288 rows of 128 63 us (6.4 TB/s; 93 without the row ahead and the
-// streaming stores); the seam's backward with all parts, 8192 rows of 2048, 60 us with the parameter
-// sums (4.5 TB/s); the seam for 33 rows of 2047 in fp32 4.2 us, of which a launch takes most.
+// Measured, bf16, with inputs that change from call to call: gated norm of 524288 rows of 128 76 us
+// (5.3 TB/s); the seam's backward with all parts, 8192 rows of 2048, 65 to 71 us with the parameter sums
+// (3.8 to 4.1 TB/s); the seam for 33 rows of 2047 in fp32 4.2 us, of which a launch takes most. With the same
+// inputs again, part of which the last-level cache then holds, 64 and 60 us (93 the former without the
+// row ahead and the streaming stores); so were the comparisons below taken.
+// Far from HBM's rate above 8192 columns, where 1024 threads may have 128 registers each: the backward
+// spills 285 to 334 of them, and 1024 rows of 16384 with all parts take 430 us in bf16 and 487 in fp32 (0.6
+// and 1.1 TB/s; forward 55 and 72 us). The backward of 4097 to 8192 columns spills where it takes single
+// elements (78 registers in bf16, 48 in fp32) and 6 in fp32 with pieces: 2048 rows of 8192 89 us in bf16,
+// 125 in fp32 (3.0 and 4.3 TB/s). Rows of odd widths, whose elements are read one by one, cost no more than
+// their neighbours: 8192 rows of 2047 / 2048, all parts, forward 36 / 43 us in bf16, 64 / 64 in fp32,
+// backward 66 / 68 and 118 / 114.
 #include "column_sums.h"
 #include "comba.h"
 #include "launch.h"

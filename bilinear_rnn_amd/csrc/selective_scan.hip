@@ -5,16 +5,17 @@
 //   y_t = (sum_s C_t[g, s] h_t[s] + skip x_t) z_t sigmoid(z_t)
 // The state and all sums are float32; y is rounded once.
 //
-// Per (token, channel, state) one exponential, three multiplications and two fused multiply-adds
+// Per (token, channel, state) one exponential, two multiplications and two fused multiply-adds
 // against 8 / S bytes of HBM per state (bf16): at S = 16 the vector ALU is the bound, not HBM, and
 // since A differs per channel and state no matrix product can take the work over. The kernel
-// therefore keeps everything but those six instructions out of the inner loop: B, C, step sizes and
+// therefore keeps everything but those five instructions out of the inner loop: B, C, step sizes and
 // inputs as float32 in LDS, formed once; sums over the states halved over the channel's lanes, eight
 // tokens at a time.
 //
-// Measured, bf16, S = 16, D = 2048: 8 x 4096 tokens 354 to 375 us (2.9e12 states per second; HBM alone
-// would take 87), 1 x 65536 tokens, cut, 890 to 925 us. The uncut scan has the two wavefronts per SIMD
-// that sequences and channels give, and the vector ALU is busy 75 % of the time; the cut one has four
+// Measured, bf16, S = 16, D = 2048: 8 x 4096 tokens 350 to 357 us once the clock has settled, up to 380
+// in the first fifty launches (3.0e12 states per second; HBM alone would take 87), 1 x 65536 tokens, cut,
+// 890 to 945 us; 8 x 4096 with 4 states 281 us, with 16 in fp32 372. The uncut scan has the two wavefronts per
+// SIMD that sequences and channels give, and the vector ALU is busy 75 to 78 % of the time; the cut one has four
 // and runs at the rate of its instructions, 17.2 per token and wavefront: 10 of the recurrence, 2.1 of
 // the sum over the lanes, 5 of the work per token. Not better: y summed by the matrix cores (16x16x4
 // fp32 blocks hold the SIMD for 32 cycles each: 515 us against 421 then), the work per token spread
@@ -318,9 +319,9 @@ __global__ __launch_bounds__(kScanBlock) void scan_carry_kernel(const float* __r
 
 // One token per sequence: the state is read once and written once, 8 S bytes per channel: bound by
 // HBM. Four lanes per channel, a workgroup takes several sequences with A in registers, two
-// sequences' loads in flight. Measured at D = 2048, S = 16, bf16, in place: 13.5 us for 256 sequences
-// (5.3 TB/s; 19.6 us with one sequence's loads in flight and B and C element by element), 101 us for
-// 2048 (5.5 TB/s); 256 with 13 states, whose rows start anywhere, 16 us
+// sequences' loads in flight. Measured at D = 2048, S = 16, bf16, in place: 13.5 to 15 us for 256
+// sequences (4.8 to 5.3 TB/s; 19.6 us with one sequence's loads in flight and B and C element by element),
+// 101 to 117 us for 2048 (4.9 to 5.6 TB/s); 256 with 13 states, whose rows start anywhere, 16 us
 // (24 element by element). States stored past the caches; loads that skip them too cost 16.8 us for 256.
 template <typename T, int NPL>
 __global__ __launch_bounds__(kScanBlock) void scan_step_kernel(

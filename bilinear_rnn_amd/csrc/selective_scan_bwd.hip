@@ -19,12 +19,14 @@
 // Where no sequence can be longer than a segment (T <= L), 3 starts from the given states itself and
 // writes d_initial_state: two launches instead of four, which is what a short batch's time is made of.
 // Nothing is kept from the forward. Bound by the vector ALU like the forward: three exponentials and
-// about 25 instructions per (token, channel, state). The sums over the 16 channels of a wavefront
+// 38 instructions per (token, channel, state), 9 of them in 1 and 29 in 3. The sums over the 16 channels of a wavefront
 // halve the values at every step. Through LDS instead (terms written, one sum per lane read back) the
 // vector ALU has 12 % less to do, but the kernel waits for LDS longer than that: 316 us against 300 at
 // B = 4, T = 2048, D = 2048, S = 16.
-// Measured there, bf16: 357 to 360 us in all: 78 (1), 10 (2), 283 (3), 9 (4), without the gaps.
-// The vector ALU is busy 75 % of 3's time, at two wavefronts per SIMD (240 registers: 16 tokens'
+// Measured there, bf16, once the clock has settled: 359 to 369 us in all: 76 (1), 10 (2), 271 (3), 8.5 (4);
+// in fp32 367 to 375. 8 x 4096 tokens 1370 us. 4 x 2048 tokens of 1024 channels with 32 states 506 us, with 64,
+// at one wavefront per SIMD, 1370; of 2048 channels with 8 states 220 (two registers spilled for a
+// third wavefront). The vector ALU is busy 79 to 83 % of 3's time, at two wavefronts per SIMD (240 registers: 16 tokens'
 // states and decays; 61 KB of LDS). HBM moves 0.33 GB in 3.
 #include <utility>
 

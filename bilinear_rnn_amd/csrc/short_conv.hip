@@ -6,11 +6,13 @@
 // bytes of channels and walks along a tile of tokens with the last W - 1 inputs in registers, so
 // that every input is loaded once per tile; eight loads are in flight before the first is used.
 // Sums and the SiLU are float32, the output is rounded once. Measured, W = 4, bf16:
-//   8 x 4096 tokens of 2048 channels: 46 us, 5.8 TB/s of the 6.2 that an elementwise sum reaches
-//   (56 us with loads only at natural alignment and stores through the caches); fp32, W = 3,
-//   15001 packed tokens of 1001 channels, whose rows start anywhere: 25 us, 4.8 TB/s (35 us with
-//   element loads);
+//   8 x 4096 tokens of 2048 channels: 56 to 59 us, 4.6 to 4.8 TB/s, of the 5.2 that a copy and the 6.2
+//   that an elementwise sum reach; 45 to 47 us where the input is the one of the call before, part of
+//   which the last-level cache then holds (56 so with loads only at natural alignment and stores
+//   through the caches). fp32, W = 3, 15001 packed tokens of 1001 channels, whose rows start anywhere:
+//   25 us, 4.8 TB/s (35 us with element loads);
 //   one token for 256 sequences: 4.8 us, of which a launch takes most.
+// The comparisons below were taken with the same inputs call after call.
 #include "comba.h"
 #include "column_sums.h"
 #include "launch.h"
@@ -227,9 +229,10 @@ __device__ __forceinline__ void silu_grad(const float (&p)[E], float (&d)[E]) {
 // gradients: one float32 partial sum per four tiles, added up in a fixed order by a second kernel.
 // The last N items form the gradients of the initial states from the first W - 1 tokens.
 // Bound by HBM in principle (x and dy read, dx written); measured, 4 x 2048 tokens of 2048 bf16
-// channels, W = 4: 28 us with the parameter sums, 3.6 TB/s, 80 us (5.0 TB/s) for 8 x 4096. The
-// smaller one has two wavefronts per SIMD, each with eight loads in flight: too few; four channels
-// per thread and sums over four tiles in LDS took it from 48 to 28 us.
+// channels, W = 4: 35 us with the parameter sums, 2.9 TB/s, 27 us where the last-level cache holds part
+// of the inputs; 93 us (4.3 TB/s) for 8 x 4096, in cache 83; 47 us (4.3 TB/s) for 4 x 2048 in fp32. The
+// smaller one has two wavefronts per SIMD, each with eight loads in flight and none while it works on
+// them: too few; four channels per thread and sums over four tiles in LDS took it from 48 to 28 us.
 template <typename T, typename G, int E, bool V, int W>
 __global__ __launch_bounds__(kConvBlock) void conv_bwd_kernel(
     const T* __restrict__ x, const float* __restrict__ weight, const float* __restrict__ bias,
