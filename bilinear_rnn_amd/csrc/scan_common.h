@@ -106,7 +106,7 @@ __device__ __forceinline__ float decay_rate(float A) {
 // finite: it is then scaled by the factor's mantissa and exponent one after the other.
 __device__ __forceinline__ float carried(float h, float p, float own) {
   if (fabsf(p) < 126.f) return fmaf(__builtin_amdgcn_exp2f(p), h, own);
-  const float n = rintf(__builtin_amdgcn_fmed3f(p, -1e5f, 1e5f));
+  const float n = rintf(__builtin_amdgcn_fmed3f(p, -1e9f, 1e9f));
   return own + __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f(p - n) * h, static_cast<int>(n));
 }
 

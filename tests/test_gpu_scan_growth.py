@@ -149,3 +149,21 @@ def test_backward_of_tiny_states_and_gradients():
     on, ref, grow, per = make(1, sum(lens), 48, 16, 1, F32, lens, 6.6, edit)
     assert 16 * 6.6 * 0.9 > 89 and per * 18 < 69 + 80
     backward(on, ref, lens, True, 40, per * 18, 48, 1, sum(lens))
+
+
+def test_a_state_of_zero_over_the_longest_segments():
+    """Decays of 2^125 per token, the largest that are finite, over segments of 900 tokens and more: 2^112500."""
+    N, D = 256, 64
+    lens = [880] * (N - 1) + [5000]
+    T = sum(lens)
+    # enough sequences: segments of their mean length
+    assert comba.selective_scan_workspace_size(1, T, D, 4, 1, N) > 0
+    zero, one = torch.zeros(1, T, D, device="cuda"), torch.ones(1, T, D, device="cuda")
+    A = torch.full((D, 4), 125 * float(np.log(2)), device="cuda")
+    A[D // 2:] = -1
+    bc = torch.ones(1, T, 1, 4, device="cuda")
+    x = zero.clone()
+    x[..., D // 2:] = 1
+    y, f = comba.selective_scan(x, one, A, bc, bc, softplus=False, cu_seqlens=cu_dev(cu_of(lens)))
+    assert torch.all(y[..., :D // 2] == 0) and torch.all(f[:, :D // 2] == 0)
+    assert torch.isfinite(y).all() and torch.isfinite(f).all() and torch.all(f[:, D // 2:] > 1)
