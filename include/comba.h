@@ -506,10 +506,10 @@ int32_t comba_short_conv_bwd(const void* x, const float* weight, const float* bi
  *     y_t    = (sum_s Cm_t[g, s] h_t[s] + skip x_t) * z_t sigmoid(z_t)
  *   x, dt, z, y    [B, T, D]        dtype; z may be NULL (no gate)
  *   A              [D, S]           float32 (negative for a decay; not checked.
- *                                   States may grow: a result is finite where
- *                                   every token's exp(d A), state and, in the
- *                                   backward, gradient of a state are, however
- *                                   large a product of several exp(d A) is.
+ *                                   States may grow: a product of exp(d A) over
+ *                                   several tokens may leave float32's range,
+ *                                   one token's, a state and, in the backward,
+ *                                   a gradient of a state may not.
  *                                   -infinity keeps nothing of the state, but
  *                                   all of it where d is 0)
  *   Bm, Cm         [B, T, G, S]     dtype; G divides D
