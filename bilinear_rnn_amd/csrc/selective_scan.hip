@@ -14,7 +14,7 @@
 //
 // Measured, bf16, S = 16, D = 2048: 8 x 4096 tokens 350 to 357 us once the clock has settled, up to 380
 // in the first fifty launches (3.0e12 states per second; HBM alone would take 87), 1 x 65536 tokens, cut,
-// 890 to 945 us; 8 x 4096 with 4 states 281 us, with 16 in fp32 372. The uncut scan has the two wavefronts per
+// 882 to 945 us; 8 x 4096 with 4 states 281 us, with 16 in fp32 372. The uncut scan has the two wavefronts per
 // SIMD that sequences and channels give, and the vector ALU is busy 75 to 78 % of the time; the cut one has four
 // and runs at the rate of its instructions, 17.2 per token and wavefront: 10 of the recurrence, 2.1 of
 // the sum over the lanes, 5 of the work per token. Not better: y summed by the matrix cores (16x16x4

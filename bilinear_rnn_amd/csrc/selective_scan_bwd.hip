@@ -23,7 +23,7 @@
 // halve the values at every step. Through LDS instead (terms written, one sum per lane read back) the
 // vector ALU has 12 % less to do, but the kernel waits for LDS longer than that: 316 us against 300 at
 // B = 4, T = 2048, D = 2048, S = 16.
-// Measured there, bf16, once the clock has settled: 359 to 369 us in all: 76 (1), 10 (2), 271 (3), 8.5 (4);
+// Measured there, bf16, once the clock has settled: 356 to 369 us in all: 76 (1), 10 (2), 271 (3), 8.5 (4);
 // in fp32 367 to 375. 8 x 4096 tokens 1370 us. 4 x 2048 tokens of 1024 channels with 32 states 506 us, with 64,
 // at one wavefront per SIMD, 1370; of 2048 channels with 8 states 220 (two registers spilled for a
 // third wavefront). The vector ALU is busy 79 to 83 % of 3's time, at two wavefronts per SIMD (240 registers: 16 tokens'

@@ -509,7 +509,8 @@ int32_t comba_short_conv_bwd(const void* x, const float* weight, const float* bi
  *                                   States may grow: a product of exp(d A) over
  *                                   several tokens may leave float32's range,
  *                                   one token's, a state and, in the backward,
- *                                   a gradient of a state may not.
+ *                                   a gradient of a state may not. Where d x is
+ *                                   infinite, y is infinite or NaN from there on.
  *                                   -infinity keeps nothing of the state, but
  *                                   all of it where d is 0)
  *   Bm, Cm         [B, T, G, S]     dtype; G divides D
