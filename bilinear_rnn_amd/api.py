@@ -48,7 +48,9 @@ EXPORTED = ("comba_abi_version", "comba_status_string", "comba_last_error",
             "comba_short_conv_fwd", "comba_short_conv_step", "comba_short_conv_bwd_workspace_size",
             "comba_short_conv_bwd", "comba_selective_scan_workspace_size", "comba_selective_scan_fwd",
             "comba_selective_step", "comba_selective_scan_bwd_workspace_size", "comba_selective_scan_bwd",
-            "comba_block_norm_fwd", "comba_block_norm_bwd_workspace_size", "comba_block_norm_bwd")
+            "comba_block_norm_fwd", "comba_block_norm_bwd_workspace_size", "comba_block_norm_bwd",
+            "comba_linear_attn_workspace_size", "comba_linear_attn_fwd", "comba_linear_attn_step",
+            "comba_linear_attn_bwd_workspace_size", "comba_linear_attn_bwd")
 
 
 class CombaError(RuntimeError):
@@ -157,6 +159,18 @@ def lib() -> ctypes.CDLL:
         L.comba_block_norm_bwd.argtypes = [vp, vp, vp, fp, fp, fp, i64, i32, f32, i32, vp, vp, vp, vp, vp, fp, fp,
                                            fp, vp, sz, vp]
         L.comba_block_norm_bwd.restype = i32
+        L.comba_linear_attn_workspace_size.argtypes = [i32] * 7
+        L.comba_linear_attn_workspace_size.restype = sz
+        L.comba_linear_attn_fwd.argtypes = [vp, vp, vp, fp, i32, fp, ip, i32, i32, i32, i32, i32, i32, i32, i32, f32,
+                                            vp, fp, vp, sz, vp]
+        L.comba_linear_attn_fwd.restype = i32
+        L.comba_linear_attn_step.argtypes = [vp, vp, vp, fp, i32, fp, i32, i32, i32, i32, i32, i32, f32, vp, fp, vp]
+        L.comba_linear_attn_step.restype = i32
+        L.comba_linear_attn_bwd_workspace_size.argtypes = [i32] * 7
+        L.comba_linear_attn_bwd_workspace_size.restype = sz
+        L.comba_linear_attn_bwd.argtypes = [vp, vp, vp, fp, i32, fp, ip, i32, i32, i32, i32, i32, i32, i32, i32, f32,
+                                            vp, fp, vp, vp, vp, fp, fp, vp, sz, vp]
+        L.comba_linear_attn_bwd.restype = i32
         _lib = L
     return _lib
 
@@ -858,6 +872,102 @@ def block_norm_bwd(y: torch.Tensor, dr: Optional[torch.Tensor] = None, dn: Optio
          _at(y), _at(gate), _at(residual), _at(scale), _at(post_weight), _at(pre_weight), rows, D, float(eps),
          _DT[y.dtype], _at(dr), _at(dn), _at(g["dy"]), _at(g["dgate"]), _at(g["dresidual"]),
          _at(g["dscale"]), _at(g["dpost_weight"]), _at(g["dpre_weight"]), *_ws(workspace))
+    return g
+
+
+def _attn_args(q, k, v, log_decay, initial_state, N, scale, index):
+    rows = tuple(q.shape[:-2])
+    Hk, K = q.shape[-2:]
+    _need(k, "k", q.dtype, q.shape, index)
+    if not isinstance(v, torch.Tensor) or v.dim() != q.dim():
+        raise ValueError(f"v must be [{'B, T' if len(rows) == 2 else 'N'}, H, V]")
+    H, V = v.shape[-2:]
+    if Hk < 1 or H % Hk != 0:
+        raise ValueError(f"the q / k head count {Hk} must divide the value head count {H}")
+    _need(v, "v", q.dtype, rows + (H, V), index)
+    per_token = not (isinstance(log_decay, torch.Tensor) and log_decay.dim() == 1)
+    _need(log_decay, "log_decay", torch.float32, rows + (H,) if per_token else (H,), index)
+    _may(initial_state, "initial_state", torch.float32, (N, H, V, K), index)
+    return H, Hk, K, V, int(per_token), float(scale)
+
+
+def linear_attention_workspace_size(B: int, T: int, H: int, Hk: int, K: int, V: int, num_seqs: int = 0) -> int:
+    return int(lib().comba_linear_attn_workspace_size(B, T, H, Hk, K, V, num_seqs))
+
+
+def linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
+                     initial_state: Optional[torch.Tensor] = None, cu_seqlens: Optional[torch.Tensor] = None,
+                     scale: float = 1.0, output_final_state: bool = True, out: Optional[torch.Tensor] = None,
+                     final_state: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Linear attention with a decay for each head, S_t = exp(g_t) S_{t-1} + v_t k_t^T, o_t = scale S_t q_t,
+    through ``comba_linear_attn_fwd``. q, k [B, T, Hk, K] (Hk divides H: consecutive value heads share one
+    q / k head), v [B, T, H, V], log_decay [B, T, H] or, constant in time, [H] in float32. Returns
+    (o, final_state), the state [N, H, V, K] in float32."""
+    index = _activation(q, "q", 4)
+    B, T = q.shape[:2]
+    N = _sequences(B, T, cu_seqlens, index)
+    H, Hk, K, V, per_token, scale = _attn_args(q, k, v, log_decay, initial_state, N, scale, index)
+    if out is None:
+        out = torch.empty_like(v)
+    else:
+        _need(out, "out", q.dtype, v.shape, index)
+    if final_state is not None or not output_final_state:
+        _may(final_state, "final_state", torch.float32, (N, H, V, K), index)
+    else:
+        final_state = _new_state(q, initial_state, (N, H, V, K), torch.float32)
+    nseq = N if cu_seqlens is not None else 0
+    workspace = _workspace(workspace, linear_attention_workspace_size(B, T, H, Hk, K, V, nseq), q)
+    _run(lib().comba_linear_attn_fwd, index,
+         _at(q), _at(k), _at(v), _at(log_decay), per_token, _at(initial_state), _at(cu_seqlens), nseq, B, T, H, Hk, K, V,
+         _DT[q.dtype], scale, _at(out), _at(final_state), *_ws(workspace))
+    return out, final_state
+
+
+def linear_attention_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
+                          initial_state: Optional[torch.Tensor] = None, scale: float = 1.0, in_place: bool = False,
+                          output_final_state: bool = True, out: Optional[torch.Tensor] = None,
+                          final_state: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """One token per sequence through ``comba_linear_attn_step``: q, k [N, Hk, K], v [N, H, V], log_decay
+    [N, H] or [H]. With ``in_place`` the state is updated in ``initial_state`` itself. Returns
+    (o, final_state)."""
+    index = _activation(q, "q", 3)
+    N = q.shape[0]
+    H, Hk, K, V, per_token, scale = _attn_args(q, k, v, log_decay, initial_state, N, scale, index)
+    if out is None:
+        out = torch.empty_like(v)
+    else:
+        _need(out, "out", q.dtype, v.shape, index)
+    final_state = _step_state(q, initial_state, final_state, in_place, output_final_state, (N, H, V, K), torch.float32,
+                              index)
+    _run(lib().comba_linear_attn_step, index,
+         _at(q), _at(k), _at(v), _at(log_decay), per_token, _at(initial_state), N, H, Hk, K, V, _DT[q.dtype], scale,
+         _at(out), _at(final_state))
+    return out, final_state
+
+
+def linear_attention_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor, do: torch.Tensor,
+                         initial_state: Optional[torch.Tensor] = None, cu_seqlens: Optional[torch.Tensor] = None,
+                         d_final_state: Optional[torch.Tensor] = None, scale: float = 1.0,
+                         workspace: Optional[torch.Tensor] = None) -> dict:
+    """Gradients of ``linear_attention`` through ``comba_linear_attn_bwd``, from its inputs alone. Returns dq,
+    dk (summed over the value heads that share them) and dv in q's type, dlog_decay (of log_decay's shape)
+    and dinitial_state (None without an initial state) in float32."""
+    index = _activation(q, "q", 4)
+    B, T = q.shape[:2]
+    N = _sequences(B, T, cu_seqlens, index)
+    H, Hk, K, V, per_token, scale = _attn_args(q, k, v, log_decay, initial_state, N, scale, index)
+    _need(do, "do", q.dtype, v.shape, index)
+    _may(d_final_state, "d_final_state", torch.float32, (N, H, V, K), index)
+    nseq = N if cu_seqlens is not None else 0
+    L = lib()
+    g = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v), dlog_decay=torch.empty_like(log_decay),
+             dinitial_state=None if initial_state is None else torch.empty_like(initial_state))
+    workspace = _workspace(workspace, int(L.comba_linear_attn_bwd_workspace_size(B, T, H, Hk, K, V, nseq)), q)
+    _run(L.comba_linear_attn_bwd, index,
+         _at(q), _at(k), _at(v), _at(log_decay), per_token, _at(initial_state), _at(cu_seqlens), nseq, B, T, H, Hk, K, V,
+         _DT[q.dtype], scale, _at(do), _at(d_final_state), _at(g["dq"]), _at(g["dk"]), _at(g["dv"]), _at(g["dlog_decay"]),
+         _at(g["dinitial_state"]), *_ws(workspace))
     return g
 
 

@@ -1,0 +1,178 @@
+// Tiles of the decayed linear attention in LDS and the matrix-core operands built from them, for
+// bf16 and float32 inputs.
+//
+// A product's operands and results are 16 x 16 tiles: lane l (g = l / 16, l16 = l % 16) holds rows
+// 4 g + i, i < 4, of column l16 of a result, and for an operand row (or column) l16 with BLK / 4
+// reduction indices. Those indices are chosen such that the registers of a result are an operand
+// of the next product as they stand:
+//   bf16     blocks of 32 indices; a lane has 8 of them, the rows 4 g + i of two result tiles
+//   float32  blocks of 16 indices; a lane has the 4 rows of one result tile
+// A float32 value enters a bf16 product as NT bf16 terms whose sum is the value to 8 NT bits
+// (three: exactly, but for the last bit).
+#pragma once
+
+#include <type_traits>
+
+#include "layer_common.h"
+
+namespace comba {
+
+template <typename T> struct Tiles;
+
+template <> struct Tiles<u16> {
+  static constexpr int CH = 64;         // tokens per chunk
+  static constexpr int BLK = 32;        // reduction indices per block
+  static constexpr int PIECE = 8;       // elements of 16 bytes
+  typedef bf16x8 Frag;
+  typedef u16 P;                        // element of the score tiles
+  // Elements of an LDS tile of R rows of L elements, and an element's place. Whole 16-byte pieces stay whole.
+  static constexpr int size(int R, int L) { return R * L; }
+  template <int L> static __device__ __forceinline__ int at(int row, int col) { return swz<L>(row, col); }
+  // Result row 4 g + i of tile j of a reduction axis <-> index on that axis.
+  static __device__ __forceinline__ int index(int j, int g, int i) { return 32 * (j >> 1) + 8 * g + 4 * (j & 1) + i; }
+  // Operand whose reduction runs along a tile's row: block p of row `row`.
+  template <int L> static __device__ __forceinline__ Frag along(const u16* t, int row, int p, int g) {
+    return lds8(t + swz<L>(row, 32 * p + 8 * g));
+  }
+  // Operand whose reduction runs down the rows (block b of 32 rows), for column tile j in index() order.
+  template <int L> static __device__ __forceinline__ Frag down_index(const u16* t, int b, int j, int g, int l16) {
+    return tr_frag<L>(t, 32 * b, 32 * (j >> 1) + 8 * (l16 & 3) + 4 * (j & 1), g, l16);
+  }
+  // The same for the 16 neighbouring columns from col0 on.
+  template <int L> static __device__ __forceinline__ Frag down(const u16* t, int b, int col0, int g, int l16) {
+    return tr_frag<L>(t, 32 * b, col0 + 4 * (l16 & 3), g, l16);
+  }
+  // Row of the block that element e of a `down` operand came from.
+  static __device__ __forceinline__ int down_row(int g, int e) { return 4 * g + (e & 3) + 16 * (e >> 2); }
+  static __device__ __forceinline__ float value(const Frag& f, int e) {
+    const u32x4 w = __builtin_bit_cast(u32x4, f);
+    return __uint_as_float(e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16);
+  }
+  static constexpr int TERMS(int nt) { return nt; }
+  // NT terms of eight values.
+  template <int NT> static __device__ __forceinline__ void split(const float (&x)[8], Frag (&out)[NT]) {
+    unsigned w[NT][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float a = x[2 * i], b = x[2 * i + 1];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        w[t][i] = __builtin_bit_cast(unsigned, __builtin_convertvector((f32x2){a, b}, bf16x2));
+        a -= __uint_as_float(w[t][i] << 16);
+        b -= __uint_as_float(w[t][i] & 0xffff0000u);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) out[t] = __builtin_bit_cast(Frag, (u32x4){w[t][0], w[t][1], w[t][2], w[t][3]});
+  }
+  // Operand of block p from the result tiles m of its axis.
+  template <int NT> static __device__ __forceinline__ void from_tiles(const f32x4* m, int p, Frag (&out)[NT]) {
+    const f32x4 a = m[2 * p], b = m[2 * p + 1];
+    split<NT>({a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}, out);
+  }
+  static __device__ __forceinline__ f32x4 mma(const Frag& a, const Frag& b, f32x4 c) { return mfma16x16x32(a, b, c); }
+  // Score tiles: [NT][CH][CH], the source axis along the row, its 32-blocks in perm32 order. A result
+  // tile of sources 16 j + 4 g + i and target t:
+  template <int NT> static __device__ __forceinline__ void put_scores(u16* p, int t, int j, int g, const f32x4& x) {
+    const int at = swz<64>(t, 32 * (j >> 1) + 8 * g + 4 * (j & 1));
+    float r[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      u32x2 w;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        w[i] = __builtin_bit_cast(unsigned, __builtin_convertvector((f32x2){r[2 * i], r[2 * i + 1]}, bf16x2));
+        r[2 * i] -= __uint_as_float(w[i] << 16);
+        r[2 * i + 1] -= __uint_as_float(w[i] & 0xffff0000u);
+      }
+      *reinterpret_cast<u32x2*>(p + n * CH * CH + at) = w;
+    }
+  }
+  static __device__ __forceinline__ Frag scores(const u16* p, int n, int t, int b, int g) {
+    return lds8(p + n * CH * CH + swz<64>(t, 32 * b + 8 * g));
+  }
+  static constexpr int score_elems(int nt) { return nt * CH * CH; }
+};
+
+template <> struct Tiles<float> {
+  static constexpr int CH = 32;
+  static constexpr int BLK = 16;
+  static constexpr int PIECE = 4;
+  typedef f32x4 Frag;
+  typedef float P;
+  // Rows lie 4 floats further apart than they are long: 16 rows' pieces at one column then cover all banks.
+  static constexpr int size(int R, int L) { return R * (L + 4); }
+  template <int L> static __device__ __forceinline__ int at(int row, int col) { return row * (L + 4) + col; }
+  static __device__ __forceinline__ int index(int j, int g, int i) { return 16 * j + 4 * g + i; }
+  template <int L> static __device__ __forceinline__ Frag along(const float* t, int row, int p, int g) {
+    return *reinterpret_cast<const f32x4*>(t + at<L>(row, 16 * p + 4 * g));
+  }
+  template <int L> static __device__ __forceinline__ Frag down(const float* t, int b, int col0, int g, int l16) {
+    const float* c = t + at<L>(16 * b + 4 * g, col0 + l16);
+    return f32x4{c[0], c[L + 4], c[2 * (L + 4)], c[3 * (L + 4)]};
+  }
+  template <int L> static __device__ __forceinline__ Frag down_index(const float* t, int b, int j, int g, int l16) {
+    return down<L>(t, b, 16 * j, g, l16);
+  }
+  static __device__ __forceinline__ int down_row(int g, int e) { return 4 * g + e; }
+  static __device__ __forceinline__ float value(const Frag& f, int e) { return f[e]; }
+  static constexpr int TERMS(int) { return 1; }
+  template <int NT> static __device__ __forceinline__ void split(const float (&x)[4], Frag (&out)[NT]) {
+    static_assert(NT == 1, "float32 products take values whole");
+    out[0] = f32x4{x[0], x[1], x[2], x[3]};
+  }
+  template <int NT> static __device__ __forceinline__ void from_tiles(const f32x4* m, int p, Frag (&out)[NT]) { out[0] = m[p]; }
+  static __device__ __forceinline__ f32x4 mma(const Frag& a, const Frag& b, f32x4 c) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i], b[i], c, 0, 0, 0);
+    return c;
+  }
+  template <int NT> static __device__ __forceinline__ void put_scores(float* p, int t, int j, int g, const f32x4& x) {
+    *reinterpret_cast<f32x4*>(p + at<CH>(t, 16 * j + 4 * g)) = x;
+  }
+  static __device__ __forceinline__ Frag scores(const float* p, int, int t, int b, int g) {
+    return *reinterpret_cast<const f32x4*>(p + at<CH>(t, 16 * b + 4 * g));
+  }
+  static constexpr int score_elems(int) { return size(CH, CH); }
+};
+
+// 16 bytes of a row of `dim` elements from column `col` on, as registers. Rows may start at any
+// element-aligned address. fetch() reads whole pieces inside the row (a row's last, ragged piece moved back;
+// rows shorter than a piece element by element); place() brings the elements to their places, with zeros
+// behind the row's end.
+template <typename T> struct RowPiece {
+  static constexpr int E = Tiles<T>::PIECE;
+  static __device__ __forceinline__ u32x4 fetch(const T* row, int col, int dim) {
+    if (dim >= E) {
+      const int c = col + E <= dim ? col : dim - E;
+      return reinterpret_cast<const Loose<u32x4>*>(row + c)->v;
+    }
+    float x[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) x[i] = col + i < dim ? Elem<T>::load(row, col + i) : 0.f;
+    return Pack<T, E, true>::words(x);
+  }
+  static __device__ __forceinline__ u32x4 place(u32x4 w, int col, int dim, bool live) {
+    if (dim >= E && dim % E != 0) {
+      const int over = col + E - dim;  // elements behind the row's end
+      if (over > 0) {
+        const int bits = over * 8 * static_cast<int>(sizeof(T));
+        uint64_t lo = static_cast<uint64_t>(w[1]) << 32 | w[0], hi = static_cast<uint64_t>(w[3]) << 32 | w[2];
+        if (bits >= 128) {
+          lo = hi = 0;
+        } else if (bits >= 64) {
+          lo = hi >> (bits - 64);
+          hi = 0;
+        } else {
+          lo = lo >> bits | hi << (64 - bits);
+          hi >>= bits;
+        }
+        w = u32x4{static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32), static_cast<uint32_t>(hi),
+                  static_cast<uint32_t>(hi >> 32)};
+      }
+    }
+    return live && col < dim ? w : u32x4{0, 0, 0, 0};
+  }
+};
+
+}  // namespace comba

@@ -6,6 +6,7 @@
 
 #include "comba.h"
 #include "layer.h"
+#include "linear_attn.h"
 
 #define COMBA_API extern "C" __attribute__((visibility("default")))
 
@@ -415,4 +416,167 @@ COMBA_API int32_t comba_block_norm_bwd(const void* y, const void* gate, const vo
                              dr, dn, dy, dgate, dresidual, dscale, dpost_weight, dpre_weight,
                              static_cast<float*>(workspace)};
   return report_launch(comba::launch_norm_bwd(a, static_cast<hipStream_t>(stream)));
+}
+
+// --- linear attention ----------------------------------------------------------------------------
+
+namespace {
+
+int32_t check_attn(const void* q, const void* k, const void* v, const float* log_decay, int32_t H, int32_t Hk, int32_t K,
+                   int32_t V, int32_t dtype, float scale) {
+  if (!q || !k || !v || !log_decay) return report(COMBA_ERR_INVALID_ARG, "q, k, v and log_decay must be non-NULL");
+  if (!known_dtype(dtype)) return report(COMBA_ERR_INVALID_ARG, "dtype must be COMBA_BF16 or COMBA_FP32");
+  if (H < 1 || Hk < 1 || H % Hk != 0) return report(COMBA_ERR_INVALID_ARG, "num_qk_heads must be >= 1 and divide H");
+  if (K < 1 || V < 1) return report(COMBA_ERR_INVALID_ARG, "K and V must be >= 1");
+  if (!std::isfinite(scale)) return report(COMBA_ERR_INVALID_ARG, "scale must be finite");
+  if (K > comba::kAttnMaxWidth || V > comba::kAttnMaxWidth) return report(COMBA_ERR_UNSUPPORTED, "K or V above 256");
+  if (H > kMaxWidth) return report(COMBA_ERR_UNSUPPORTED, "H above 2^22");
+  return COMBA_OK;
+}
+
+bool attn_sizes_ok(int32_t B, int32_t T, int32_t H, int32_t Hk, int32_t K, int32_t V) {
+  return B >= 1 && T >= 0 && H >= 1 && H <= kMaxWidth && Hk >= 1 && H % Hk == 0 && K >= 1 && K <= comba::kAttnMaxWidth &&
+         V >= 1 && V <= comba::kAttnMaxWidth && static_cast<int64_t>(B) * T <= kMaxTokens;
+}
+
+// Column blocks of the largest launch per (segment, head), and the blocks of the scan over segments.
+int32_t check_attn_grid(int64_t slots, int64_t H, int64_t N, int32_t K, int32_t V, int64_t blocks) {
+  const int64_t units = slots * H + 8;
+  if (units * blocks > kMaxBlocks || N * H * comba::attn_inner_blocks(K, V) > kMaxBlocks)
+    return report(COMBA_ERR_UNSUPPORTED, "too many (segment, head) pairs for one launch");
+  return COMBA_OK;
+}
+
+struct AttnWs {  // offsets of a cut forward's parts
+  size_t decay, total;
+};
+AttnWs attn_ws(const comba::AttnPlan& p, int64_t H, int64_t K, int64_t V) {
+  AttnWs w{0, 0};
+  if (!p.L) return w;
+  w.decay = up256(sizeof(float) * p.slots * H * K * V);
+  w.total = w.decay + up256(sizeof(double) * p.slots * H);
+  return w;
+}
+
+struct AttnBwdWs {
+  size_t grad, decay, inner, rdot, hsum, dqk, total;
+};
+AttnBwdWs attn_bwd_ws(const comba::AttnPlan& p, int64_t tokens, int64_t H, int64_t Hk, int32_t K, int32_t V) {
+  const size_t states = up256(sizeof(float) * p.slots * H * K * V), d = sizeof(double);
+  AttnBwdWs w;
+  w.grad = states;
+  w.decay = 2 * states;
+  w.inner = w.decay + up256(d * p.slots * H);
+  w.rdot = w.inner + up256(d * p.slots * H * comba::attn_inner_blocks(K, V));
+  w.hsum = w.rdot + up256(sizeof(float) * 2 * comba::attn_blocks(K) * tokens * H);
+  w.dqk = w.hsum + up256(d * p.slots * H);
+  w.total = w.dqk + (H == Hk ? 0 : up256(sizeof(float) * 2 * tokens * H * K));
+  return w;
+}
+
+}  // namespace
+
+COMBA_API size_t comba_linear_attn_workspace_size(int32_t B, int32_t T, int32_t H, int32_t num_qk_heads, int32_t K,
+                                                  int32_t V, int32_t num_seqs) {
+  if (!attn_sizes_ok(B, T, H, num_qk_heads, K, V)) return 0;
+  return attn_ws(comba::attn_plan(B, T, H, V, num_seqs > 0 ? num_seqs : B, num_seqs > 0), H, K, V).total;
+}
+
+COMBA_API int32_t comba_linear_attn_fwd(const void* q, const void* k, const void* v, const float* log_decay,
+                                        int32_t decay_per_token, const float* initial_state, const int32_t* cu_seqlens,
+                                        int32_t num_seqs, int32_t B, int32_t T, int32_t H, int32_t num_qk_heads, int32_t K,
+                                        int32_t V, int32_t dtype, float scale, void* o, float* final_state, void* workspace,
+                                        size_t workspace_bytes, void* stream) {
+  int32_t rc = check_attn(q, k, v, log_decay, H, num_qk_heads, K, V, dtype, scale);
+  if (rc != COMBA_OK) return rc;
+  if (!o) return report(COMBA_ERR_INVALID_ARG, "o must be non-NULL");
+  int64_t N = 0;
+  if ((rc = check_batch(cu_seqlens, num_seqs, B, T, N)) != COMBA_OK) return rc;
+  const int64_t state = N * H * K * V * 4;
+  if ((rc = check_states(initial_state, final_state, state)) != COMBA_OK) return rc;
+  const comba::AttnPlan p = comba::attn_plan(B, T, H, V, N, cu_seqlens != nullptr);
+  if ((rc = check_attn_grid(p.slots, H, N, K, V, comba::attn_blocks(V))) != COMBA_OK) return rc;
+  const AttnWs w = attn_ws(p, H, K, V);
+  rc = check_workspace(workspace, workspace_bytes, w.total,
+                       "workspace is NULL or smaller than comba_linear_attn_workspace_size()");
+  if (rc != COMBA_OK) return rc;
+  const int64_t rows = static_cast<int64_t>(B) * T, e = size_of(dtype), decays = decay_per_token ? rows * H : H;
+  const Span sq{q, rows * num_qk_heads * K * e}, sk{k, sq.bytes}, sv{v, rows * H * V * e}, sg{log_decay, 4 * decays},
+      sc{cu_seqlens, 4 * (N + 1)}, ws{workspace, static_cast<int64_t>(w.total)};
+  if ((rc = check_apart({{o, sv.bytes}, ws}, {sq, sk, sv, sg, sc, {initial_state, state}, {final_state, state}})) !=
+          COMBA_OK ||
+      (rc = check_apart({{final_state, state}}, {sq, sk, sv, sg, sc})) != COMBA_OK)
+    return rc;
+  char* at = static_cast<char*>(workspace);
+  const comba::AttnArgs a{q, k, v, log_decay, decay_per_token != 0, scale, initial_state, cu_seqlens,
+                          static_cast<int>(N), B, T, H, num_qk_heads, K, V, dtype, o, final_state};
+  const comba::AttnWorkspace parts{p.L ? reinterpret_cast<float*>(at) : nullptr,
+                                   p.L ? reinterpret_cast<double*>(at + w.decay) : nullptr};
+  return report_launch(comba::launch_attn(a, p, parts, static_cast<hipStream_t>(stream)));
+}
+
+COMBA_API int32_t comba_linear_attn_step(const void* q, const void* k, const void* v, const float* log_decay,
+                                         int32_t decay_per_token, const float* initial_state, int32_t N, int32_t H,
+                                         int32_t num_qk_heads, int32_t K, int32_t V, int32_t dtype, float scale, void* o,
+                                         float* final_state, void* stream) {
+  int32_t rc = check_attn(q, k, v, log_decay, H, num_qk_heads, K, V, dtype, scale);
+  if (rc != COMBA_OK) return rc;
+  if (!o) return report(COMBA_ERR_INVALID_ARG, "o must be non-NULL");
+  if (N < 1) return report(COMBA_ERR_INVALID_ARG, "N must be >= 1");
+  const int64_t state = static_cast<int64_t>(N) * H * K * V * 4;
+  if ((rc = check_states(initial_state, final_state, state)) != COMBA_OK) return rc;
+  if (comba::attn_step_blocks(N, H, V) > kMaxBlocks)
+    return report(COMBA_ERR_UNSUPPORTED, "too many (sequence, head) pairs for one launch");
+  const int64_t e = size_of(dtype), heads = static_cast<int64_t>(N) * H;
+  const Span sq{q, static_cast<int64_t>(N) * num_qk_heads * K * e}, sk{k, sq.bytes}, sv{v, heads * V * e},
+      sg{log_decay, 4 * (decay_per_token ? heads : H)};
+  if ((rc = check_apart({{o, sv.bytes}}, {sq, sk, sv, sg, {initial_state, state}, {final_state, state}})) != COMBA_OK ||
+      (rc = check_apart({{final_state, state}}, {sq, sk, sv, sg})) != COMBA_OK)
+    return rc;
+  const comba::AttnArgs a{q, k, v, log_decay, decay_per_token != 0, scale, initial_state, nullptr, N, N, 1, H,
+                          num_qk_heads, K, V, dtype, o, final_state};
+  return report_launch(comba::launch_attn_step(a, static_cast<hipStream_t>(stream)));
+}
+
+COMBA_API size_t comba_linear_attn_bwd_workspace_size(int32_t B, int32_t T, int32_t H, int32_t num_qk_heads, int32_t K,
+                                                      int32_t V, int32_t num_seqs) {
+  if (!attn_sizes_ok(B, T, H, num_qk_heads, K, V)) return 0;
+  const comba::AttnPlan p = comba::attn_bwd_plan(B, T, H, num_seqs > 0 ? num_seqs : B, num_seqs > 0);
+  return attn_bwd_ws(p, static_cast<int64_t>(B) * T, H, num_qk_heads, K, V).total;
+}
+
+COMBA_API int32_t comba_linear_attn_bwd(const void* q, const void* k, const void* v, const float* log_decay,
+                                        int32_t decay_per_token, const float* initial_state, const int32_t* cu_seqlens,
+                                        int32_t num_seqs, int32_t B, int32_t T, int32_t H, int32_t num_qk_heads, int32_t K,
+                                        int32_t V, int32_t dtype, float scale, const void* d_o, const float* d_final_state,
+                                        void* dq, void* dk, void* dv, float* dlog_decay, float* d_initial_state,
+                                        void* workspace, size_t workspace_bytes, void* stream) {
+  int32_t rc = check_attn(q, k, v, log_decay, H, num_qk_heads, K, V, dtype, scale);
+  if (rc != COMBA_OK) return rc;
+  if (!d_o || !dq || !dk || !dv || !dlog_decay)
+    return report(COMBA_ERR_INVALID_ARG, "d_o, dq, dk, dv and dlog_decay must be non-NULL");
+  int64_t N = 0;
+  if ((rc = check_batch(cu_seqlens, num_seqs, B, T, N)) != COMBA_OK) return rc;
+  const comba::AttnPlan p = comba::attn_bwd_plan(B, T, H, N, cu_seqlens != nullptr);
+  if ((rc = check_attn_grid(p.slots, H, N, K, V, 2 * comba::attn_blocks(K) + comba::attn_blocks(V))) != COMBA_OK) return rc;
+  const int64_t rows = static_cast<int64_t>(B) * T, e = size_of(dtype);
+  const AttnBwdWs w = attn_bwd_ws(p, rows, H, num_qk_heads, K, V);
+  rc = check_workspace(workspace, workspace_bytes, w.total,
+                       "workspace is NULL or smaller than comba_linear_attn_bwd_workspace_size()");
+  if (rc != COMBA_OK) return rc;
+  const int64_t qk = rows * num_qk_heads * K * e, vo = rows * H * V * e, state = N * H * K * V * 4;
+  const int64_t decays = 4 * (decay_per_token ? rows * H : H);
+  rc = check_apart({{dq, qk}, {dk, qk}, {dv, vo}, {dlog_decay, decays}, {d_initial_state, state},
+                    {workspace, static_cast<int64_t>(w.total)}},
+                   {{q, qk}, {k, qk}, {v, vo}, {log_decay, decays}, {initial_state, state}, {cu_seqlens, 4 * (N + 1)},
+                    {d_o, vo}, {d_final_state, state}});
+  if (rc != COMBA_OK) return rc;
+  char* ws = static_cast<char*>(workspace);
+  auto f32 = [&](size_t o) { return reinterpret_cast<float*>(ws + o); };
+  auto f64 = [&](size_t o) { return reinterpret_cast<double*>(ws + o); };
+  const comba::AttnBwdArgs a{{q, k, v, log_decay, decay_per_token != 0, scale, initial_state, cu_seqlens,
+                              static_cast<int>(N), B, T, H, num_qk_heads, K, V, dtype, nullptr, nullptr},
+                             d_o, d_final_state, dq, dk, dv, dlog_decay, d_initial_state, f32(0), f32(w.grad),
+                             f64(w.decay), f64(w.inner), f32(w.rdot), f64(w.hsum), H == num_qk_heads ? nullptr : f32(w.dqk)};
+  return report_launch(comba::launch_attn_bwd(a, p, static_cast<hipStream_t>(stream)));
 }

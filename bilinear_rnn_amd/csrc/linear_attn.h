@@ -1,0 +1,71 @@
+// Launchers of the decayed linear attention. Arguments are already validated.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace comba {
+
+struct AttnArgs {
+  const void* q;              // [B, T, Hk, K] (step: [N, Hk, K])
+  const void* k;
+  const void* v;              // [B, T, H, V]
+  const float* log_decay;     // [B, T, H], or [H] if not per_token
+  bool per_token;
+  float scale;
+  const float* init;          // [N, H, V, K] or null
+  const int32_t* cu_seqlens;  // [N + 1] or null
+  int N, B, T, H, Hk, K, V, dtype;
+  void* o;                    // [B, T, H, V]
+  float* fin;                 // [N, H, V, K] or null
+};
+
+// Segments of a sequence: sequence n's segment c (L tokens each) has slot
+//   n * ceil(T / L) + c               (fixed-length batches)
+//   cu_seqlens[n] / L + n + c         (packed batches; unique because starts increase)
+struct AttnPlan {
+  int L;                      // tokens per segment; 0: sequences are not cut (slot n)
+  int64_t slots;
+};
+AttnPlan attn_plan(int64_t B, int64_t T, int64_t H, int64_t V, int64_t N, bool packed);
+AttnPlan attn_bwd_plan(int64_t B, int64_t T, int64_t H, int64_t N, bool packed);
+
+struct AttnWorkspace {        // of a cut forward; null when not cut
+  float* state;               // [slots, H, V, K]: every segment's end state from 0, then its incoming state
+  double* decay;              // [slots, H]: sum of the segment's log2 decays
+};
+
+struct AttnBwdArgs {
+  AttnArgs f;                 // the forward's inputs; o and fin unused
+  const void* dO;             // [B, T, H, V]
+  const float* dfin;          // [N, H, V, K] or null
+  void* dq;                   // [B, T, Hk, K]
+  void* dk;
+  void* dv;                   // [B, T, H, V]
+  float* dlog_decay;          // [B, T, H] or [H]
+  float* dinit;               // [N, H, V, K] or null
+  // workspace
+  float* state;               // [slots, H, V, K]: as above
+  float* grad;                // [slots, H, V, K]: every segment's own part of the gradient at its start, then the
+                              // gradient at its end
+  double* decay;              // [slots, H]
+  double* inner;              // [slots, H, attn_inner_blocks]: <gradient at the end, state at the end>, in parts
+  float* rdot;                // [2, K blocks, B * T, H]: q . dq and k . dk over 64 columns each
+  double* hsum;               // [slots, H]: sums of dlog_decay (constant decays)
+  float* dqk;                 // [2, B * T, H, K]: dq and dk of every value head (shared q / k heads), else null
+};
+
+// Widest head; the state's tiles of one wavefront stay in its registers.
+constexpr int kAttnMaxWidth = 256;
+constexpr int kAttnBlock = 64;  // output columns per workgroup
+__host__ __device__ inline int attn_blocks(int width) { return (width + kAttnBlock - 1) / kAttnBlock; }
+// Elements of a state that a workgroup of the scan over segments takes.
+constexpr int kAttnScanElems = 1024;
+__host__ __device__ inline int attn_inner_blocks(int K, int V) { return (K * V + kAttnScanElems - 1) / kAttnScanElems; }
+
+hipError_t launch_attn(const AttnArgs& a, const AttnPlan& p, const AttnWorkspace& w, hipStream_t st);
+hipError_t launch_attn_step(const AttnArgs& a, hipStream_t st);
+hipError_t launch_attn_bwd(const AttnBwdArgs& a, const AttnPlan& p, hipStream_t st);
+int64_t attn_step_blocks(int64_t N, int64_t H, int64_t V);
+
+}  // namespace comba

@@ -595,6 +595,69 @@ int32_t comba_block_norm_bwd(const void* y, const void* gate, const void* residu
                              float* dscale, float* dpost_weight, float* dpre_weight, void* workspace,
                              size_t workspace_bytes, void* stream);
 
+/*
+ * Linear attention with a decay for each head, the plain recurrence beside
+ * Comba's (no correction of the value or the output by the key). Per value
+ * head h, with S a V x K state:
+ *     S_t = exp(g_t) S_{t-1} + v_t k_t^T,      o_t = scale S_t q_t
+ *   q, k           [B, T, Hk, K]    dtype; Hk = num_qk_heads divides H, value
+ *                                   head h reads q / k head h / (H / Hk)
+ *   v, o           [B, T, H, V]     dtype
+ *   log_decay      float32: g of every token and head, [B, T, H]
+ *                  (decay_per_token non-zero), or a constant of every head,
+ *                  [H]. g <= 0; values below -200, -infinity among them, keep
+ *                  nothing of the state. Positive values make it grow: its
+ *                  elements, and the decays multiplied over any 64 tokens, must
+ *                  then stay in float32's range. (Not checked.)
+ *   initial_state  [N, H, V, K]     float32, or NULL for zeros
+ *   final_state    [N, H, V, K]     float32, or NULL (not written); may be
+ *                                   initial_state itself, but no other overlap
+ * comba_linear_attn_fwd works in chunks of 64 tokens (bf16; 32 in float32) on the
+ * matrix cores. float32 operands of a product with bf16 inputs are split into
+ * bf16 terms, two for o and three for the states, so that o is right to its own
+ * rounding and states and gradients of the decay to float32's. An input that is
+ * infinite or NaN makes outputs of the same sequence, head and chunk infinite or
+ * NaN, earlier tokens' among them, and everything after it.
+ * Batches with too few sequences and heads for the chip are cut along time; the
+ * call then needs workspace of comba_linear_attn_workspace_size(...) bytes,
+ * 256-byte aligned (0: none, NULL is accepted). num_seqs is N with cu_seqlens
+ * and 0 without.
+ * comba_linear_attn_step is the single-token form: q, k [N, Hk, K], v, o
+ * [N, H, V], log_decay [N, H] or [H], one token for each of N sequences.
+ * comba_linear_attn_bwd: gradients for d_o = dL/do [B, T, H, V] (dtype) and
+ * d_final_state (float32 [N, H, V, K]; NULL: 0), from the forward's inputs:
+ *   dq, dk [B, T, Hk, K], dv [B, T, H, V] dtype (dq and dk summed over the value
+ *   heads that share them); dlog_decay float32, [B, T, H] or [H] as log_decay;
+ *   d_initial_state [N, H, V, K] float32 (may be NULL: not written).
+ * It needs comba_linear_attn_bwd_workspace_size(...) bytes, 256-byte aligned.
+ * All three give the same bits on every run.
+ * Errors: COMBA_ERR_UNSUPPORTED for K or V above 256, H above 2^22, more than
+ * 2^31 - 2^16 tokens, and for launches of more than 2^32 - 1 threads.
+ */
+size_t comba_linear_attn_workspace_size(int32_t B, int32_t T, int32_t H, int32_t num_qk_heads, int32_t K, int32_t V,
+                                        int32_t num_seqs);
+
+int32_t comba_linear_attn_fwd(const void* q, const void* k, const void* v, const float* log_decay,
+                              int32_t decay_per_token, const float* initial_state, const int32_t* cu_seqlens,
+                              int32_t num_seqs, int32_t B, int32_t T, int32_t H, int32_t num_qk_heads, int32_t K, int32_t V,
+                              int32_t dtype, float scale, void* o, float* final_state, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+int32_t comba_linear_attn_step(const void* q, const void* k, const void* v, const float* log_decay,
+                               int32_t decay_per_token, const float* initial_state, int32_t N, int32_t H,
+                               int32_t num_qk_heads, int32_t K, int32_t V, int32_t dtype, float scale, void* o,
+                               float* final_state, void* stream);
+
+size_t comba_linear_attn_bwd_workspace_size(int32_t B, int32_t T, int32_t H, int32_t num_qk_heads, int32_t K, int32_t V,
+                                            int32_t num_seqs);
+
+int32_t comba_linear_attn_bwd(const void* q, const void* k, const void* v, const float* log_decay,
+                              int32_t decay_per_token, const float* initial_state, const int32_t* cu_seqlens,
+                              int32_t num_seqs, int32_t B, int32_t T, int32_t H, int32_t num_qk_heads, int32_t K, int32_t V,
+                              int32_t dtype, float scale, const void* d_o, const float* d_final_state, void* dq, void* dk,
+                              void* dv, float* dlog_decay, float* d_initial_state, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -175,3 +175,53 @@ def block_norm(y, gate=None, residual=None, scale=None, post_weight=None, pre_we
         d = k1 * (d + sign * mag(y) * k1 * k1 * (d * mag(y)).mean(-1, keepdims=True))
     g["dy"] = d
     return g
+
+
+def linear_attention(q, k, v, log_decay, scale=1.0, init=None, cu=None, do=None, dfin=None, magnitude=False):
+    """Returns (o, final_state), or with do a dict of the gradients. log_decay is [B, T, H] or [H].
+
+    With ``magnitude``, decays are taken at half their logarithm (X e^-X <= (2 / e) e^(-X / 2) counts a
+    relative error of X per decay), and dlog_decay sums |q . dq| + |k . dk| over the rest of the sequence,
+    the terms of the sum that an evaluation may take it from."""
+    q, k, v, log_decay, init, do, dfin = (_f(x) for x in (q, k, v, log_decay, init, do, dfin))
+    mag = np.abs if magnitude else (lambda x: x)
+    B, T, Hk, K = q.shape
+    H, V = v.shape[2:]
+    N = _num_seqs(B, cu)
+    rep = H // Hk
+    head = log_decay.ndim == 1
+    g = np.broadcast_to(log_decay, (B, T, H))
+    a = np.exp(g / 2 if magnitude else g)
+    qh, kh = (mag(np.repeat(x, rep, 2)) for x in (q, k))
+    v, scale = mag(v), mag(scale)
+    o = np.full_like(v, np.nan)
+    fin = np.zeros((N, H, V, K))
+    dq, dk = np.full_like(q, np.nan), np.full_like(q, np.nan)
+    dv, dg, dinit = np.full_like(v, np.nan), np.full((B, T, H), np.nan), np.zeros_like(fin)
+    for n, row, t0, t1 in _segments(B, T, cu):
+        S = np.zeros((H, V, K)) if init is None else mag(init[n])
+        states = [S]
+        for t in range(t0, t1):
+            S = a[row, t][:, None, None] * S + v[row, t][:, :, None] * kh[row, t][:, None]
+            o[row, t] = scale * np.einsum("hvk,hk->hv", S, qh[row, t])
+            states.append(S)
+        fin[n] = S
+        if do is None:
+            continue
+        E = np.zeros((H, V, K)) if dfin is None else mag(dfin[n])
+        terms = (E * S).sum((1, 2))
+        for t in reversed(range(t0, t1)):
+            d = scale * mag(do[row, t])
+            hq = np.einsum("hvk,hv->hk", states[t - t0 + 1], d)
+            E = E + d[:, :, None] * qh[row, t][:, None]
+            hk = np.einsum("hvk,hv->hk", E, v[row, t])
+            dv[row, t] = np.einsum("hvk,hk->hv", E, kh[row, t])
+            dq[row, t], dk[row, t] = (x.reshape(Hk, rep, K).sum(1) for x in (hq, hk))
+            E = a[row, t][:, None, None] * E
+            terms = terms + (hq * qh[row, t]).sum(1) + (hk * kh[row, t]).sum(1)
+            dg[row, t] = terms if magnitude else (E * states[t - t0]).sum((1, 2))
+        dinit[n] = E
+    if do is None:
+        return o, fin
+    return dict(dq=dq, dk=dk, dv=dv, dlog_decay=np.nansum(dg, (0, 1)) if head else dg,
+                dinitial_state=None if init is None else dinit)
