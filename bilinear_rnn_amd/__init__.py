@@ -9,7 +9,7 @@ This package is the thin Python binding over that library.
 """
 from .api import (CombaError, block_norm, block_norm_bwd, bwd_cached_workspace_size, bwd_workspace_size, check_inputs,  # noqa: F401
                   chunk_bwd, chunk_fwd, chunk_fwd_noalloc,
-                  chunk_states_size, lds_probe, lib, library_path, linear_attention, linear_attention_bwd,
+                  chunk_states_size, group_norm, group_norm_bwd, lds_probe, lib, library_path, linear_attention, linear_attention_bwd,
                   linear_attention_step, linear_attention_workspace_size,
                   mfma_peak_probe, recurrent_step, segmented_workspace_size, selective_scan, selective_scan_bwd,
                   selective_scan_workspace_size, selective_step, short_conv, short_conv_bwd, short_conv_step,
@@ -20,4 +20,5 @@ __all__ = ["chunk_fwd", "chunk_bwd", "bwd_workspace_size", "bwd_cached_workspace
            "lds_probe", "check_inputs", "short_conv", "short_conv_step", "short_conv_bwd", "selective_scan",
            "selective_step", "selective_scan_bwd", "selective_scan_workspace_size", "block_norm", "block_norm_bwd",
            "linear_attention", "linear_attention_step", "linear_attention_bwd", "linear_attention_workspace_size",
+           "group_norm", "group_norm_bwd",
            "CombaError"]

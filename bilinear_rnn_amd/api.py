@@ -50,7 +50,9 @@ EXPORTED = ("comba_abi_version", "comba_status_string", "comba_last_error",
             "comba_selective_step", "comba_selective_scan_bwd_workspace_size", "comba_selective_scan_bwd",
             "comba_block_norm_fwd", "comba_block_norm_bwd_workspace_size", "comba_block_norm_bwd",
             "comba_linear_attn_workspace_size", "comba_linear_attn_fwd", "comba_linear_attn_step",
-            "comba_linear_attn_bwd_workspace_size", "comba_linear_attn_bwd")
+            "comba_linear_attn_bwd_workspace_size", "comba_linear_attn_bwd",
+            "comba_group_norm_workspace_size", "comba_group_norm_fwd", "comba_group_norm_bwd_workspace_size",
+            "comba_group_norm_bwd")
 
 
 class CombaError(RuntimeError):
@@ -171,6 +173,15 @@ def lib() -> ctypes.CDLL:
         L.comba_linear_attn_bwd.argtypes = [vp, vp, vp, fp, i32, fp, ip, i32, i32, i32, i32, i32, i32, i32, i32, f32,
                                             vp, fp, vp, vp, vp, fp, fp, vp, sz, vp]
         L.comba_linear_attn_bwd.restype = i32
+        L.comba_group_norm_workspace_size.argtypes = [i32] * 5
+        L.comba_group_norm_workspace_size.restype = sz
+        L.comba_group_norm_fwd.argtypes = [vp, fp, fp, ip, i32, i32, i32, i32, i32, f32, i32, i32, vp, fp, vp, sz, vp]
+        L.comba_group_norm_fwd.restype = i32
+        L.comba_group_norm_bwd_workspace_size.argtypes = [i32] * 5
+        L.comba_group_norm_bwd_workspace_size.restype = sz
+        L.comba_group_norm_bwd.argtypes = [vp, vp, fp, fp, fp, ip, i32, i32, i32, i32, i32, i32, i32, vp, fp, fp, vp, sz,
+                                           vp]
+        L.comba_group_norm_bwd.restype = i32
         _lib = L
     return _lib
 
@@ -968,6 +979,63 @@ def linear_attention_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_
          _at(q), _at(k), _at(v), _at(log_decay), per_token, _at(initial_state), _at(cu_seqlens), nseq, B, T, H, Hk, K, V,
          _DT[q.dtype], scale, _at(do), _at(d_final_state), _at(g["dq"]), _at(g["dk"]), _at(g["dv"]), _at(g["dlog_decay"]),
          _at(g["dinitial_state"]), *_ws(workspace))
+    return g
+
+
+def _group_args(x, groups, weight, bias, cu_seqlens):
+    dims = 2 if isinstance(x, torch.Tensor) and x.dim() == 2 and cu_seqlens is None else 3
+    index = _activation(x, "x", dims)
+    B, D = x.shape[0], x.shape[-1]
+    T = x.shape[1] if dims == 3 else 1
+    if groups < 1 or D % groups != 0:
+        raise ValueError(f"the group count {groups} must divide the channel count {D}")
+    N = _sequences(B, T, cu_seqlens, index)
+    _may(weight, "weight", torch.float32, (D,), index)
+    _may(bias, "bias", torch.float32, (D,), index)
+    return B, T, D, N, N if cu_seqlens is not None else 0, index
+
+
+def group_norm(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+               cu_seqlens: Optional[torch.Tensor] = None, silu: bool = False, eps: float = 1e-5,
+               output_stats: bool = True, out: Optional[torch.Tensor] = None, stats: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Group norm over channels-last activations with optional SiLU through ``comba_group_norm_fwd``: over
+    every token alone for x [N, D], over every sequence for x [B, T, D] (packed ones with cu_seqlens).
+    weight and bias [D] in float32. Returns (y, stats), stats [N, G, 2] the mean and 1 / deviation of every
+    sequence and group, in float32."""
+    B, T, D, N, nseq, index = _group_args(x, groups, weight, bias, cu_seqlens)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _need(out, "out", x.dtype, x.shape, index)
+    if stats is not None or not output_stats:
+        _may(stats, "stats", torch.float32, (N, groups, 2), index)
+    else:
+        stats = x.new_empty((N, groups, 2), dtype=torch.float32)
+    L = lib()
+    workspace = _workspace(workspace, int(L.comba_group_norm_workspace_size(B, T, D, groups, nseq)), x)
+    _run(L.comba_group_norm_fwd, index,
+         _at(x), _at(weight), _at(bias), _at(cu_seqlens), nseq, B, T, D, groups, float(eps), _DT[x.dtype], int(bool(silu)),
+         _at(out), _at(stats), *_ws(workspace))
+    return out, stats
+
+
+def group_norm_bwd(x: torch.Tensor, dy: torch.Tensor, stats: torch.Tensor, groups: int,
+                   weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                   cu_seqlens: Optional[torch.Tensor] = None, silu: bool = False,
+                   workspace: Optional[torch.Tensor] = None) -> dict:
+    """Gradients of ``group_norm`` through ``comba_group_norm_bwd``, from its input and the stats it
+    returned. Returns dx in x's type, dweight and dbias in float32 (None where theirs was not given)."""
+    B, T, D, N, nseq, index = _group_args(x, groups, weight, bias, cu_seqlens)
+    _need(dy, "dy", x.dtype, x.shape, index)
+    _need(stats, "stats", torch.float32, (N, groups, 2), index)
+    L = lib()
+    g = dict(dx=torch.empty_like(x), dweight=None if weight is None else torch.empty_like(weight),
+             dbias=None if bias is None else torch.empty_like(bias))
+    workspace = _workspace(workspace, int(L.comba_group_norm_bwd_workspace_size(B, T, D, groups, nseq)), x)
+    _run(L.comba_group_norm_bwd, index,
+         _at(x), _at(dy), _at(stats), _at(weight), _at(bias), _at(cu_seqlens), nseq, B, T, D, groups, _DT[x.dtype],
+         int(bool(silu)), _at(g["dx"]), _at(g["dweight"]), _at(g["dbias"]), *_ws(workspace))
     return g
 
 

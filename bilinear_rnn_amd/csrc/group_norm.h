@@ -1,0 +1,46 @@
+// Launchers of the group norm. Arguments are already validated.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace comba {
+
+struct GroupNormArgs {
+  const void* x;              // [B, T, D]
+  const float* weight;        // [D] or null
+  const float* bias;          // [D] or null
+  const int32_t* cu_seqlens;  // [N + 1] or null
+  int N, B, T, D, G, dtype;
+  float eps;
+  bool silu;
+  void* y;                    // [B, T, D]
+  float* stats;               // [N, G, 2]: mean and 1 / deviation; or null
+};
+
+struct GroupNormBwdArgs {
+  GroupNormArgs f;            // the forward's inputs; stats is an input, y unused
+  const void* dy;             // [B, T, D]
+  void* dx;                   // [B, T, D]
+  float* dweight;             // [D] or null
+  float* dbias;               // [D] or null
+};
+
+// How a call is cut. Every token alone (rows): `slots` rows of parameter sums. Sequences: tiles of L tokens with
+// the slots of a scan's segments (layer.h), and blocks of `lanes` pieces of E channels; a tile's sums of group g
+// in channel block c lie at part g + c.
+struct GroupNormPlan {
+  bool rows;
+  bool vec;                   // 16-byte pieces
+  int L, E, lanes, cblocks;
+  int64_t slots;
+};
+GroupNormPlan group_norm_plan(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N, bool packed, bool vec, bool bwd);
+// Floats of workspace; the larger of the pieces' and the single channels' form.
+int64_t group_norm_floats(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N, bool packed, bool bwd);
+int64_t group_norm_blocks(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N, bool packed, bool bwd);  // of a launch
+
+hipError_t launch_group_norm(const GroupNormArgs& a, float* ws, hipStream_t st);
+hipError_t launch_group_norm_bwd(const GroupNormBwdArgs& a, float* ws, hipStream_t st);
+
+}  // namespace comba

@@ -1,0 +1,694 @@
+// Group norm over channels-last activations, with SiLU. Per sequence (of tokens) and group of C = D / G
+// neighbouring channels:
+//   n = (x - mean) rstd,  rstd = 1 / sqrt(var + eps);   p = n weight + bias;   y = p or p sigmoid(p)
+// Backward, with d = dL/dp and g = d weight:
+//   dx = rstd (g - mean(g) - n mean(g n)),   dweight = sum d n,   dbias = sum d
+//
+// Two forms. Sequences of one token (the heads of a recurrence's output, say) are rows of C elements in registers:
+// every input is read once. Longer sequences take two passes: sums per tile of tokens, and a second
+// pass in which every workgroup first joins its sequence's tiles.
+#include "column_sums.h"
+#include "comba.h"
+#include "group_norm.h"
+#include "launch.h"
+#include "norm_rows.h"
+#include "scan_common.h"
+
+namespace comba {
+
+// --- every token alone ---------------------------------------------------------------------------
+
+// `stride` rows (instances of C elements) apart, a multiple of G: a lane keeps its group and parameters.
+template <typename T, bool V, int LPR, int NV>
+__global__ __launch_bounds__(LPR > kNormThreads ? LPR : kNormThreads) void group_rows_fwd_kernel(
+    const T* __restrict__ x, const float* __restrict__ weight, const float* __restrict__ bias, NormShape s, int G,
+    int64_t stride, bool silu, T* __restrict__ y, float* __restrict__ stats) {
+  constexpr int TH = LPR > kNormThreads ? LPR : kNormThreads, RPB = TH / LPR;
+  constexpr bool PF = TH <= 512 && NV == 1;
+  using E = Eight<T, V, LPR>;
+  __shared__ float red[2][TH / 64];
+  const int l = threadIdx.x % LPR, r = threadIdx.x / LPR, C = s.D;
+  const uint32_t at = static_cast<uint32_t>(r) * C * sizeof(T);
+  int64_t first = static_cast<int64_t>(blockIdx.x) * RPB;
+  const int64_t c0 = (first + r) % G * C;
+  float w[NV][8], b[NV][8];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    E::params(weight ? weight + c0 : nullptr, l, j, C, 1.f, w[j]);
+    E::params(bias ? bias + c0 : nullptr, l, j, C, 0.f, b[j]);
+  }
+  E xn[NV];
+  auto fetch = [&](int64_t f) {
+    const Range<T> m = step_range<T, RPB>(x, f, s);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) xn[j].load(m, at, l, j, C);
+  };
+  if (PF) fetch(first);
+  for (; first < s.rows; first += stride) {
+    if (!PF) fetch(first);
+    E xc[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) xc[j] = xn[j];
+    if (PF) fetch(first + stride);
+    float sum[1] = {0.f}, sq[1] = {0.f};
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[0] += xc[j][i];
+    row_sums<LPR, 1>(sum, red[0]);
+    const float mean = sum[0] * s.inv;
+    float d[NV][8];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        d[j][i] = E::col(l, j, i) < C ? xc[j][i] - mean : 0.f;
+        sq[0] = fmaf(d[j][i], d[j][i], sq[0]);
+      }
+    row_sums<LPR, 1>(sq, red[1]);
+    const float rstd = 1.f / sqrtf(fmaf(sq[0], s.inv, s.eps));
+    const Range<T> o = step_range<T, RPB>(y, first, s);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float p = fmaf(d[j][i] * rstd, w[j][i], b[j][i]);
+        d[j][i] = silu ? p * sigmoid_fast(p) : p;
+      }
+      E::store(o, at, l, j, C, d[j]);
+    }
+    if (stats && l == 0 && first + r < s.rows) {
+      stats[2 * (first + r)] = mean;
+      stats[2 * (first + r) + 1] = rstd;
+    }
+  }
+}
+
+// part: [stride / G][2][D]: sums of d n and of d over the rows of a lane.
+template <typename T, bool V, int LPR, int NV>
+__global__ __launch_bounds__(LPR > kNormThreads ? LPR : kNormThreads) void group_rows_bwd_kernel(
+    const T* __restrict__ x, const T* __restrict__ dy, const float* __restrict__ stats, const float* __restrict__ weight,
+    const float* __restrict__ bias, NormShape s, int G, int64_t stride, bool silu, T* __restrict__ dx,
+    float* __restrict__ part) {
+  constexpr int TH = LPR > kNormThreads ? LPR : kNormThreads, RPB = TH / LPR;
+  constexpr bool PF = TH <= 512 && NV == 1;
+  using E = Eight<T, V, LPR>;
+  __shared__ float red[2][2 * (TH / 64)];
+  const int l = threadIdx.x % LPR, r = threadIdx.x / LPR, C = s.D;
+  const uint32_t at = static_cast<uint32_t>(r) * C * sizeof(T);
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * RPB + r;
+  const int64_t c0 = unit % G * C;
+  float w[NV][8], b[NV][8], aw[NV][8], ab[NV][8];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    E::params(weight ? weight + c0 : nullptr, l, j, C, 1.f, w[j]);
+    E::params(bias ? bias + c0 : nullptr, l, j, C, 0.f, b[j]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) aw[j][i] = ab[j][i] = 0.f;
+  }
+  E xn[NV], gn[NV];
+  float mn = 0.f, rn = 0.f;
+  auto fetch = [&](int64_t f) {
+    const Range<T> m = step_range<T, RPB>(x, f, s), e = step_range<T, RPB>(dy, f, s);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      xn[j].load(m, at, l, j, C);
+      gn[j].load(e, at, l, j, C);
+    }
+    const bool here = f + r < s.rows;
+    mn = here ? stats[2 * (f + r)] : 0.f;
+    rn = here ? stats[2 * (f + r) + 1] : 0.f;
+  };
+  int64_t first = static_cast<int64_t>(blockIdx.x) * RPB;
+  if (PF) fetch(first);
+  int side = 0;
+  for (; first < s.rows; first += stride, side ^= 1) {
+    if (!PF) fetch(first);
+    E xc[NV], gc[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      xc[j] = xn[j];
+      gc[j] = gn[j];
+    }
+    const float mean = mn, rstd = rn;
+    if (PF) fetch(first + stride);
+    float n[NV][8], g[NV][8], sums[2] = {0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        n[j][i] = E::col(l, j, i) < C ? (xc[j][i] - mean) * rstd : 0.f;
+        float d = gc[j][i];
+        if (silu) {
+          const float p = fmaf(n[j][i], w[j][i], b[j][i]), sg = sigmoid_fast(p);
+          d *= sg * fmaf(p, 1.f - sg, 1.f);
+        }
+        aw[j][i] = fmaf(d, n[j][i], aw[j][i]);
+        ab[j][i] += d;
+        g[j][i] = d * w[j][i];
+        sums[0] += g[j][i];
+        sums[1] = fmaf(g[j][i], n[j][i], sums[1]);
+      }
+    row_sums<LPR, 2>(sums, red[side]);
+    const float mg = sums[0] * s.inv, mgn = sums[1] * s.inv;
+    const Range<T> o = step_range<T, RPB>(dx, first, s);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) g[j][i] = rstd * (g[j][i] - mg - n[j][i] * mgn);
+      E::store(o, at, l, j, C, g[j]);
+    }
+  }
+  if (part) {
+    float* const to = part + unit / G * 2 * G * C + c0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (E::col(l, j, i) < C) {
+          to[E::col(l, j, i)] = aw[j][i];
+          to[static_cast<int64_t>(G) * C + E::col(l, j, i)] = ab[j][i];
+        }
+  }
+}
+
+// --- sequences -----------------------------------------------------------------------------------
+
+struct Moments {  // count, mean, sum of squared distances from it
+  float n, mean, m2;
+  __device__ __forceinline__ void join(const Moments& o) {
+    const float all = n + o.n, d = o.mean - mean;
+    if (o.n == 0.f) return;
+    const float f = o.n / all;
+    mean = fmaf(d, f, mean);
+    m2 += fmaf(d * d, n * f, o.m2);
+    n = all;
+  }
+};
+__device__ __forceinline__ Moments shuffled(const Moments& m, int off) {
+  return {__shfl_xor(m.n, off, kWave), __shfl_xor(m.mean, off, kWave), __shfl_xor(m.m2, off, kWave)};
+}
+
+template <typename T> struct GroupK {
+  const T* x;
+  const T* dy;
+  const float* weight;
+  const float* bias;
+  const int32_t* cu;
+  int N, Tn, D, G, C, L, lanes, cblocks;
+  float eps;
+  bool silu;
+  float* stats;
+  T* out;                     // y or dx
+  float* part;                // [slots, G + cblocks, 2]
+  float* cols;                // [slots, 2, D] or null
+};
+
+// A workgroup's tile: tokens of one sequence and `lanes` pieces of E channels; 256 / lanes tokens at a time.
+template <typename T, int E> struct GroupTile {
+  ScanPlace pl;
+  int cb, CB, RG, l, rg, c0;
+  int gA, groups;             // groups that the block's channels belong to
+  int64_t slot;
+  bool have;
+  __device__ __forceinline__ GroupTile(const GroupK<T>& a) {
+    slot = blockIdx.x / a.cblocks;
+    cb = blockIdx.x % a.cblocks;
+    pl = scan_place<1>(slot, 0, a.cu, a.N, a.Tn, 1, 1, a.L);
+    CB = a.lanes * E;
+    RG = 256 / a.lanes;
+    l = threadIdx.x & (a.lanes - 1);
+    rg = threadIdx.x / a.lanes;
+    c0 = cb * CB + l * E;
+    have = c0 < a.D;
+    gA = cb * CB / a.C;
+    groups = (min(a.D, cb * CB + CB) - 1) / a.C - gA + 1;
+  }
+  template <typename Q> __device__ __forceinline__ Q* row(Q* base, const GroupK<T>& a, int t) const {
+    return base + (static_cast<int64_t>(pl.b) * a.Tn + t) * a.D + c0;
+  }
+  // Lanes that share a group of the block in the joins: a power of two.
+  __device__ __forceinline__ int join_lanes() const {
+    int p = 64;
+    while (p > 4 && groups * p > 256) p >>= 1;
+    return p;
+  }
+  // f(first piece, one past the last piece) of group gA + i in this block, in units of E channels.
+  __device__ __forceinline__ int piece_lo(const GroupK<T>& a, int i) const { return max(0, (gA + i) * a.C - cb * CB) / E; }
+  __device__ __forceinline__ int piece_hi(const GroupK<T>& a, int i) const {
+    return min(CB, (gA + i + 1) * a.C - cb * CB) / E;
+  }
+};
+
+template <typename T, int E> __device__ __forceinline__ void get(const T* p, float (&x)[E]) {
+  if constexpr (E == 1) x[0] = Elem<T>::load(p, 0);
+  else Pack<T, E, true>::load(p, x, E);
+}
+template <typename T, int E> __device__ __forceinline__ void put(T* p, const float (&x)[E]) {
+  if constexpr (E == 1) Elem<T>::store(p, 0, x[0]);
+  else Pack<T, E, true>::store(p, x, E);
+}
+
+template <typename T, int E>
+__global__ __launch_bounds__(256) void group_moments_kernel(GroupK<T> a) {
+  const GroupTile<T, E> t(a);
+  if (!t.pl.ok || t.pl.t1 <= t.pl.t0) return;
+  __shared__ float cnt[256], mean[256], m2[256];
+  float k[E], s[E], ss[E];
+  int n = 0;
+  if (t.have) {
+    for (int r = t.pl.t0 + t.rg; r < t.pl.t1; r += t.RG, ++n) {
+      float x[E];
+      get<T, E>(t.row(a.x, a, r), x);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        if (n == 0) {  // sums about the first value, so that a far mean costs nothing
+          k[e] = x[e];
+          s[e] = ss[e] = 0.f;
+        }
+        const float d = x[e] - k[e];
+        s[e] += d;
+        ss[e] = fmaf(d, d, ss[e]);
+      }
+    }
+  }
+  Moments m{0.f, 0.f, 0.f};
+  if (n > 0) {
+    const float fn = static_cast<float>(n), inv = 1.f / fn;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const float d = s[e] * inv;
+      m.join({fn, k[e] + d, fmaxf(fmaf(-d, s[e], ss[e]), 0.f)});
+    }
+  }
+  cnt[threadIdx.x] = m.n;
+  mean[threadIdx.x] = m.mean;
+  m2[threadIdx.x] = m.m2;
+  __syncthreads();
+  const int P = t.join_lanes(), j = threadIdx.x & (P - 1);
+  for (int i = threadIdx.x / P; i < t.groups; i += 256 / P) {
+    const int lo = t.piece_lo(a, i), w = t.piece_hi(a, i) - lo;
+    Moments g{0.f, 0.f, 0.f};
+    for (int q = j; q < w * t.RG; q += P) {
+      const int at = q / w * a.lanes + lo + q % w;
+      g.join({cnt[at], mean[at], m2[at]});
+    }
+    for (int off = P / 2; off > 0; off >>= 1) {
+      // both sides join in the same order, so that they agree
+      const Moments o = shuffled(g, off);
+      Moments first = j & off ? o : g;
+      first.join(j & off ? g : o);
+      g = first;
+    }
+    if (j == 0) {
+      float* const to = a.part + 2 * (t.slot * (a.G + a.cblocks) + t.gA + i + t.cb);
+      to[0] = g.mean;
+      to[1] = g.m2;
+    }
+  }
+}
+
+// Calls f(part, tokens of the tile, channels of the part) for every q-th part of group g of the tile's sequence.
+template <typename T, int E, typename F>
+__device__ __forceinline__ void for_parts(const GroupTile<T, E>& t, const GroupK<T>& a, int g, int j, int P, F f) {
+  const int len = t.pl.s1 - t.pl.s0, nseg = segments_of(len, a.L);
+  const int cA = g * a.C / t.CB, ncb = ((g + 1) * a.C - 1) / t.CB - cA + 1;
+  const int64_t slot0 = t.slot - t.pl.seg;
+  for (int q = j; q < nseg * ncb; q += P) {
+    const int tile = q / ncb, cb = cA + q % ncb;
+    const int rows = min(a.L, len - tile * a.L);
+    const int chans = min((g + 1) * a.C, (cb + 1) * t.CB) - max(g * a.C, cb * t.CB);
+    f(a.part + 2 * ((slot0 + tile) * (a.G + a.cblocks) + g + cb), rows, chans);
+  }
+}
+
+template <typename T, int E>
+__global__ __launch_bounds__(256) void group_apply_kernel(GroupK<T> a) {
+  const GroupTile<T, E> t(a);
+  if (!t.pl.ok) return;
+  __shared__ float mean[72], rstd[72];
+  const int P = t.join_lanes(), j = threadIdx.x & (P - 1);
+  const bool some = t.pl.t1 > t.pl.t0;
+  for (int i = threadIdx.x / P; i < t.groups; i += 256 / P) {
+    const int g = t.gA + i;
+    Moments m{0.f, 0.f, 0.f};
+    if (some)
+      for_parts(t, a, g, j, P, [&](const float* p, int rows, int chans) {
+        m.join({static_cast<float>(rows) * static_cast<float>(chans), p[0], p[1]});
+      });
+    for (int off = P / 2; off > 0; off >>= 1) {
+      const Moments o = shuffled(m, off);
+      Moments first = j & off ? o : m;
+      first.join(j & off ? m : o);
+      m = first;
+    }
+    if (j == 0) {
+      const float rs = some ? 1.f / sqrtf(m.m2 / m.n + a.eps) : 0.f;
+      mean[i] = m.mean;
+      rstd[i] = rs;
+      // one workgroup of the sequence hands them on: that of its first tile and the group's first channel
+      if (a.stats && t.pl.seg == 0 && g * a.C >= t.cb * t.CB) {
+        a.stats[2 * (static_cast<int64_t>(t.pl.n) * a.G + g)] = m.mean;
+        a.stats[2 * (static_cast<int64_t>(t.pl.n) * a.G + g) + 1] = rs;
+      }
+    }
+  }
+  __syncthreads();
+  if (!t.have || !some) return;
+  const int i = t.c0 / a.C - t.gA;  // a piece lies in one group
+  const float mu = mean[i], rs = rstd[i];
+  float w[E], b[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    w[e] = a.weight ? a.weight[t.c0 + e] : 1.f;
+    b[e] = a.bias ? a.bias[t.c0 + e] : 0.f;
+  }
+#pragma unroll 2
+  for (int r = t.pl.t0 + t.rg; r < t.pl.t1; r += t.RG) {
+    float x[E];
+    get<T, E>(t.row(a.x, a, r), x);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const float p = fmaf((x[e] - mu) * rs, w[e], b[e]);
+      x[e] = a.silu ? p * sigmoid_fast(p) : p;
+    }
+    put<T, E>(t.row(a.out, a, r), x);
+  }
+}
+
+// The sums of d n and d per channel (cols) and, times the weights, per group (part), of a tile.
+template <typename T, int E>
+__global__ __launch_bounds__(256) void group_sums_kernel(GroupK<T> a) {
+  const GroupTile<T, E> t(a);
+  __shared__ float sn[256 * E], sd[256 * E];
+  const bool some = t.pl.ok && t.pl.t1 > t.pl.t0;
+  if (!some) {
+    if (a.cols)
+      for (int c = threadIdx.x; c < t.CB; c += 256)
+        if (t.cb * t.CB + c < a.D) {
+          a.cols[t.slot * 2 * a.D + t.cb * t.CB + c] = 0.f;
+          a.cols[t.slot * 2 * a.D + a.D + t.cb * t.CB + c] = 0.f;
+        }
+    return;
+  }
+  float an[E], ad[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) an[e] = ad[e] = 0.f;
+  if (t.have) {
+    const float* const st = a.stats + 2 * (static_cast<int64_t>(t.pl.n) * a.G + t.c0 / a.C);
+    const float mu = st[0], rs = st[1];
+    float w[E], b[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      w[e] = a.weight ? a.weight[t.c0 + e] : 1.f;
+      b[e] = a.bias ? a.bias[t.c0 + e] : 0.f;
+    }
+#pragma unroll 2
+    for (int r = t.pl.t0 + t.rg; r < t.pl.t1; r += t.RG) {
+      float x[E], d[E];
+      get<T, E>(t.row(a.x, a, r), x);
+      get<T, E>(t.row(a.dy, a, r), d);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float n = (x[e] - mu) * rs;
+        if (a.silu) {
+          const float p = fmaf(n, w[e], b[e]), sg = sigmoid_fast(p);
+          d[e] *= sg * fmaf(p, 1.f - sg, 1.f);
+        }
+        an[e] = fmaf(d[e], n, an[e]);
+        ad[e] += d[e];
+      }
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    sn[t.rg * t.CB + t.l * E + e] = an[e];
+    sd[t.rg * t.CB + t.l * E + e] = ad[e];
+  }
+  __syncthreads();
+  for (int c = threadIdx.x; c < t.CB; c += 256) {
+    float n = sn[c], d = sd[c];
+    for (int q = 1; q < t.RG; ++q) {
+      n += sn[q * t.CB + c];
+      d += sd[q * t.CB + c];
+    }
+    const int ch = t.cb * t.CB + c;
+    const bool in = ch < a.D;
+    if (in && a.cols) {
+      a.cols[t.slot * 2 * a.D + ch] = n;
+      a.cols[t.slot * 2 * a.D + a.D + ch] = d;
+    }
+    const float w = in ? (a.weight ? a.weight[ch] : 1.f) : 0.f;
+    sn[c] = n * w;
+    sd[c] = d * w;
+  }
+  __syncthreads();
+  const int P = t.join_lanes(), j = threadIdx.x & (P - 1);
+  for (int i = threadIdx.x / P; i < t.groups; i += 256 / P) {
+    const int lo = t.piece_lo(a, i) * E, hi = t.piece_hi(a, i) * E;
+    float n = 0.f, d = 0.f;
+    for (int c = lo + j; c < hi; c += P) {
+      n += sn[c];
+      d += sd[c];
+    }
+    for (int off = P / 2; off > 0; off >>= 1) {
+      n += __shfl_xor(n, off, kWave);
+      d += __shfl_xor(d, off, kWave);
+    }
+    if (j == 0) {
+      float* const to = a.part + 2 * (t.slot * (a.G + a.cblocks) + t.gA + i + t.cb);
+      to[0] = n;
+      to[1] = d;
+    }
+  }
+}
+
+template <typename T, int E>
+__global__ __launch_bounds__(256) void group_dx_kernel(GroupK<T> a) {
+  const GroupTile<T, E> t(a);
+  if (!t.pl.ok || t.pl.t1 <= t.pl.t0) return;
+  __shared__ float mgn[72], mg[72];
+  const int P = t.join_lanes(), j = threadIdx.x & (P - 1);
+  const float inv = 1.f / (static_cast<float>(t.pl.s1 - t.pl.s0) * static_cast<float>(a.C));
+  for (int i = threadIdx.x / P; i < t.groups; i += 256 / P) {
+    float n = 0.f, d = 0.f;
+    for_parts(t, a, t.gA + i, j, P, [&](const float* p, int, int) {
+      n += p[0];
+      d += p[1];
+    });
+    for (int off = P / 2; off > 0; off >>= 1) {
+      n += __shfl_xor(n, off, kWave);
+      d += __shfl_xor(d, off, kWave);
+    }
+    if (j == 0) {
+      mgn[i] = n * inv;
+      mg[i] = d * inv;
+    }
+  }
+  __syncthreads();
+  if (!t.have) return;
+  const float* const st = a.stats + 2 * (static_cast<int64_t>(t.pl.n) * a.G + t.c0 / a.C);
+  const float mu = st[0], rs = st[1], mn = mgn[t.c0 / a.C - t.gA], md = mg[t.c0 / a.C - t.gA];
+  float w[E], b[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    w[e] = a.weight ? a.weight[t.c0 + e] : 1.f;
+    b[e] = a.bias ? a.bias[t.c0 + e] : 0.f;
+  }
+#pragma unroll 2
+  for (int r = t.pl.t0 + t.rg; r < t.pl.t1; r += t.RG) {
+    float x[E], d[E];
+    get<T, E>(t.row(a.x, a, r), x);
+    get<T, E>(t.row(a.dy, a, r), d);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const float n = (x[e] - mu) * rs;
+      if (a.silu) {
+        const float p = fmaf(n, w[e], b[e]), sg = sigmoid_fast(p);
+        d[e] *= sg * fmaf(p, 1.f - sg, 1.f);
+      }
+      x[e] = rs * (d[e] * w[e] - md - n * mn);
+    }
+    put<T, E>(t.row(a.out, a, r), x);
+  }
+}
+
+// --- launches ------------------------------------------------------------------------------------
+
+GroupNormPlan group_norm_plan(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N, bool packed, bool vec, bool bwd) {
+  GroupNormPlan p{};
+  const int64_t C = D / G;
+  p.vec = vec && C % 8 == 0;
+  p.rows = T == 1 && !packed && C <= 8192;
+  if (p.rows) {
+    int lpr = 8, nv = 1;
+    (void)with_tile(static_cast<int>(C), [&](auto t) {
+      lpr = decltype(t)::LPR;
+      nv = decltype(t)::NV;
+      return hipSuccess;
+    });
+    (void)nv;
+    const int th = lpr > kNormThreads ? lpr : kNormThreads, rpb = th / lpr;
+    // rows of B in flight: whole workgroups of whole rows
+    const int64_t most = bwd ? 256 * (512 / th) : 256 * (1024 / th);
+    int64_t unit = rpb;  // rpb / gcd(rpb, G): a power of two
+    for (int64_t g = G; unit > 1 && g % 2 == 0; g /= 2) unit /= 2;
+    int64_t k = most * rpb / G / unit * unit;
+    const int64_t need = (B + unit - 1) / unit * unit;
+    k = k < unit ? unit : k > need ? need : k;
+    p.slots = k;
+    return p;
+  }
+  p.E = p.vec ? 8 : 1;
+  p.lanes = 64;
+  while (p.lanes > 1 && p.lanes / 2 * p.E >= D) p.lanes /= 2;
+  p.cblocks = static_cast<int>((D + p.lanes * p.E - 1) / (p.lanes * p.E));
+  const int64_t step = 256 / p.lanes;
+  int64_t L = B * T * p.cblocks / 1024;
+  L = L < 4 * step ? 4 * step : L > 512 ? 512 : L;
+  L = (L + step - 1) / step * step;
+  p.L = static_cast<int>(L);
+  p.slots = packed ? T / L + N + 1 : B * ((T + L - 1) / L);
+  return p;
+}
+
+static int64_t plan_floats(const GroupNormPlan& p, int64_t D, int64_t G, bool bwd) {
+  if (p.rows) return bwd ? p.slots * 2 * D : 0;
+  return p.slots * (G + p.cblocks) * 2 + (bwd ? p.slots * 2 * D : 0);
+}
+
+int64_t group_norm_floats(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N, bool packed, bool bwd) {
+  const int64_t a = plan_floats(group_norm_plan(B, T, D, G, N, packed, true, bwd), D, G, bwd);
+  const int64_t b = plan_floats(group_norm_plan(B, T, D, G, N, packed, false, bwd), D, G, bwd);
+  return a > b ? a : b;
+}
+
+int64_t group_norm_blocks(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N, bool packed, bool bwd) {
+  const GroupNormPlan a = group_norm_plan(B, T, D, G, N, packed, true, bwd), b = group_norm_plan(B, T, D, G, N, packed, false, bwd);
+  // rows: at most one workgroup of 256 or more threads per row
+  auto blocks = [&](const GroupNormPlan& p) { return p.rows ? p.slots * G * 2 : p.slots * p.cblocks; };
+  return blocks(a) > blocks(b) ? blocks(a) : blocks(b);
+}
+
+namespace {
+
+template <typename T, bool V> hipError_t rows_fwd(const GroupNormArgs& a, const GroupNormPlan& p, hipStream_t st) {
+  const int C = a.D / a.G;
+  return with_tile(C, [&](auto tile) {
+    constexpr int LPR = decltype(tile)::LPR, NV = decltype(tile)::NV;
+    if constexpr (LPR > 512) return hipErrorInvalidValue;  // the plan takes tiles then
+    else {
+    constexpr int TH = LPR > kNormThreads ? LPR : kNormThreads;
+    const NormShape s{static_cast<int64_t>(a.B) * a.G, C, a.eps, 1.f / C};
+    const int64_t stride = p.slots * a.G;
+    group_rows_fwd_kernel<T, V, LPR, NV><<<static_cast<unsigned>(stride / (TH / LPR)), TH, 0, st>>>(
+        static_cast<const T*>(a.x), a.weight, a.bias, s, a.G, stride, a.silu, static_cast<T*>(a.y), a.stats);
+    return hipGetLastError();
+    }
+  });
+}
+
+hipError_t param_sums(const GroupNormBwdArgs& a, const float* part, int64_t rows, hipStream_t st) {
+  float *dw = a.dweight, *db = a.dbias;
+  if (!dw && !db) return hipSuccess;
+  const int D = a.f.D;
+  return column_sums(part, rows, 2 * static_cast<int64_t>(D), 2 * D, st, [=] __device__(int col, float v) {
+    float* const to = col < D ? dw : db;
+    if (to) to[col < D ? col : col - D] = v;
+  });
+}
+
+template <typename T, bool V>
+hipError_t rows_bwd(const GroupNormBwdArgs& b, const GroupNormPlan& p, float* ws, hipStream_t st) {
+  const GroupNormArgs& a = b.f;
+  const int C = a.D / a.G;
+  float* const part = b.dweight || b.dbias ? ws : nullptr;
+  const hipError_t e = with_tile(C, [&](auto tile) {
+    constexpr int LPR = decltype(tile)::LPR, NV = decltype(tile)::NV;
+    if constexpr (LPR > 512) return hipErrorInvalidValue;
+    else {
+    constexpr int TH = LPR > kNormThreads ? LPR : kNormThreads;
+    const NormShape s{static_cast<int64_t>(a.B) * a.G, C, a.eps, 1.f / C};
+    const int64_t stride = p.slots * a.G;
+    group_rows_bwd_kernel<T, V, LPR, NV><<<static_cast<unsigned>(stride / (TH / LPR)), TH, 0, st>>>(
+        static_cast<const T*>(a.x), static_cast<const T*>(b.dy), a.stats, a.weight, a.bias, s, a.G, stride, a.silu,
+        static_cast<T*>(b.dx), part);
+    return hipGetLastError();
+    }
+  });
+  return e != hipSuccess ? e : param_sums(b, part, p.slots, st);
+}
+
+template <typename T> GroupK<T> group_args(const GroupNormArgs& a, const GroupNormPlan& p, float* ws) {
+  GroupK<T> k{};
+  k.x = static_cast<const T*>(a.x);
+  k.weight = a.weight;
+  k.bias = a.bias;
+  k.cu = a.cu_seqlens;
+  k.N = a.N;
+  k.Tn = a.T;
+  k.D = a.D;
+  k.G = a.G;
+  k.C = a.D / a.G;
+  k.L = p.L;
+  k.lanes = p.lanes;
+  k.cblocks = p.cblocks;
+  k.eps = a.eps;
+  k.silu = a.silu;
+  k.stats = a.stats;
+  k.part = ws;
+  return k;
+}
+
+template <typename T, int E> hipError_t seqs_fwd(const GroupNormArgs& a, const GroupNormPlan& p, float* ws, hipStream_t st) {
+  GroupK<T> k = group_args<T>(a, p, ws);
+  k.out = static_cast<T*>(a.y);
+  const unsigned grid = static_cast<unsigned>(p.slots * p.cblocks);
+  group_moments_kernel<T, E><<<grid, 256, 0, st>>>(k);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  group_apply_kernel<T, E><<<grid, 256, 0, st>>>(k);
+  return hipGetLastError();
+}
+
+template <typename T, int E>
+hipError_t seqs_bwd(const GroupNormBwdArgs& b, const GroupNormPlan& p, float* ws, hipStream_t st) {
+  const GroupNormArgs& a = b.f;
+  GroupK<T> k = group_args<T>(a, p, ws);
+  k.dy = static_cast<const T*>(b.dy);
+  k.out = static_cast<T*>(b.dx);
+  if (b.dweight || b.dbias) k.cols = ws + p.slots * (a.G + p.cblocks) * 2;
+  const unsigned grid = static_cast<unsigned>(p.slots * p.cblocks);
+  group_sums_kernel<T, E><<<grid, 256, 0, st>>>(k);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  group_dx_kernel<T, E><<<grid, 256, 0, st>>>(k);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  return param_sums(b, k.cols, p.slots, st);
+}
+
+template <typename T> hipError_t group_fwd_t(const GroupNormArgs& a, float* ws, hipStream_t st) {
+  const bool vec = norm_aligned(a.x) && norm_aligned(a.y);
+  const GroupNormPlan p = group_norm_plan(a.B, a.T, a.D, a.G, a.N, a.cu_seqlens != nullptr, vec, false);
+  if (p.rows) return p.vec ? rows_fwd<T, true>(a, p, st) : rows_fwd<T, false>(a, p, st);
+  return p.vec ? seqs_fwd<T, 8>(a, p, ws, st) : seqs_fwd<T, 1>(a, p, ws, st);
+}
+
+template <typename T> hipError_t group_bwd_t(const GroupNormBwdArgs& a, float* ws, hipStream_t st) {
+  const bool vec = norm_aligned(a.f.x) && norm_aligned(a.dy) && norm_aligned(a.dx);
+  const GroupNormPlan p = group_norm_plan(a.f.B, a.f.T, a.f.D, a.f.G, a.f.N, a.f.cu_seqlens != nullptr, vec, true);
+  if (p.rows) return p.vec ? rows_bwd<T, true>(a, p, ws, st) : rows_bwd<T, false>(a, p, ws, st);
+  return p.vec ? seqs_bwd<T, 8>(a, p, ws, st) : seqs_bwd<T, 1>(a, p, ws, st);
+}
+
+}  // namespace
+
+hipError_t launch_group_norm(const GroupNormArgs& a, float* ws, hipStream_t st) {
+  return a.dtype == COMBA_BF16 ? group_fwd_t<u16>(a, ws, st) : group_fwd_t<float>(a, ws, st);
+}
+
+hipError_t launch_group_norm_bwd(const GroupNormBwdArgs& a, float* ws, hipStream_t st) {
+  return a.f.dtype == COMBA_BF16 ? group_bwd_t<u16>(a, ws, st) : group_bwd_t<float>(a, ws, st);
+}
+
+}  // namespace comba

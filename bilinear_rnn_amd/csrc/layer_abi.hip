@@ -5,6 +5,7 @@
 #include <initializer_list>
 
 #include "comba.h"
+#include "group_norm.h"
 #include "layer.h"
 #include "linear_attn.h"
 
@@ -579,4 +580,86 @@ COMBA_API int32_t comba_linear_attn_bwd(const void* q, const void* k, const void
                              d_o, d_final_state, dq, dk, dv, dlog_decay, d_initial_state, f32(0), f32(w.grad),
                              f64(w.decay), f64(w.inner), f32(w.rdot), f64(w.hsum), H == num_qk_heads ? nullptr : f32(w.dqk)};
   return report_launch(comba::launch_attn_bwd(a, p, static_cast<hipStream_t>(stream)));
+}
+
+// --- group norm ----------------------------------------------------------------------------------
+
+namespace {
+
+int32_t check_group_norm(const void* x, int32_t D, int32_t G, int32_t dtype) {
+  if (!x) return report(COMBA_ERR_INVALID_ARG, "x must be non-NULL");
+  if (!known_dtype(dtype)) return report(COMBA_ERR_INVALID_ARG, "dtype must be COMBA_BF16 or COMBA_FP32");
+  if (D < 1 || G < 1 || D % G != 0) return report(COMBA_ERR_INVALID_ARG, "D and G must be >= 1 and G divide D");
+  if (D > kMaxWidth) return report(COMBA_ERR_UNSUPPORTED, "D above 2^22");
+  return COMBA_OK;
+}
+
+int32_t check_group_grid(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N, bool packed, bool bwd) {
+  if (comba::group_norm_blocks(B, T, D, G, N, packed, bwd) > kMaxBlocks)
+    return report(COMBA_ERR_UNSUPPORTED, "too many (token tile, channel) pairs for one launch");
+  return COMBA_OK;
+}
+
+size_t group_norm_bytes(int32_t B, int32_t T, int32_t D, int32_t G, int32_t num_seqs, bool bwd) {
+  if (B < 1 || T < 0 || D < 1 || D > kMaxWidth || G < 1 || D % G != 0 || static_cast<int64_t>(B) * T > kMaxTokens) return 0;
+  return up256(sizeof(float) * comba::group_norm_floats(B, T, D, G, num_seqs > 0 ? num_seqs : B, num_seqs > 0, bwd));
+}
+
+}  // namespace
+
+COMBA_API size_t comba_group_norm_workspace_size(int32_t B, int32_t T, int32_t D, int32_t G, int32_t num_seqs) {
+  return group_norm_bytes(B, T, D, G, num_seqs, false);
+}
+
+COMBA_API int32_t comba_group_norm_fwd(const void* x, const float* weight, const float* bias, const int32_t* cu_seqlens,
+                                       int32_t num_seqs, int32_t B, int32_t T, int32_t D, int32_t G, float eps,
+                                       int32_t dtype, int32_t silu, void* y, float* stats, void* workspace,
+                                       size_t workspace_bytes, void* stream) {
+  int32_t rc = check_group_norm(x, D, G, dtype);
+  if (rc != COMBA_OK) return rc;
+  if (!y) return report(COMBA_ERR_INVALID_ARG, "y must be non-NULL");
+  if (!(eps >= 0.f) || std::isinf(eps)) return report(COMBA_ERR_INVALID_ARG, "eps must be >= 0 and finite");
+  int64_t N = 0;
+  if ((rc = check_batch(cu_seqlens, num_seqs, B, T, N)) != COMBA_OK) return rc;
+  if ((rc = check_group_grid(B, T, D, G, N, cu_seqlens != nullptr, false)) != COMBA_OK) return rc;
+  const size_t need = group_norm_bytes(B, T, D, G, cu_seqlens ? num_seqs : 0, false);
+  rc = check_workspace(workspace, workspace_bytes, need,
+                       "workspace is NULL or smaller than comba_group_norm_workspace_size()");
+  if (rc != COMBA_OK) return rc;
+  const int64_t act = static_cast<int64_t>(B) * T * D * size_of(dtype), par = 4ll * D;
+  rc = check_apart({{y, act}, {stats, 8 * N * G}, {workspace, static_cast<int64_t>(need)}},
+                   {{x, act}, {weight, par}, {bias, par}, {cu_seqlens, 4 * (N + 1)}});
+  if (rc != COMBA_OK) return rc;
+  const comba::GroupNormArgs a{x, weight, bias, cu_seqlens, static_cast<int>(N), B, T, D, G, dtype, eps, silu != 0, y, stats};
+  return report_launch(comba::launch_group_norm(a, static_cast<float*>(workspace), static_cast<hipStream_t>(stream)));
+}
+
+COMBA_API size_t comba_group_norm_bwd_workspace_size(int32_t B, int32_t T, int32_t D, int32_t G, int32_t num_seqs) {
+  return group_norm_bytes(B, T, D, G, num_seqs, true);
+}
+
+COMBA_API int32_t comba_group_norm_bwd(const void* x, const void* dy, const float* stats, const float* weight,
+                                       const float* bias, const int32_t* cu_seqlens, int32_t num_seqs, int32_t B, int32_t T,
+                                       int32_t D, int32_t G, int32_t dtype, int32_t silu, void* dx, float* dweight,
+                                       float* dbias, void* workspace, size_t workspace_bytes, void* stream) {
+  int32_t rc = check_group_norm(x, D, G, dtype);
+  if (rc != COMBA_OK) return rc;
+  if (!dy || !stats || !dx) return report(COMBA_ERR_INVALID_ARG, "dy, stats and dx must be non-NULL");
+  if ((weight == nullptr) != (dweight == nullptr) || (bias == nullptr) != (dbias == nullptr))
+    return report(COMBA_ERR_INVALID_ARG, "a gradient is given exactly when its input is");
+  int64_t N = 0;
+  if ((rc = check_batch(cu_seqlens, num_seqs, B, T, N)) != COMBA_OK) return rc;
+  if ((rc = check_group_grid(B, T, D, G, N, cu_seqlens != nullptr, true)) != COMBA_OK) return rc;
+  const size_t need = group_norm_bytes(B, T, D, G, cu_seqlens ? num_seqs : 0, true);
+  rc = check_workspace(workspace, workspace_bytes, need,
+                       "workspace is NULL or smaller than comba_group_norm_bwd_workspace_size()");
+  if (rc != COMBA_OK) return rc;
+  const int64_t act = static_cast<int64_t>(B) * T * D * size_of(dtype), par = 4ll * D;
+  rc = check_apart({{dx, act}, {dweight, par}, {dbias, par}, {workspace, static_cast<int64_t>(need)}},
+                   {{x, act}, {dy, act}, {stats, 8 * N * G}, {weight, par}, {bias, par}, {cu_seqlens, 4 * (N + 1)}});
+  if (rc != COMBA_OK) return rc;
+  const comba::GroupNormBwdArgs a{{x, weight, bias, cu_seqlens, static_cast<int>(N), B, T, D, G, dtype, 0.f, silu != 0,
+                                   nullptr, const_cast<float*>(stats)},
+                                  dy, dx, dweight, dbias};
+  return report_launch(comba::launch_group_norm_bwd(a, static_cast<float*>(workspace), static_cast<hipStream_t>(stream)));
 }

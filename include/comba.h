@@ -658,6 +658,47 @@ int32_t comba_linear_attn_bwd(const void* q, const void* k, const void* v, const
                               void* dv, float* dlog_decay, float* d_initial_state, void* workspace,
                               size_t workspace_bytes, void* stream);
 
+/*
+ * Group norm over channels-last activations, with optional SiLU. The D channels
+ * form G groups of C = D / G neighbours; per sequence and group, with mean and
+ * var (the mean of the squared distances) over its tokens and C channels:
+ *     p = (x - mean) / sqrt(var + eps) * weight + bias
+ *     y = p, or with `silu` (non-zero) p * sigmoid(p)
+ * With T == 1 every token is normalised alone: the heads of a recurrence's
+ * output are then the groups, each channel with a weight of its own (where
+ * comba_block_norm_fwd's heads share one). With cu_seqlens the statistics are
+ * those of every packed sequence.
+ *   x, y           [B, T, D]     dtype
+ *   weight, bias   [D]           float32, either may be NULL (1, 0)
+ *   stats          [N, G, 2]     float32: mean and 1 / sqrt(var + eps) (0, 0 of an
+ *                                empty sequence), what the backward takes; may be
+ *                                NULL (not written)
+ * Sequences of more than one token need workspace of
+ * comba_group_norm_workspace_size(...) bytes, 256-byte aligned (0: none, NULL is
+ * accepted). num_seqs is N with cu_seqlens and 0 without.
+ * comba_group_norm_bwd: gradients for dy = dL/dy [B, T, D] (dtype), from x and
+ * the forward's stats:
+ *   dx [B, T, D] dtype; dweight, dbias [D] float32, each exactly when its input
+ *   is given
+ * It needs comba_group_norm_bwd_workspace_size(...) bytes, 256-byte aligned.
+ * Both give the same bits on every run. A group's value that is infinite or NaN makes
+ * all of its sequence's values in that group NaN.
+ * Errors: COMBA_ERR_UNSUPPORTED for D > 2^22, more than 2^31 - 2^16 tokens, and
+ * for launches of more than 2^32 - 1 threads.
+ */
+size_t comba_group_norm_workspace_size(int32_t B, int32_t T, int32_t D, int32_t G, int32_t num_seqs);
+
+int32_t comba_group_norm_fwd(const void* x, const float* weight, const float* bias, const int32_t* cu_seqlens,
+                             int32_t num_seqs, int32_t B, int32_t T, int32_t D, int32_t G, float eps, int32_t dtype,
+                             int32_t silu, void* y, float* stats, void* workspace, size_t workspace_bytes, void* stream);
+
+size_t comba_group_norm_bwd_workspace_size(int32_t B, int32_t T, int32_t D, int32_t G, int32_t num_seqs);
+
+int32_t comba_group_norm_bwd(const void* x, const void* dy, const float* stats, const float* weight, const float* bias,
+                             const int32_t* cu_seqlens, int32_t num_seqs, int32_t B, int32_t T, int32_t D, int32_t G,
+                             int32_t dtype, int32_t silu, void* dx, float* dweight, float* dbias, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -225,3 +225,46 @@ def linear_attention(q, k, v, log_decay, scale=1.0, init=None, cu=None, do=None,
         return o, fin
     return dict(dq=dq, dk=dk, dv=dv, dlog_decay=np.nansum(dg, (0, 1)) if head else dg,
                 dinitial_state=None if init is None else dinit)
+
+
+def group_norm(x, groups, weight=None, bias=None, eps=1e-5, silu=False, cu=None, dy=None, magnitude=False):
+    """x [B, T, D]. Returns (y, stats), or with dy a dict of the gradients. ``magnitude``: the terms of x - mean
+    and of p are added up as absolute values; a relative error of 1 / deviation shows in p itself."""
+    x, weight, bias, dy = (_f(v) for v in (x, weight, bias, dy))
+    mag = np.abs if magnitude else (lambda v: v)
+    B, T, D = x.shape
+    C, N = D // groups, _num_seqs(B, cu)
+    w = (np.ones(D) if weight is None else weight).reshape(groups, C)
+    b = (np.zeros(D) if bias is None else bias).reshape(groups, C)
+    y, dx = np.full_like(x, np.nan), np.full_like(x, np.nan)
+    stats, dw, db = np.zeros((N, groups, 2)), np.zeros(D), np.zeros(D)
+    for n, row, t0, t1 in _segments(B, T, cu):
+        if t1 == t0:
+            continue
+        u = x[row, t0:t1].reshape(t1 - t0, groups, C)
+        mean = u.mean((0, 2))
+        rstd = 1.0 / np.sqrt(((u - mean[:, None]) ** 2).mean((0, 2)) + eps)
+        stats[n] = np.stack([np.abs(u).mean((0, 2)) if magnitude else mean, rstd], -1)
+        h = (u - mean[:, None]) * rstd[:, None]
+        hm = (np.abs(u) + np.abs(u).mean((0, 2))[:, None]) * rstd[:, None]  # how far h may be off
+        p = h * w + b
+        pm = hm * np.abs(w) + np.abs(b)
+        s = sigmoid(p)
+        y[row, t0:t1] = (1.1 * pm if magnitude else p * s if silu else p).reshape(-1, D)
+        if dy is None:
+            continue
+        d = dy[row, t0:t1].reshape(u.shape)
+        if silu:  # the slope's own slope is at most 0.5
+            d = np.abs(d) * (1.1 + 0.5 * pm) if magnitude else d * s * (1 + p * (1 - s))
+        d = mag(d)
+        if magnitude:
+            h = hm
+        g = d * mag(w)
+        sign = 1.0 if magnitude else -1.0
+        dx[row, t0:t1] = (rstd[:, None] * (g + sign * g.mean((0, 2))[:, None] +
+                                           sign * h * (g * h).mean((0, 2))[:, None])).reshape(-1, D)
+        dw += (d * h).sum(0).reshape(D)
+        db += d.sum(0).reshape(D)
+    if dy is None:
+        return y, stats
+    return dict(dx=dx, dweight=None if weight is None else dw, dbias=None if bias is None else db)
