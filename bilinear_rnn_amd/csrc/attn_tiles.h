@@ -20,7 +20,6 @@ namespace comba {
 template <typename T> struct Tiles;
 
 template <> struct Tiles<u16> {
-  static constexpr int CH = 64;         // tokens per chunk
   static constexpr int BLK = 32;        // reduction indices per block
   static constexpr int PIECE = 8;       // elements of 16 bytes
   typedef bf16x8 Frag;
@@ -71,10 +70,11 @@ template <> struct Tiles<u16> {
     split<NT>({a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}, out);
   }
   static __device__ __forceinline__ f32x4 mma(const Frag& a, const Frag& b, f32x4 c) { return mfma16x16x32(a, b, c); }
-  // Score tiles: [NT][CH][CH], the source axis along the row, its 32-blocks in perm32 order. A result
-  // tile of sources 16 j + 4 g + i and target t:
-  template <int NT> static __device__ __forceinline__ void put_scores(u16* p, int t, int j, int g, const f32x4& x) {
-    const int at = swz<64>(t, 32 * (j >> 1) + 8 * g + 4 * (j & 1));
+  // Score tiles of CH tokens: [NT][CH][CH], the source axis along the row, its 32-blocks in perm32 order. A
+  // result tile of sources 16 j + 4 g + i and target t:
+  template <int CH, int NT>
+  static __device__ __forceinline__ void put_scores(u16* p, int t, int j, int g, const f32x4& x) {
+    const int at = swz<CH>(t, 32 * (j >> 1) + 8 * g + 4 * (j & 1));
     float r[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -88,14 +88,13 @@ template <> struct Tiles<u16> {
       *reinterpret_cast<u32x2*>(p + n * CH * CH + at) = w;
     }
   }
-  static __device__ __forceinline__ Frag scores(const u16* p, int n, int t, int b, int g) {
-    return lds8(p + n * CH * CH + swz<64>(t, 32 * b + 8 * g));
+  template <int CH> static __device__ __forceinline__ Frag scores(const u16* p, int n, int t, int b, int g) {
+    return lds8(p + n * CH * CH + swz<CH>(t, 32 * b + 8 * g));
   }
-  static constexpr int score_elems(int nt) { return nt * CH * CH; }
+  static constexpr int score_elems(int CH, int nt) { return nt * CH * CH; }
 };
 
 template <> struct Tiles<float> {
-  static constexpr int CH = 32;
   static constexpr int BLK = 16;
   static constexpr int PIECE = 4;
   typedef f32x4 Frag;
@@ -127,51 +126,73 @@ template <> struct Tiles<float> {
     for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i], b[i], c, 0, 0, 0);
     return c;
   }
-  template <int NT> static __device__ __forceinline__ void put_scores(float* p, int t, int j, int g, const f32x4& x) {
+  template <int CH, int NT>
+  static __device__ __forceinline__ void put_scores(float* p, int t, int j, int g, const f32x4& x) {
     *reinterpret_cast<f32x4*>(p + at<CH>(t, 16 * j + 4 * g)) = x;
   }
-  static __device__ __forceinline__ Frag scores(const float* p, int, int t, int b, int g) {
+  template <int CH> static __device__ __forceinline__ Frag scores(const float* p, int, int t, int b, int g) {
     return *reinterpret_cast<const f32x4*>(p + at<CH>(t, 16 * b + 4 * g));
   }
-  static constexpr int score_elems(int) { return size(CH, CH); }
+  static constexpr int score_elems(int CH, int) { return size(CH, CH); }
 };
 
-// 16 bytes of a row of `dim` elements from column `col` on, as registers. Rows may start at any
-// element-aligned address. fetch() reads whole pieces inside the row (a row's last, ragged piece moved back;
-// rows shorter than a piece element by element); place() brings the elements to their places, with zeros
-// behind the row's end.
-template <typename T> struct RowPiece {
+// Wavefront inclusive prefix sum in double, by DPP moves (see wave_scan_dpp).
+template <int CTRL, int ROWS> __device__ __forceinline__ double dpp_or_zero(double x) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(b), CTRL, ROWS, 0xf, ROWS == 0xf);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(b >> 32), CTRL, ROWS, 0xf, ROWS == 0xf);
+  return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+__device__ __forceinline__ double wave_scan_f64_dpp(double x) {
+  x += dpp_or_zero<0x111, 0xf>(x);
+  x += dpp_or_zero<0x112, 0xf>(x);
+  x += dpp_or_zero<0x114, 0xf>(x);
+  x += dpp_or_zero<0x118, 0xf>(x);
+  x += dpp_or_zero<0x142, 0xa>(x);
+  x += dpp_or_zero<0x143, 0xc>(x);
+  return x;
+}
+
+// 16-byte pieces of a chunk's rows of `dim` elements, `stride` elements apart: piece p is 16 bytes of row p / PPR
+// from column (p % PPR) * E + c0 on. Rows and columns that are not there are read as zeros.
+// WHOLE: dim is a multiple of the piece and the rows lie on 16-byte boundaries: loads go through a range that
+// ends with the chunk's last row, and what is constant over the chunks is in the offset. Otherwise a
+// row's last, ragged piece is read moved back, so that it lies inside the row (dim >= E), and brought to its
+// place in registers.
+template <typename T, bool WHOLE> struct Pieces {
   static constexpr int E = Tiles<T>::PIECE;
-  static __device__ __forceinline__ u32x4 fetch(const T* row, int col, int dim) {
-    if (dim >= E) {
-      const int c = col + E <= dim ? col : dim - E;
-      return reinterpret_cast<const Loose<u32x4>*>(row + c)->v;
-    }
-    float x[E];
-#pragma unroll
-    for (int i = 0; i < E; ++i) x[i] = col + i < dim ? Elem<T>::load(row, col + i) : 0.f;
-    return Pack<T, E, true>::words(x);
+  // Offset of a piece (bytes), or nowhere.
+  static __device__ __forceinline__ uint32_t offset(int row, int col, int stride, int dim) {
+    if constexpr (WHOLE) return col < dim ? (static_cast<uint32_t>(row) * stride + col) * sizeof(T) : kNowhere;
+    else return static_cast<uint32_t>(min(col, dim - E));
   }
-  static __device__ __forceinline__ u32x4 place(u32x4 w, int col, int dim, bool live) {
-    if (dim >= E && dim % E != 0) {
-      const int over = col + E - dim;  // elements behind the row's end
-      if (over > 0) {
-        const int bits = over * 8 * static_cast<int>(sizeof(T));
-        uint64_t lo = static_cast<uint64_t>(w[1]) << 32 | w[0], hi = static_cast<uint64_t>(w[3]) << 32 | w[2];
-        if (bits >= 128) {
-          lo = hi = 0;
-        } else if (bits >= 64) {
-          lo = hi >> (bits - 64);
-          hi = 0;
-        } else {
-          lo = lo >> bits | hi << (64 - bits);
-          hi >>= bits;
-        }
-        w = u32x4{static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32), static_cast<uint32_t>(hi),
-                  static_cast<uint32_t>(hi >> 32)};
-      }
+  struct Rows {
+    const T* base;            // the chunk's first row
+    int n, stride, dim;       // rows of the chunk
+  };
+  static __device__ __forceinline__ u32x4 fetch(const Rows& c, uint32_t off, int row) {
+    if constexpr (WHOLE) {
+      return Range<T>(c.base, (static_cast<int64_t>(c.n - 1) * c.stride + c.dim) * sizeof(T)).load16(off);
+    } else {
+      const uint32_t at = static_cast<uint32_t>(min(row, c.n - 1)) * c.stride + off;
+      return reinterpret_cast<const Loose<u32x4>*>(c.base + at)->v;
     }
-    return live && col < dim ? w : u32x4{0, 0, 0, 0};
+  }
+  static __device__ __forceinline__ u32x4 place(u32x4 w, int row, int n, int col, int dim) {
+    if constexpr (WHOLE) return w;
+    const int over = col + E - dim;  // elements behind the row's end
+    const int bits = over > 0 ? over * 8 * static_cast<int>(sizeof(T)) : 0;
+    uint64_t lo = static_cast<uint64_t>(w[1]) << 32 | w[0], hi = static_cast<uint64_t>(w[3]) << 32 | w[2];
+    if (bits >= 64) {
+      lo = hi;
+      hi = 0;
+    }
+    const int in = bits & 63;
+    lo = lo >> in | (in ? hi << (64 - in) : 0);
+    hi >>= in;
+    if (row >= n || col >= dim) lo = hi = 0;
+    return u32x4{static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32), static_cast<uint32_t>(hi),
+                 static_cast<uint32_t>(hi >> 32)};
   }
 };
 

@@ -429,15 +429,18 @@ int32_t check_attn(const void* q, const void* k, const void* v, const float* log
   if (!known_dtype(dtype)) return report(COMBA_ERR_INVALID_ARG, "dtype must be COMBA_BF16 or COMBA_FP32");
   if (H < 1 || Hk < 1 || H % Hk != 0) return report(COMBA_ERR_INVALID_ARG, "num_qk_heads must be >= 1 and divide H");
   if (K < 1 || V < 1) return report(COMBA_ERR_INVALID_ARG, "K and V must be >= 1");
+  if (K < comba::kAttnMinWidth || V < comba::kAttnMinWidth) return report(COMBA_ERR_UNSUPPORTED, "K or V below 8");
   if (!std::isfinite(scale)) return report(COMBA_ERR_INVALID_ARG, "scale must be finite");
   if (K > comba::kAttnMaxWidth || V > comba::kAttnMaxWidth) return report(COMBA_ERR_UNSUPPORTED, "K or V above 256");
-  if (H > kMaxWidth) return report(COMBA_ERR_UNSUPPORTED, "H above 2^22");
+  // the tokens of a chunk are addressed with 32-bit offsets
+  if (static_cast<int64_t>(H) * (K > V ? K : V) > kMaxWidth) return report(COMBA_ERR_UNSUPPORTED, "H * max(K, V) above 2^22");
   return COMBA_OK;
 }
 
 bool attn_sizes_ok(int32_t B, int32_t T, int32_t H, int32_t Hk, int32_t K, int32_t V) {
-  return B >= 1 && T >= 0 && H >= 1 && H <= kMaxWidth && Hk >= 1 && H % Hk == 0 && K >= 1 && K <= comba::kAttnMaxWidth &&
-         V >= 1 && V <= comba::kAttnMaxWidth && static_cast<int64_t>(B) * T <= kMaxTokens;
+  return B >= 1 && T >= 0 && H >= 1 && static_cast<int64_t>(H) * (K > V ? K : V) <= kMaxWidth &&
+         Hk >= 1 && H % Hk == 0 && K >= comba::kAttnMinWidth && K <= comba::kAttnMaxWidth &&
+         V >= comba::kAttnMinWidth && V <= comba::kAttnMaxWidth && static_cast<int64_t>(B) * T <= kMaxTokens;
 }
 
 // Column blocks of the largest launch per (segment, head), and the blocks of the scan over segments.
@@ -469,7 +472,7 @@ AttnBwdWs attn_bwd_ws(const comba::AttnPlan& p, int64_t tokens, int64_t H, int64
   w.decay = 2 * states;
   w.inner = w.decay + up256(d * p.slots * H);
   w.rdot = w.inner + up256(d * p.slots * H * comba::attn_inner_blocks(K, V));
-  w.hsum = w.rdot + up256(sizeof(float) * 2 * comba::attn_blocks(K) * tokens * H);
+  w.hsum = w.rdot + up256(sizeof(float) * 4 * comba::attn_blocks(K) * tokens * H);
   w.dqk = w.hsum + up256(d * p.slots * H);
   w.total = w.dqk + (H == Hk ? 0 : up256(sizeof(float) * 2 * tokens * H * K));
   return w;

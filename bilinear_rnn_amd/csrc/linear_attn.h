@@ -50,13 +50,15 @@ struct AttnBwdArgs {
                               // gradient at its end
   double* decay;              // [slots, H]
   double* inner;              // [slots, H, attn_inner_blocks]: <gradient at the end, state at the end>, in parts
-  float* rdot;                // [2, K blocks, B * T, H]: q . dq and k . dk over 64 columns each
+  float* rdot;                // [4, K blocks, H, B * T]: q . dq, its part from the states, and k . dk, its part,
+                              // over 64 columns each
   double* hsum;               // [slots, H]: sums of dlog_decay (constant decays)
   float* dqk;                 // [2, B * T, H, K]: dq and dk of every value head (shared q / k heads), else null
 };
 
 // Widest head; the state's tiles of one wavefront stay in its registers.
 constexpr int kAttnMaxWidth = 256;
+constexpr int kAttnMinWidth = 8;  // a 16-byte piece of bf16
 constexpr int kAttnBlock = 64;  // output columns per workgroup
 __host__ __device__ inline int attn_blocks(int width) { return (width + kAttnBlock - 1) / kAttnBlock; }
 // Elements of a state that a workgroup of the scan over segments takes.

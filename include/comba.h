@@ -631,8 +631,8 @@ int32_t comba_block_norm_bwd(const void* y, const void* gate, const void* residu
  *   d_initial_state [N, H, V, K] float32 (may be NULL: not written).
  * It needs comba_linear_attn_bwd_workspace_size(...) bytes, 256-byte aligned.
  * All three give the same bits on every run.
- * Errors: COMBA_ERR_UNSUPPORTED for K or V above 256, H above 2^22, more than
- * 2^31 - 2^16 tokens, and for launches of more than 2^32 - 1 threads.
+ * Errors: COMBA_ERR_UNSUPPORTED for K or V below 8 or above 256, H max(K, V)
+ * above 2^22, more than 2^31 - 2^16 tokens, and for launches of more than 2^32 - 1 threads.
  */
 size_t comba_linear_attn_workspace_size(int32_t B, int32_t T, int32_t H, int32_t num_qk_heads, int32_t K, int32_t V,
                                         int32_t num_seqs);

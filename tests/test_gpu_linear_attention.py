@@ -41,16 +41,16 @@ def gamma(K, V, T, dtype, exact=False, ways=1):
 
 
 CASES = [  # B, T, H, Hk, K, V, dtype, lens, head, init
-    (1, 1, 1, 1, 1, 1, F32, None, False, True),
+    (1, 1, 1, 1, 8, 8, F32, None, False, True),
     (2, 1, 2, 2, 64, 64, BF16, None, False, True),
-    (1, 2, 3, 1, 3, 5, BF16, None, True, True),
+    (1, 2, 3, 1, 9, 11, BF16, None, True, True),
     (2, 31, 2, 2, 16, 64, F32, None, False, False),
     (1, 32, 2, 1, 64, 65, F32, None, True, True),
     (2, 33, 4, 2, 65, 17, F32, None, False, True),
     (1, 63, 1, 1, 128, 128, BF16, None, False, False),
     (2, 64, 2, 2, 128, 64, BF16, None, True, True),
     (1, 65, 2, 2, 64, 128, BF16, None, False, True),
-    (1, 130, 2, 2, 129, 7, BF16, None, False, True),
+    (1, 130, 2, 2, 129, 9, BF16, None, False, True),
     (1, 100, 1, 1, 256, 256, BF16, None, False, True),
     (1, 70, 1, 1, 256, 200, F32, None, False, True),
     (2, 200, 3, 3, 72, 99, BF16, None, False, True),
@@ -95,7 +95,7 @@ def test_backward(B, T, H, Hk, K, V, dtype, lens, head, init):
     check("dlog_decay", got["dlog_decay"], r["dlog_decay"], m["dlog_decay"], gamma(K, V, T, dtype, exact=True, ways=3))
 
 
-@pytest.mark.parametrize("N,H,Hk,K,V,dtype,head", [(1, 1, 1, 1, 1, F32, False), (3, 2, 2, 64, 64, BF16, False),
+@pytest.mark.parametrize("N,H,Hk,K,V,dtype,head", [(1, 1, 1, 8, 8, F32, False), (3, 2, 2, 64, 64, BF16, False),
                                                   (2, 4, 2, 128, 128, BF16, True), (5, 3, 1, 72, 99, F32, False),
                                                   (2, 2, 2, 255, 17, BF16, False), (1, 2, 1, 256, 256, F32, True),
                                                   (70, 16, 16, 128, 40, BF16, False)])
