@@ -17,6 +17,18 @@
 
 namespace comba {
 
+// What two floats lose when they are rounded to the bf16 pair h, exactly: a dot product with (-1, 0) or (0, -1)
+// instead of a shift or mask and a subtraction. (The constants are hidden from the compiler, which would make
+// the inline constant -1.0 of one, and the hardware reads that as the other.)
+struct LostParts {
+  unsigned first = 0xbf80u, second = 0xbf800000u;
+  __device__ __forceinline__ LostParts() { asm("" : "+s"(first), "+s"(second)); }
+  __device__ __forceinline__ void operator()(unsigned h, float& a, float& b) const {
+    a = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, h), __builtin_bit_cast(bf16x2, first), a, false);
+    b = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, h), __builtin_bit_cast(bf16x2, second), b, false);
+  }
+};
+
 template <typename T> struct Tiles;
 
 template <> struct Tiles<u16> {
@@ -24,9 +36,13 @@ template <> struct Tiles<u16> {
   static constexpr int PIECE = 8;       // elements of 16 bytes
   typedef bf16x8 Frag;
   typedef u16 P;                        // element of the score tiles
-  // Elements of an LDS tile of R rows of L elements, and an element's place. Whole 16-byte pieces stay whole.
+  // LDS tiles of R rows of L elements keep 16-byte pieces whole: place `slot` of a row holds piece
+  // piece_at(row, slot) of it.
   static constexpr int size(int R, int L) { return R * L; }
-  template <int L> static __device__ __forceinline__ int at(int row, int col) { return swz<L>(row, col); }
+  template <int L> static __device__ __forceinline__ int piece_at(int row, int slot) {
+    return (swz<L>(row, 8 * slot) & (L - 1)) >> 3;
+  }
+  static constexpr int pitch(int L) { return L; }  // elements from a row to the next
   // Result row 4 g + i of tile j of a reduction axis <-> index on that axis.
   static __device__ __forceinline__ int index(int j, int g, int i) { return 32 * (j >> 1) + 8 * g + 4 * (j & 1) + i; }
   // Operand whose reduction runs along a tile's row: block p of row `row`.
@@ -51,14 +67,14 @@ template <> struct Tiles<u16> {
   // NT terms of eight values.
   template <int NT> static __device__ __forceinline__ void split(const float (&x)[8], Frag (&out)[NT]) {
     unsigned w[NT][4];
+    const LostParts lost;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float a = x[2 * i], b = x[2 * i + 1];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         w[t][i] = __builtin_bit_cast(unsigned, __builtin_convertvector((f32x2){a, b}, bf16x2));
-        a -= __uint_as_float(w[t][i] << 16);
-        b -= __uint_as_float(w[t][i] & 0xffff0000u);
+        if (t + 1 < NT) lost(w[t][i], a, b);
       }
     }
 #pragma unroll
@@ -76,14 +92,14 @@ template <> struct Tiles<u16> {
   static __device__ __forceinline__ void put_scores(u16* p, int t, int j, int g, const f32x4& x) {
     const int at = swz<CH>(t, 32 * (j >> 1) + 8 * g + 4 * (j & 1));
     float r[4] = {x[0], x[1], x[2], x[3]};
+    const LostParts lost;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       u32x2 w;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         w[i] = __builtin_bit_cast(unsigned, __builtin_convertvector((f32x2){r[2 * i], r[2 * i + 1]}, bf16x2));
-        r[2 * i] -= __uint_as_float(w[i] << 16);
-        r[2 * i + 1] -= __uint_as_float(w[i] & 0xffff0000u);
+        if (n + 1 < NT) lost(w[i], r[2 * i], r[2 * i + 1]);
       }
       *reinterpret_cast<u32x2*>(p + n * CH * CH + at) = w;
     }
@@ -99,16 +115,20 @@ template <> struct Tiles<float> {
   static constexpr int PIECE = 4;
   typedef f32x4 Frag;
   typedef float P;
-  // Rows lie 4 floats further apart than they are long: 16 rows' pieces at one column then cover all banks.
-  static constexpr int size(int R, int L) { return R * (L + 4); }
-  template <int L> static __device__ __forceinline__ int at(int row, int col) { return row * (L + 4) + col; }
+  // Rows lie 4 floats further apart than they are long: 16 rows' pieces at one column cover all banks, and so do
+  // 16 neighbouring columns of four rows that are four apart. (No exclusive-or in the addresses, as bf16 tiles have:
+  // single floats are read down a column, and every tile would have four addresses of its own.)
+  static constexpr int pitch(int L) { return L + 4; }
+  static constexpr int size(int R, int L) { return R * pitch(L); }
+  template <int L> static __device__ __forceinline__ int piece_at(int, int slot) { return slot; }
+  template <int L> static __device__ __forceinline__ int at(int row, int col) { return row * pitch(L) + col; }
   static __device__ __forceinline__ int index(int j, int g, int i) { return 16 * j + 4 * g + i; }
   template <int L> static __device__ __forceinline__ Frag along(const float* t, int row, int p, int g) {
     return *reinterpret_cast<const f32x4*>(t + at<L>(row, 16 * p + 4 * g));
   }
   template <int L> static __device__ __forceinline__ Frag down(const float* t, int b, int col0, int g, int l16) {
     const float* c = t + at<L>(16 * b + 4 * g, col0 + l16);
-    return f32x4{c[0], c[L + 4], c[2 * (L + 4)], c[3 * (L + 4)]};
+    return f32x4{c[0], c[pitch(L)], c[2 * pitch(L)], c[3 * pitch(L)]};
   }
   template <int L> static __device__ __forceinline__ Frag down_index(const float* t, int b, int j, int g, int l16) {
     return down<L>(t, b, 16 * j, g, l16);
@@ -126,14 +146,15 @@ template <> struct Tiles<float> {
     for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i], b[i], c, 0, 0, 0);
     return c;
   }
+  // Score tiles: rows 4 floats further apart than they are long.
   template <int CH, int NT>
   static __device__ __forceinline__ void put_scores(float* p, int t, int j, int g, const f32x4& x) {
-    *reinterpret_cast<f32x4*>(p + at<CH>(t, 16 * j + 4 * g)) = x;
+    *reinterpret_cast<f32x4*>(p + t * (CH + 4) + 16 * j + 4 * g) = x;
   }
   template <int CH> static __device__ __forceinline__ Frag scores(const float* p, int, int t, int b, int g) {
-    return *reinterpret_cast<const f32x4*>(p + at<CH>(t, 16 * b + 4 * g));
+    return *reinterpret_cast<const f32x4*>(p + t * (CH + 4) + 16 * b + 4 * g);
   }
-  static constexpr int score_elems(int CH, int) { return size(CH, CH); }
+  static constexpr int score_elems(int CH, int) { return CH * (CH + 4); }
 };
 
 // Wavefront inclusive prefix sum in double, by DPP moves (see wave_scan_dpp).
@@ -153,29 +174,36 @@ __device__ __forceinline__ double wave_scan_f64_dpp(double x) {
   return x;
 }
 
-// 16-byte pieces of a chunk's rows of `dim` elements, `stride` elements apart: piece p is 16 bytes of row p / PPR
-// from column (p % PPR) * E + c0 on. Rows and columns that are not there are read as zeros.
+// 16-byte pieces of a chunk's rows of `dim` elements, `stride` elements apart, in LDS from the chunk's first
+// token on or, when time runs back, from its last. Rows and columns that are not there are read as zeros.
 // WHOLE: dim is a multiple of the piece and the rows lie on 16-byte boundaries: loads go through a range that
 // ends with the chunk's last row, and what is constant over the chunks is in the offset. Otherwise a
 // row's last, ragged piece is read moved back, so that it lies inside the row (dim >= E), and brought to its
 // place in registers.
-template <typename T, bool WHOLE> struct Pieces {
+template <typename T, bool WHOLE, int CH> struct Pieces {
   static constexpr int E = Tiles<T>::PIECE;
-  // Offset of a piece (bytes), or nowhere.
-  static __device__ __forceinline__ uint32_t offset(int row, int col, int stride, int dim) {
-    if constexpr (WHOLE) return col < dim ? (static_cast<uint32_t>(row) * stride + col) * sizeof(T) : kNowhere;
-    else return static_cast<uint32_t>(min(col, dim - E));
-  }
   struct Rows {
     const T* base;            // the chunk's first row
     int n, stride, dim;       // rows of the chunk
+    bool back;
   };
+  // What stays the same over the chunks for the piece of LDS row `row` from column `col` on.
+  static __device__ __forceinline__ uint32_t offset(int row, int col, int stride, int dim, bool back) {
+    if constexpr (WHOLE)
+      return col < dim ? (static_cast<uint32_t>(back ? CH - 1 - row : row) * stride + col) * sizeof(T) : kNowhere;
+    else
+      return static_cast<uint32_t>(min(col, dim - E));
+  }
   static __device__ __forceinline__ u32x4 fetch(const Rows& c, uint32_t off, int row) {
     if constexpr (WHOLE) {
-      return Range<T>(c.base, (static_cast<int64_t>(c.n - 1) * c.stride + c.dim) * sizeof(T)).load16(off);
+      // backwards, rows that a short chunk lacks wrap round to far behind the range's end
+      const uint32_t lacks = c.back ? static_cast<uint32_t>(CH - c.n) * c.stride * sizeof(T) : 0;
+      const Range<T> m(c.base, (static_cast<int64_t>(c.n - 1) * c.stride + c.dim) * sizeof(T));
+      const uint32_t at = off - lacks;
+      return m.load16(at > off ? kNowhere : at);
     } else {
-      const uint32_t at = static_cast<uint32_t>(min(row, c.n - 1)) * c.stride + off;
-      return reinterpret_cast<const Loose<u32x4>*>(c.base + at)->v;
+      const uint32_t r = static_cast<uint32_t>(c.back ? max(c.n - 1 - row, 0) : min(row, c.n - 1));
+      return reinterpret_cast<const Loose<u32x4>*>(c.base + (r * c.stride + off))->v;
     }
   }
   static __device__ __forceinline__ u32x4 place(u32x4 w, int row, int n, int col, int dim) {

@@ -76,6 +76,9 @@ template <typename T> struct Range {
     else return __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
   }
   __device__ __forceinline__ u32x4 load16(uint32_t off) const { return __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0); }
+  __device__ __forceinline__ void store8(uint32_t off, uint32_t __attribute__((ext_vector_type(2))) v) const {
+    __builtin_amdgcn_raw_buffer_store_b64(v, r, off, 0, 0);
+  }
   // Not kept in the caches on its way out (bit 1: nontemporal): a stream of outputs then leaves the
   // lines of the inputs alone.
   __device__ __forceinline__ void store16(uint32_t off, u32x4 v) const {

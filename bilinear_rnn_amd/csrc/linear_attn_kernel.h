@@ -1,0 +1,673 @@
+// The chunk kernel of the decayed linear attention (the mathematics are in linear_attn.hip).
+#pragma once
+
+#include "attn_tiles.h"
+#include "comba.h"
+#include "linear_attn.h"
+#include "scan_common.h"
+
+namespace comba {
+
+// Logarithms of decays below this one are taken as it: its exponential is 0 in float32, and differences
+// of sums stay finite.
+constexpr float kLeastDecay = -200.f;
+
+template <typename T> struct AttnRole {
+  const T* x;                 // [tokens, xh heads, A]
+  const T* y;                 // [tokens, yh heads, A]
+  const T* z;                 // [tokens, zh heads, Z]
+  T* out;                     // [tokens, H, Z], or null
+  float* out32;               // the same in float32 (then out is null)
+  const T* own;               // [tokens, own_h heads, Z]: its products with out's rows are wanted, or null
+  float* rdot;                // [Z blocks, H, tokens]: those products
+  int64_t rdot_inter;         // the same of f M^T x alone, so many floats behind
+  float* state;               // [slots, H, V, K]: incoming states, or (state pass) where the segment's own go
+  int xh, yh, zh, own_h, A, Z;
+  bool back;                  // time runs from the segment's end
+  bool a_is_k;                // A is the axis of K in a state, Z that of V; else the other way round
+  float f_state, f_score, f_into;   // factors of M^T x, of the scores, of what goes into M
+};
+
+template <typename T> struct AttnK {
+  AttnRole<T> role[3];
+  const float* log_decay;
+  const float* init;          // [N, H, V, K] or null: incoming state of sequences of one segment (forward)
+  float* fin;                 // [N, H, V, K] or null
+  const int32_t* cu_seqlens;
+  double* decay;              // [slots, H]: the segment's sum of log2 decays (state pass)
+  int N, Tn, H, K, V, L, roles;
+  int64_t slots, tokens;
+  bool per_token;
+  bool whole_pass;            // backward: every segment has its states in role.state; state pass: the last one too
+};
+
+// Where a unit's workgroups find its column blocks and roles.
+template <typename T> __host__ __device__ inline int attn_unit_blocks(const AttnK<T>& a, int ZB) {
+  int n = 0;
+  for (int r = 0; r < a.roles; ++r) n += (a.role[r].Z + ZB - 1) / ZB;
+  return n;
+}
+
+// Four elements a0 .. a0 + 3 of column z of M in a state [V, K].
+struct StateMap {
+  int K, A, Z;
+  bool a_is_k;
+  __device__ __forceinline__ f32x4 load(const float* s, int a0, int z) const {
+    f32x4 r = {0.f, 0.f, 0.f, 0.f};
+    if (z >= Z) return r;
+    if (a_is_k && a0 + 4 <= A) return reinterpret_cast<const Loose<f32x4>*>(s + static_cast<int64_t>(z) * K + a0)->v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (a0 + i < A) r[i] = a_is_k ? s[z * K + a0 + i] : s[(a0 + i) * K + z];
+    return r;
+  }
+  __device__ __forceinline__ void store(float* s, int a0, int z, const f32x4& x) const {
+    if (z >= Z) return;
+    if (a_is_k && a0 + 4 <= A) {
+      reinterpret_cast<Loose<f32x4>*>(s + static_cast<int64_t>(z) * K + a0)->v = x;
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (a0 + i < A) s[a_is_k ? z * K + a0 + i : (a0 + i) * K + z] = x[i];
+  }
+};
+
+// Tokens per chunk: what the LDS holds twice.
+template <typename T> __host__ __device__ constexpr int attn_chunk(int AP) {
+  return (sizeof(T) == 2 ? 64 : 32) / (AP > 128 ? 2 : 1);
+}
+
+// One chunk's tensors and decays in LDS.
+template <typename T, int AP, bool X, int ZB> struct AttnChunk {
+  typedef Tiles<T> Ti;
+  static constexpr int CH = attn_chunk<T>(AP);
+  alignas(16) T xs[X ? Ti::size(CH, AP) : 8];
+  alignas(16) T ys[Ti::size(CH, AP)];
+  alignas(16) T zs[Ti::size(CH, ZB)];
+  alignas(16) float gh[CH];   // sums of log2 decays from the chunk's first row on, in two terms
+  alignas(16) float gl[CH];
+  alignas(16) float fs[CH];   // f_u, r_w and the whole chunk's decay
+  alignas(16) float rs[CH];
+  float whole;
+};
+
+// A workgroup's place: the role, head and segment that it works for.
+struct AttnPlace {
+  int role, zb, h, chunks;
+  int64_t unit, row0;         // row0: token 0 of the batch row
+  ScanPlace pl;
+  bool back, ok;
+  template <typename T> __device__ __forceinline__ AttnPlace(const AttnK<T>& a, int CH, int ZB) {
+    // the workgroups of one (segment, head) on one XCD, whose L2 they share
+    const int per_unit = attn_unit_blocks(a, ZB);
+    unit = static_cast<int64_t>(blockIdx.x / (8 * per_unit)) * 8 + blockIdx.x % 8;
+    ok = unit < a.slots * a.H;
+    if (!ok) return;
+    zb = blockIdx.x / 8 % per_unit;
+    role = 0;
+    while (zb >= (a.role[role].Z + ZB - 1) / ZB) zb -= (a.role[role++].Z + ZB - 1) / ZB;
+    const int64_t slot = unit / a.H;
+    h = static_cast<int>(unit - slot * a.H);
+    pl = scan_place<1>(slot, 0, a.cu_seqlens, a.N, a.Tn, 1, 1, a.L);
+    ok = pl.ok;
+    chunks = (pl.t1 - pl.t0 + CH - 1) / CH;
+    row0 = static_cast<int64_t>(pl.b) * a.Tn;
+    back = a.role[role].back;
+  }
+  __device__ __forceinline__ int first_token(int it, int CH) const { return pl.t0 + (back ? chunks - 1 - it : it) * CH; }
+  __device__ __forceinline__ int rows(int it, int CH) const { return min(CH, pl.t1 - first_token(it, CH)); }
+};
+
+// Brings chunks into LDS with PT threads: fetch() puts the loads of a chunk in flight, stage() writes them.
+template <typename T, int AP, bool X, bool WHOLE, int ZB> struct AttnStage {
+  typedef Tiles<T> Ti;
+  typedef AttnChunk<T, AP, X, ZB> Chunk;
+  static constexpr int CH = Chunk::CH, E = Ti::PIECE, PT = 256;
+  static constexpr int XN = CH * AP / E, ZN = CH * ZB / E;   // pieces
+  static constexpr int XP = XN / PT, ZP = ZN / PT;
+  static_assert(XN % PT == 0 && ZN % PT == 0, "whole pieces per thread");
+  typedef Pieces<T, WHOLE, CH> Piece;
+  const AttnK<T>& a;
+  const AttnPlace& at;
+  const int A, Z, xst, yst, zst, z0, pt;  // elements from a token to the next; the block's first column; thread
+  const bool gates;                     // this wavefront takes the decays
+  const T *xb, *yb, *zb;
+  float f_state, f_into;
+  uint32_t xo[X ? XP : 1], yo[XP], zo[ZP];
+  u32x4 xr[X ? XP : 1], yr[XP], zr[ZP];
+  float gr = 0.f, g0 = 0.f;
+  double total = 0.0;                   // of the segment's log2 decays
+
+  // Piece number pt + PT i of a tile is place `slot` of an LDS row.
+  template <int L> __device__ __forceinline__ void place_of(int i, int& row, int& col) const {
+    const int p = pt + i * PT;
+    row = p / (L / E);
+    col = Ti::template piece_at<L>(row, p % (L / E)) * E;
+  }
+  template <int L> __device__ __forceinline__ u32x4* lds_of(T* tile, int i) const {
+    const int p = pt + i * PT;
+    return reinterpret_cast<u32x4*>(tile + p / (L / E) * Ti::pitch(L) + p % (L / E) * E);
+  }
+  __device__ __forceinline__ AttnStage(const AttnK<T>& a_, const AttnPlace& at_, int pt_, bool gates_)
+      : a(a_), at(at_), A(a_.role[at_.role].A), Z(a_.role[at_.role].Z), xst(a_.role[at_.role].xh * A),
+        yst(a_.role[at_.role].yh * A), zst(a_.role[at_.role].zh * Z), z0(at_.zb * ZB), pt(pt_), gates(gates_) {
+    const AttnRole<T>& R = a.role[at.role];
+    f_state = R.f_state;
+    f_into = R.f_into;
+    xb = X ? R.x + at.row0 * xst + at.h / (a.H / R.xh) * A : nullptr;
+    yb = R.y + at.row0 * yst + at.h / (a.H / R.yh) * A;
+    zb = R.z + at.row0 * zst + at.h / (a.H / R.zh) * Z;
+#pragma unroll
+    for (int i = 0; i < XP; ++i) {
+      int r, col;
+      place_of<AP>(i, r, col);
+      if (X) xo[i] = Piece::offset(r, col, xst, A, at.back);
+      yo[i] = Piece::offset(r, col, yst, A, at.back);
+    }
+#pragma unroll
+    for (int i = 0; i < ZP; ++i) {
+      int r, col;
+      place_of<ZB>(i, r, col);
+      zo[i] = Piece::offset(r, z0 + col, zst, Z, at.back);
+    }
+  }
+  __device__ __forceinline__ void fetch(int it) {
+    const int t0 = at.first_token(it, CH), n = at.rows(it, CH);
+    const typename Piece::Rows xc{X ? xb + static_cast<int64_t>(t0) * xst : nullptr, n, xst, A, at.back},
+        yc{yb + static_cast<int64_t>(t0) * yst, n, yst, A, at.back}, zc{zb + static_cast<int64_t>(t0) * zst, n, zst, Z, at.back};
+#pragma unroll
+    for (int i = 0; i < XP; ++i) {
+      int r, col;
+      place_of<AP>(i, r, col);
+      if (X) xr[i] = Piece::fetch(xc, xo[i], r);
+      yr[i] = Piece::fetch(yc, yo[i], r);
+    }
+#pragma unroll
+    for (int i = 0; i < ZP; ++i) {
+      int r, col;
+      place_of<ZB>(i, r, col);
+      zr[i] = Piece::fetch(zc, zo[i], r);
+    }
+    if (gates) {
+      // into the state before an LDS row goes the decay of the row's token, backwards that of the token behind
+      const int lane = pt & 63, r = at.back ? n - lane : lane;
+      const float* const g = a.per_token ? a.log_decay + (at.row0 + t0) * a.H + at.h : a.log_decay + at.h;
+      const int64_t step = a.per_token ? a.H : 0;
+      gr = lane < n && r < n ? g[r * step] : 0.f;
+      g0 = at.back && lane == 0 ? g[0] : 0.f;
+    }
+  }
+  __device__ __forceinline__ void stage(int it, Chunk& ck) {
+    const int n = at.rows(it, CH);
+#pragma unroll
+    for (int i = 0; i < XP; ++i) {
+      int r, col;
+      place_of<AP>(i, r, col);
+      if (X) *lds_of<AP>(ck.xs, i) = Piece::place(xr[i], r, n, col, A);
+      *lds_of<AP>(ck.ys, i) = Piece::place(yr[i], r, n, col, A);
+    }
+#pragma unroll
+    for (int i = 0; i < ZP; ++i) {
+      int r, col;
+      place_of<ZB>(i, r, col);
+      *lds_of<ZB>(ck.zs, i) = Piece::place(zr[i], r, n, z0 + col, Z);
+    }
+    if (gates) {
+      // sums of log2 decays, in 64 bits: their differences are small beside them. Backwards the first
+      // row is the last token, whose output takes the state as it is; what decays the state behind the
+      // last row is the first token's decay.
+      const int lane = pt & 63;
+      auto log2_of = [](float x) { return static_cast<double>(x < kLeastDecay ? kLeastDecay : x) * 1.4426950408889634; };
+      const double G = wave_scan_f64_dpp(log2_of(gr));
+      double all = __shfl(G, 63, kWave);
+      if (at.back) all += log2_of(__shfl(g0, 0, kWave));
+      if (lane < CH) {
+        ck.gh[lane] = static_cast<float>(G);
+        ck.gl[lane] = static_cast<float>(G - static_cast<float>(G));
+        ck.fs[lane] = f_state * __builtin_amdgcn_exp2f(static_cast<float>(G));
+        ck.rs[lane] = f_into * __builtin_amdgcn_exp2f(static_cast<float>(all - G));
+      }
+      if (lane == 0) ck.whole = __builtin_amdgcn_exp2f(static_cast<float>(all));
+      total += all;
+    }
+  }
+};
+
+// A wavefront's 16 ZT columns of M, decayed over the chunk and with what the chunk adds; zf: the z operands of those
+// columns.
+template <typename T, int AP, int ZT, typename Chunk>
+__device__ __forceinline__ void attn_update(f32x4 (&m)[ZT][AP / 16], const typename Tiles<T>::Frag* zf, const Chunk& ck,
+                                            int g, int l16) {
+  typedef Tiles<T> Ti;
+  constexpr int BLK = Ti::BLK, NS = Chunk::CH / BLK, EL = BLK / 4, NM = AP / 16, NTZ = Ti::TERMS(3);
+  // LDS reads are issued in groups, ahead of the products that wait for them: left to itself the compiler
+  // places them one by one before their use, and every one's latency shows.
+  constexpr int FRAGS = NM * NS, GROUP = 4;  // operands, number j NS + b
+  typename Ti::Frag y[2][GROUP];
+  f32x4 r[NS][EL / 4];
+  auto read = [&](int n) {
+#pragma unroll
+    for (int i = 0; i < GROUP; ++i)
+      y[n & 1][i] = Ti::template down_index<AP>(ck.ys, (n * GROUP + i) % NS, (n * GROUP + i) / NS, g, l16);
+  };
+#pragma unroll
+  for (int b = 0; b < NS; ++b)
+#pragma unroll
+    for (int e = 0; e < EL; e += 4) r[b][e / 4] = *reinterpret_cast<const f32x4*>(ck.rs + BLK * b + Ti::down_row(g, e));
+  const float keep = ck.whole;
+  read(0);
+  __builtin_amdgcn_sched_barrier(0);
+  typename Ti::Frag zt[ZT][NS][NTZ];
+#pragma unroll
+  for (int z = 0; z < ZT; ++z) {
+#pragma unroll
+    for (int b = 0; b < NS; ++b) {
+      float zw[EL];
+#pragma unroll
+      for (int e = 0; e < EL; ++e) zw[e] = Ti::value(zf[z * NS + b], e) * r[b][e / 4][e % 4];
+      Ti::template split<NTZ>(zw, zt[z][b]);
+    }
+#pragma unroll
+    for (int j = 0; j < NM; ++j) m[z][j] *= keep;
+  }
+#pragma unroll
+  for (int n = 0; n < FRAGS / GROUP; ++n) {
+    if (n + 1 < FRAGS / GROUP) {
+      read(n + 1);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int k = 0; k < NTZ; ++k)
+#pragma unroll
+      for (int i = 0; i < GROUP; ++i)
+#pragma unroll
+        for (int z = 0; z < ZT; ++z) {
+          const int f = n * GROUP + i;
+          m[z][f / NS] = Ti::mma(y[n & 1][i], zt[z][f % NS][k], m[z][f / NS]);
+        }
+  }
+}
+
+// The segment's own state, from 0: four wavefronts hold 16 columns each, four bring the next chunk.
+template <typename T, int AP, bool WHOLE>
+__global__ __launch_bounds__(512) void attn_state_kernel(AttnK<T> a) {
+  typedef Tiles<T> Ti;
+  constexpr int ZB = 64;
+  typedef AttnChunk<T, AP, false, ZB> Chunk;
+  constexpr int CH = Chunk::CH, NM = AP / 16, NS = CH / Ti::BLK;
+  __shared__ Chunk chunk[2];
+  const AttnPlace at(a, CH, ZB);
+  if (!at.ok || (last_segment(at.pl) && !a.whole_pass)) return;
+  const int tid = threadIdx.x, w = tid >> 6, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
+  const int chunks = at.chunks;
+  if (w >= 4) {
+    AttnStage<T, AP, false, WHOLE, ZB> in(a, at, tid - 256, w == 7);
+    for (int it = -2; it < chunks; ++it) {
+      if (it >= -1 && it + 1 < chunks) in.stage(it + 1, chunk[(it + 1) & 1]);
+      if (it + 2 < chunks) in.fetch(it + 2);
+      if (it > -2) __syncthreads();
+    }
+    if (blockIdx.x / 8 % attn_unit_blocks(a, ZB) == 0 && tid == 448) a.decay[at.unit] = in.total;
+    return;
+  }
+  f32x4 m[1][NM];
+#pragma unroll
+  for (int j = 0; j < NM; ++j) m[0][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  __syncthreads();
+  for (int it = 0; it < chunks; ++it) {
+    const Chunk& ck = chunk[it & 1];
+    typename Ti::Frag zf[NS];
+#pragma unroll
+    for (int b = 0; b < NS; ++b) zf[b] = Ti::template down<ZB>(ck.zs, b, 16 * w, g, l16);
+    attn_update<T, AP, 1>(m, zf, ck, g, l16);
+    __syncthreads();
+  }
+  const AttnRole<T>& R = a.role[at.role];
+  const StateMap sm{a.K, R.A, R.Z, R.a_is_k};
+  float* const to = R.state + at.unit * a.K * a.V;
+#pragma unroll
+  for (int j = 0; j < NM; ++j) sm.store(to, Ti::index(j, g, 0), at.zb * ZB + 16 * w + l16, m[0][j]);
+}
+
+// LDS of the chunk kernel: two or three chunks and the scores of one or two, whatever there is room for.
+template <typename T, int AP, int NT, int ZT> struct AttnShared {
+  typedef Tiles<T> Ti;
+  typedef AttnChunk<T, AP, true, 64 * ZT> Chunk;
+  static constexpr int CH = Chunk::CH, SCORES = Ti::score_elems(CH, Ti::TERMS(NT));
+  static constexpr size_t OTHERS = (NT > 2 ? 64 * CH : 64) + 64;
+  static constexpr size_t bytes(int chunks, int scores) {
+    return chunks * sizeof(Chunk) + scores * SCORES * sizeof(T) + OTHERS;
+  }
+  static constexpr size_t ROOM = 160 * 1024;
+  static constexpr int CHUNKS = bytes(3, 1) <= ROOM ? 3 : 2, PS = bytes(CHUNKS, 2) <= ROOM ? 2 : 1;
+  Chunk chunk[CHUNKS];
+  alignas(16) T ps[PS][SCORES];
+  float dots[2][2][4][NT > 2 ? CH : 1];  // of two iterations: all, the states' part
+  // wavefronts that have brought a chunk, and that are done with its scores, over all chunks
+  int produced, taken;
+};
+
+// AP: A padded to 64, 128 or 256. NT: terms that float32 operands of a bf16 product are split into; with three
+// the products with `own` as well.
+// WHOLE: A and Z are multiples of a 16-byte piece, the tensors on 16-byte boundaries.
+// Four wavefronts (consumers) hold 16 ZT columns of M each and run the chunks; four more (producers) bring the
+// next chunks into LDS and form their scores, which do not depend on M, with the loads of one chunk more in
+// flight. With room for three chunks a chunk's scores are formed an iteration after it was brought; with two,
+// in the same, behind a barrier of the producers alone. One barrier for all per chunk.
+template <typename T, int AP, int NT, bool WHOLE, int ZT>
+__global__ __launch_bounds__(512) void attn_kernel(AttnK<T> a) {
+  typedef Tiles<T> Ti;
+  typedef typename Ti::Frag Frag;
+  typedef AttnShared<T, AP, NT, ZT> Shared;
+  typedef typename Shared::Chunk Chunk;
+  constexpr int CH = Shared::CH, BLK = Ti::BLK, ZB = 64 * ZT, CHUNKS = Shared::CHUNKS, PS = Shared::PS;
+  constexpr int NM = AP / 16, NA = AP / BLK, NS = CH / BLK, NU = CH / 16, NTM = Ti::TERMS(NT);
+  __shared__ Shared sh;
+  static_assert(sizeof(Shared) <= Shared::ROOM, "LDS");
+
+  const AttnPlace at(a, CH, ZB);
+  if (!at.ok) return;
+  const AttnRole<T> R = a.role[at.role];
+  const int tid = threadIdx.x, w = tid >> 6, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
+  const int chunks = at.chunks, h = at.h, z0 = at.zb * ZB;
+  const bool back = at.back;
+  const int64_t KV = static_cast<int64_t>(a.K) * a.V;
+  if (tid == 0) sh.produced = sh.taken = 0;
+  __syncthreads();
+  auto arrive = [&](int* flag) {  // once per wavefront, after what it read or wrote before
+    if (lane == 0) __hip_atomic_fetch_add(flag, 1, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_WORKGROUP);
+  };
+  auto wait_for = [&](const int* flag, int count) {
+    while (__hip_atomic_load(flag, __ATOMIC_ACQUIRE, __HIP_MEMORY_SCOPE_WORKGROUP) < count) __builtin_amdgcn_s_sleep(1);
+  };
+
+  if (w >= 4) {
+    const int pt = tid - 256, pw = w - 4;
+    AttnStage<T, AP, true, WHOLE, ZB> in(a, at, pt, pw == 3);
+    for (int i = pt; i < PS * Shared::SCORES; i += 256) sh.ps[0][i] = 0;  // tiles beyond the diagonal stay 0
+    // tiles (target i, source j) on and below the diagonal
+    auto scores = [&](int it) {
+      const Chunk& ck = sh.chunk[it % CHUNKS];
+      constexpr int tiles = NU * (NU + 1) / 2, TPW = (tiles + 3) / 4;
+      int ti[TPW], tj[TPW];
+      f32x4 s[TPW], d[TPW];
+#pragma unroll
+      for (int q = 0; q < TPW; ++q) {
+        const int k = min(pw + 4 * q, tiles - 1);
+        int i = 0;
+#pragma unroll
+        for (int n = 1; n < NU; ++n) i += k >= n * (n + 1) / 2;
+        ti[q] = i;
+        tj[q] = k - i * (i + 1) / 2;
+        s[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+      }
+#pragma unroll
+      for (int q = 0; q < TPW; ++q) {
+        const int t = 16 * ti[q] + l16;
+        const float h0 = ck.gh[t], l0 = ck.gl[t];
+        const f32x4 h1 = *reinterpret_cast<const f32x4*>(ck.gh + 16 * tj[q] + 4 * g),
+                    l1 = *reinterpret_cast<const f32x4*>(ck.gl + 16 * tj[q] + 4 * g);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) d[q][r] = R.f_score * __builtin_amdgcn_exp2f((h0 - h1[r]) + (l0 - l1[r]));
+      }
+#pragma unroll
+      for (int p = 0; p < NA; ++p)
+#pragma unroll
+        for (int q = 0; q < TPW; ++q)
+          s[q] = Ti::mma(Ti::template along<AP>(ck.ys, 16 * tj[q] + l16, p, g),
+                         Ti::template along<AP>(ck.xs, 16 * ti[q] + l16, p, g), s[q]);
+      if (PS == 1) wait_for(&sh.taken, 4 * it);  // the consumers are done with the scores before these
+#pragma unroll
+      for (int q = 0; q < TPW; ++q) {
+        if (pw + 4 * q >= tiles) continue;
+        const int t = 16 * ti[q] + l16;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {  // a masked score is 0 whatever the product is
+          float x = s[q][r] * d[q][r];
+          pin(x);
+          s[q][r] = 16 * tj[q] + 4 * g + r <= t ? x : 0.f;
+        }
+        Ti::template put_scores<CH, NTM>(sh.ps[it % PS], t, tj[q], g, s[q]);
+      }
+    };
+    auto put_dots = [&](int it) {
+      if constexpr (NT > 2) {
+        const int n = at.rows(it, CH);
+        if (R.own && pt < n) {
+          const auto& d = sh.dots[it & 1];
+          float* const to = R.rdot + (static_cast<int64_t>(at.zb) * a.H + h) * a.tokens + at.row0 + at.first_token(it, CH) +
+                            (back ? n - 1 - pt : pt);
+          to[0] = (d[0][0][pt] + d[0][1][pt]) + (d[0][2][pt] + d[0][3][pt]);
+          to[R.rdot_inter] = (d[1][0][pt] + d[1][1][pt]) + (d[1][2][pt] + d[1][3][pt]);
+        }
+      }
+    };
+    // iteration `it` of the consumers, and those before their first
+    constexpr int AHEAD = CHUNKS - 1;
+    for (int it = -AHEAD - 1; it < chunks; ++it) {
+      if (it + AHEAD >= 0 && it + AHEAD < chunks) {
+        in.stage(it + AHEAD, sh.chunk[(it + AHEAD) % CHUNKS]);
+        if (CHUNKS == 2) arrive(&sh.produced);
+      }
+      if (it + AHEAD + 1 < chunks) in.fetch(it + AHEAD + 1);
+      if (it < -1) {
+        if (CHUNKS == 3 && it == -2) __syncthreads();  // the first chunk is there, the scores are cleared
+        continue;
+      }
+      if (it + 1 < chunks) {
+        if (CHUNKS == 2) wait_for(&sh.produced, 4 * (it + 2));
+        scores(it + 1);
+      }
+      if (it > 0) put_dots(it - 1);
+      __syncthreads();
+    }
+    if (chunks > 0) put_dots(chunks - 1);
+    return;
+  }
+
+  // consumers
+  const StateMap sm{a.K, R.A, R.Z, R.a_is_k};
+  const int c0 = 16 * ZT * w;        // the wavefront's first column in the block
+  f32x4 m[ZT][NM];
+  const float* from = nullptr;
+  if (R.state && (a.whole_pass || segments_of(at.pl.s1 - at.pl.s0, a.L) > 1)) from = R.state + at.unit * KV;
+  else if (a.init) from = a.init + (static_cast<int64_t>(at.pl.n) * a.H + h) * KV;
+#pragma unroll
+  for (int z = 0; z < ZT; ++z)
+#pragma unroll
+    for (int j = 0; j < NM; ++j) {
+      m[z][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (from) m[z][j] = sm.load(from, Ti::index(j, g, 0), z0 + c0 + 16 * z + l16);
+    }
+  // waits for them here: a wait in the loop would be one for the stores of every chunk
+#pragma unroll
+  for (int z = 0; z < ZT; ++z)
+#pragma unroll
+    for (int j = 0; j < NM; ++j) asm volatile("" : "+v"(m[z][j]));
+  const int zo = z0 + c0 + 4 * g;    // this lane's first output column (of the first tile)
+  const int out_stride = a.H * R.Z, own_stride = R.own_h * R.Z;
+  const int64_t out0 = at.row0 * out_stride + static_cast<int64_t>(h) * R.Z;
+  const T* const own = R.own ? R.own + at.row0 * own_stride + h / (a.H / R.own_h) * static_cast<int64_t>(R.Z) + zo : nullptr;
+  if (CHUNKS == 3) __syncthreads();
+  __syncthreads();
+  for (int it = 0; it < chunks; ++it) {
+    const Chunk& ck = sh.chunk[it % CHUNKS];
+    const int t0 = at.first_token(it, CH), n = at.rows(it, CH);
+    auto row_of = [&](int i) { return back ? n - 1 - 16 * i - l16 : 16 * i + l16; };       // the token's place in the chunk
+    auto left = [&](int i, int z) { return 16 * i + l16 < n ? R.Z - zo - 16 * z : 0; };    // columns there
+    Frag zf[ZT][NS];
+#pragma unroll
+    for (int z = 0; z < ZT; ++z)
+#pragma unroll
+      for (int b = 0; b < NS; ++b) zf[z][b] = Ti::template down<ZB>(ck.zs, b, c0 + 16 * z, g, l16);
+    typedef Pack<T, 4, WHOLE> Four;
+    typename Four::Words own_x[ZT][NT == 2 ? 1 : NU];
+    if (NT > 2 && own) {  // for the dot products at the end
+#pragma unroll
+      for (int z = 0; z < ZT; ++z)
+#pragma unroll
+        for (int i = 0; i < NU; ++i) {
+          own_x[z][i] = typename Four::Words(0);
+          if (left(i, z) > 0)
+            own_x[z][i] = Four::fetch(own + (static_cast<int64_t>(t0) + row_of(i)) * own_stride + 16 * z, min(left(i, z), 4));
+        }
+    }
+    f32x4 state_part[ZT][NU], o[ZT][NU];
+#pragma unroll
+    for (int z = 0; z < ZT; ++z)
+#pragma unroll
+      for (int i = 0; i < NU; ++i) state_part[z][i] = o[z][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // scores times z
+#pragma unroll
+    for (int i = 0; i < NU; ++i)
+#pragma unroll
+      for (int b = 0; b < NS; ++b)
+        if (BLK * b <= 16 * i)
+#pragma unroll
+          for (int k = 0; k < NTM; ++k) {
+            const Frag s = Ti::template scores<CH>(sh.ps[it % PS], k, 16 * i + l16, b, g);
+#pragma unroll
+            for (int z = 0; z < ZT; ++z) o[z][i] = Ti::mma(zf[z][b], s, o[z][i]);
+          }
+    if (PS == 1) arrive(&sh.taken);
+    // M^T x
+#pragma unroll
+    for (int p = 0; p < NA; ++p) {
+      Frag x[NU];
+#pragma unroll
+      for (int i = 0; i < NU; ++i) x[i] = Ti::template along<AP>(ck.xs, 16 * i + l16, p, g);
+#pragma unroll
+      for (int z = 0; z < ZT; ++z) {
+        Frag mf[NTM];
+        Ti::template from_tiles<NTM>(m[z], p, mf);
+#pragma unroll
+        for (int k = 0; k < NTM; ++k)
+#pragma unroll
+          for (int i = 0; i < NU; ++i) state_part[z][i] = Ti::mma(mf[k], x[i], state_part[z][i]);
+      }
+    }
+    float f[NU];
+#pragma unroll
+    for (int i = 0; i < NU; ++i) f[i] = ck.fs[16 * i + l16];
+    attn_update<T, AP, ZT>(m, &zf[0][0], ck, g, l16);
+#pragma unroll
+    for (int i = 0; i < NU; ++i)
+#pragma unroll
+      for (int z = 0; z < ZT; ++z) {
+        state_part[z][i] *= f[i];
+        o[z][i] += state_part[z][i];
+      }
+    // columns zo + 16 z .. + 3 of every token's output
+    const int64_t at0 = out0 + static_cast<int64_t>(t0) * out_stride;
+    if constexpr (WHOLE) {
+      const int64_t elems = static_cast<int64_t>(n - 1) * out_stride + R.Z;
+      auto offset = [&](int i, int z) { return static_cast<uint32_t>(row_of(i)) * out_stride + zo + 16 * z; };
+      if (R.out) {
+        const Range<T> to(R.out + at0, elems * sizeof(T));
+#pragma unroll
+        for (int i = 0; i < NU; ++i)
+#pragma unroll
+          for (int z = 0; z < ZT; ++z) {
+            const uint32_t off = left(i, z) > 0 ? offset(i, z) * sizeof(T) : kNowhere;
+            if constexpr (sizeof(T) == 2) to.store8(off, Four::words({o[z][i][0], o[z][i][1], o[z][i][2], o[z][i][3]}));
+            else to.store16(off, __builtin_bit_cast(u32x4, o[z][i]));
+          }
+      } else {
+        const Range<float> to(R.out32 + at0, elems * sizeof(float));
+#pragma unroll
+        for (int i = 0; i < NU; ++i)
+#pragma unroll
+          for (int z = 0; z < ZT; ++z)
+            to.store16(left(i, z) > 0 ? offset(i, z) * sizeof(float) : kNowhere, __builtin_bit_cast(u32x4, o[z][i]));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NU; ++i)
+#pragma unroll
+        for (int z = 0; z < ZT; ++z) {
+          if (left(i, z) <= 0) continue;
+          const float v[4] = {o[z][i][0], o[z][i][1], o[z][i][2], o[z][i][3]};
+          const int64_t to = at0 + static_cast<int64_t>(row_of(i)) * out_stride + zo + 16 * z;
+          if (R.out) Four::store(R.out + to, v, min(left(i, z), 4));
+          else Pack<float, 4, WHOLE>::store(R.out32 + to, v, min(left(i, z), 4));
+        }
+    }
+    if (NT > 2 && own) {
+#pragma unroll
+      for (int i = 0; i < NU; ++i) {
+        float d = 0.f, ds = 0.f;
+#pragma unroll
+        for (int z = 0; z < ZT; ++z) {
+          float x[4];
+          Four::unpack(own_x[z][i], x);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            d = fmaf(x[r], o[z][i][r], d);
+            ds = fmaf(x[r], state_part[z][i][r], ds);
+          }
+        }
+        d += __shfl_xor(d, 16, kWave);
+        d += __shfl_xor(d, 32, kWave);
+        ds += __shfl_xor(ds, 16, kWave);
+        ds += __shfl_xor(ds, 32, kWave);
+        if (g == 0) {
+          sh.dots[it & 1][0][w][16 * i + l16] = d;
+          sh.dots[it & 1][1][w][16 * i + l16] = ds;
+        }
+      }
+    }
+    __syncthreads();
+  }
+  if (a.fin && last_segment(at.pl)) {
+    float* const to = a.fin + (static_cast<int64_t>(at.pl.n) * a.H + h) * KV;
+#pragma unroll
+    for (int z = 0; z < ZT; ++z)
+#pragma unroll
+      for (int j = 0; j < NM; ++j) sm.store(to, Ti::index(j, g, 0), z0 + c0 + 16 * z + l16, m[z][j]);
+  }
+}
+
+// Calls f with A padded to 64, 128 or 256 as an integral constant.
+template <typename F> hipError_t with_width(int A, F f) {
+  if (A <= 64) f(std::integral_constant<int, 64>{});
+  else if (A <= 128) f(std::integral_constant<int, 128>{});
+  else f(std::integral_constant<int, 256>{});
+  return hipGetLastError();
+}
+
+// Output columns per workgroup: 128, whose scores then serve twice the columns, where that leaves enough
+// workgroups and (A up to 128) the state its registers.
+template <typename T> int attn_columns(const AttnK<T>& k, int A) {
+  bool narrow = A > 128;
+  for (int r = 0; r < k.roles; ++r) narrow = narrow || k.role[r].Z <= 64;
+  return narrow || k.slots * k.H * attn_unit_blocks(k, 128) < 256 ? 64 : 128;
+}
+
+// The chunk kernel for the roles in k, of which all have A columns in x and y; STATE: the state kernel.
+template <typename T, int NT, bool STATE> hipError_t run_attn(const AttnK<T>& k, int A, hipStream_t st) {
+  constexpr int E = Tiles<T>::PIECE;
+  bool whole = k.K % E == 0 && k.V % E == 0;
+  auto aligned = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
+  for (int r = 0; r < k.roles; ++r)
+    whole = whole && aligned(k.role[r].x) && aligned(k.role[r].y) && aligned(k.role[r].z) && aligned(k.role[r].out);
+  const int columns = STATE ? 64 : attn_columns(k, A);
+  const unsigned grid = static_cast<unsigned>((k.slots * k.H + 7) / 8 * 8 * attn_unit_blocks(k, columns));
+  return with_width(A, [&](auto ap) {
+    constexpr int AP = decltype(ap)::value;
+    if constexpr (STATE) {
+      if (whole) attn_state_kernel<T, AP, true><<<grid, 512, 0, st>>>(k);
+      else attn_state_kernel<T, AP, false><<<grid, 512, 0, st>>>(k);
+    } else {
+      if (columns == 64) {
+        if (whole) attn_kernel<T, AP, NT, true, 1><<<grid, 512, 0, st>>>(k);
+        else attn_kernel<T, AP, NT, false, 1><<<grid, 512, 0, st>>>(k);
+      } else if constexpr (AP <= 128) {
+        if (whole) attn_kernel<T, AP, NT, true, 2><<<grid, 512, 0, st>>>(k);
+        else attn_kernel<T, AP, NT, false, 2><<<grid, 512, 0, st>>>(k);
+      }
+    }
+  });
+}
+
+}  // namespace comba
