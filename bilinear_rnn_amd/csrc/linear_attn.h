@@ -61,6 +61,7 @@ constexpr int kAttnMaxWidth = 256;
 constexpr int kAttnMinWidth = 8;  // a 16-byte piece of bf16
 constexpr int kAttnBlock = 64;  // output columns per workgroup
 __host__ __device__ inline int attn_blocks(int width) { return (width + kAttnBlock - 1) / kAttnBlock; }
+constexpr int kAttnMaxSegment = 2048;  // of the backward
 // Elements of a state that a workgroup of the scan over segments takes.
 constexpr int kAttnScanElems = 1024;
 __host__ __device__ inline int attn_inner_blocks(int K, int V) { return (K * V + kAttnScanElems - 1) / kAttnScanElems; }

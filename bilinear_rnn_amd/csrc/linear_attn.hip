@@ -23,14 +23,16 @@ namespace comba {
 
 // Carries the states across the segments of every sequence: state[slot] becomes the segment's incoming
 // state. With `grad` (backward) also the gradients, from the last segment to the first: grad[slot] becomes
-// the gradient at the segment's end, and inner[slot, h, block] its product with the state there.
+// the gradient at the segment's end, and inner[slot, h, block] its product with the state there. A thread has four
+// elements; what it adds in the next eight segments is read together, since nothing else overlaps the
+// latency of the loads (one prompt of 65536 tokens in 16 segments: 28 -> 9 us).
 template <bool BWD>
 __global__ __launch_bounds__(256) void attn_carry_kernel(const float* __restrict__ init, const float* __restrict__ dfin,
                                                          const int32_t* __restrict__ cu, int N, int T, int H, int KV, int L,
                                                          float* __restrict__ state, float* __restrict__ grad,
                                                          const double* __restrict__ decay, double* __restrict__ inner,
                                                          float* __restrict__ dinit) {
-  constexpr int EPT = kAttnScanElems / 256;
+  constexpr int EPT = kAttnScanElems / 256, BATCH = 8;
   __shared__ float red[4];
   const int blocks = (KV + kAttnScanElems - 1) / kAttnScanElems;
   const int eb = blockIdx.x % blocks;
@@ -42,60 +44,77 @@ __global__ __launch_bounds__(256) void attn_carry_kernel(const float* __restrict
   if (!BWD && nseg <= 1) return;
   const int64_t first = cu ? static_cast<int64_t>(t0 / L) + n : static_cast<int64_t>(n) * ((T + L - 1) / L);
   const int e0 = eb * kAttnScanElems + threadIdx.x;
-  float S[EPT];
+  auto get = [&](const float* p, float (&x)[EPT]) {
 #pragma unroll
-  for (int i = 0; i < EPT; ++i) S[i] = init && e0 + 256 * i < KV ? init[nh * KV + e0 + 256 * i] : 0.f;
-  if (len == 0) {  // backward only: the gradient passes through
+    for (int i = 0; i < EPT; ++i) x[i] = p && e0 + 256 * i < KV ? p[e0 + 256 * i] : 0.f;
+  };
+  auto put = [&](float* p, const float (&x)[EPT]) {
 #pragma unroll
     for (int i = 0; i < EPT; ++i)
-      if (dinit && e0 + 256 * i < KV) dinit[nh * KV + e0 + 256 * i] = dfin ? dfin[nh * KV + e0 + 256 * i] : 0.f;
+      if (e0 + 256 * i < KV) p[e0 + 256 * i] = x[i];
+  };
+  auto unit = [&](int c) { return (first + c) * H + h; };
+  float S[EPT];
+  get(init ? init + nh * KV : nullptr, S);
+  if (len == 0) {  // backward only: the gradient passes through
+    if (dinit) {
+      get(dfin ? dfin + nh * KV : nullptr, S);
+      put(dinit + nh * KV, S);
+    }
     return;
   }
-  for (int c = 0; c < nseg; ++c) {
-    const int64_t unit = (first + c) * H + h;
-    const float p = BWD || c + 1 < nseg ? static_cast<float>(decay[unit]) : 0.f;
+  for (int c0 = 0; c0 < nseg; c0 += BATCH) {
+    float add[BATCH][EPT], p[BATCH];
 #pragma unroll
-    for (int i = 0; i < EPT; ++i) {
-      const int e = e0 + 256 * i;
-      if (e >= KV) continue;
-      float* const at = state + unit * KV + e;
-      const float add = BWD || c + 1 < nseg ? *at : 0.f;
-      *at = S[i];
-      S[i] = carried(S[i], p, add);
+    for (int k = 0; k < BATCH; ++k) {
+      const bool in = c0 + k < nseg - (BWD ? 0 : 1);  // the forward has nothing of the last one
+      p[k] = in ? static_cast<float>(decay[unit(c0 + k)]) : 0.f;
+      get(in ? state + unit(c0 + k) * KV : nullptr, add[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      if (c0 + k >= nseg) break;
+      put(state + unit(c0 + k) * KV, S);
+#pragma unroll
+      for (int i = 0; i < EPT; ++i) S[i] = carried(S[i], p[k], add[k][i]);
     }
   }
   if constexpr (BWD) {
     float G[EPT];
+    get(dfin ? dfin + nh * KV : nullptr, G);
+    for (int c0 = nseg - 1; c0 >= 0; c0 -= BATCH) {
+      float add[BATCH][EPT], before[BATCH][EPT], p[BATCH];
 #pragma unroll
-    for (int i = 0; i < EPT; ++i) G[i] = dfin && e0 + 256 * i < KV ? dfin[nh * KV + e0 + 256 * i] : 0.f;
-    for (int c = nseg - 1; c >= 0; --c) {
-      const int64_t unit = (first + c) * H + h;
-      const float p = static_cast<float>(decay[unit]);
-      float d = 0.f;
-#pragma unroll
-      for (int i = 0; i < EPT; ++i) {
-        const int e = e0 + 256 * i;
-        if (e >= KV) continue;
-        float* const at = grad + unit * KV + e;
-        const float add = *at;
-        *at = G[i];
-        d = fmaf(G[i], S[i], d);
-        G[i] = carried(G[i], p, add);
-        S[i] = state[unit * KV + e];
+      for (int k = 0; k < BATCH; ++k) {
+        const bool in = c0 - k >= 0;
+        p[k] = in ? static_cast<float>(decay[unit(c0 - k)]) : 0.f;
+        get(in ? grad + unit(c0 - k) * KV : nullptr, add[k]);
+        get(in ? state + unit(c0 - k) * KV : nullptr, before[k]);
       }
-      d = wave_sum(d);
-      if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = d;
-      __syncthreads();
-      if (threadIdx.x == 0) inner[unit * blocks + eb] = (static_cast<double>(red[0]) + red[1]) + (static_cast<double>(red[2]) + red[3]);
-      __syncthreads();
-    }
 #pragma unroll
-    for (int i = 0; i < EPT; ++i)
-      if (dinit && e0 + 256 * i < KV) dinit[nh * KV + e0 + 256 * i] = G[i];
+      for (int k = 0; k < BATCH; ++k) {
+        if (c0 - k < 0) break;
+        put(grad + unit(c0 - k) * KV, G);
+        float d = 0.f;
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) {
+          d = fmaf(G[i], S[i], d);
+          G[i] = carried(G[i], p[k], add[k][i]);
+          S[i] = before[k][i];
+        }
+        d = wave_sum(d);
+        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = d;
+        __syncthreads();
+        if (threadIdx.x == 0)
+          inner[unit(c0 - k) * blocks + eb] = (static_cast<double>(red[0]) + red[1]) + (static_cast<double>(red[2]) + red[3]);
+        __syncthreads();
+      }
+    }
+    if (dinit) put(dinit + nh * KV, G);
   }
 }
 
-// dlog_decay of a segment and head per wavefront: sums from the segment's end, in 64 bits. Over a whole
+// dlog_decay of a segment and head per workgroup: sums from the segment's end, in 64 bits. Over a whole
 // chunk the scores' parts of q . dq and k . dk have the same sum, so only the parts that come from
 // the states are carried from chunk to chunk: what is rounded in the others stays within the chunk.
 // rdot: [q and k][all and states' part][Z blocks, H, tokens], the four `one` floats apart.
@@ -104,37 +123,60 @@ __global__ __launch_bounds__(256) void attn_decay_grad_kernel(const float* __res
                                                               int CH, int64_t slots, int64_t tokens, int64_t one,
                                                               int zblocks, int eblocks, float* __restrict__ out,
                                                               double* __restrict__ hsum) {
-  const int lane = threadIdx.x & 63;
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  if (unit >= slots * H) return;
-  const int64_t slot = unit / H;
+  __shared__ double part[kAttnMaxSegment / 16], end, sums[4];  // the states' part of every chunk; <gradient, state> at the end
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int64_t unit = blockIdx.x, slot = unit / H;
   const int h = static_cast<int>(unit - slot * H);
   const ScanPlace pl = scan_place<1>(slot, 0, cu, N, T, 1, 1, L);
   const bool some = pl.ok && pl.t1 > pl.t0;
-  if (hsum && !some && lane == 0) hsum[unit] = 0.0;
+  if (hsum && !some && threadIdx.x == 0) hsum[unit] = 0.0;
   if (!some) return;
-  double carry = 0.0, sum = 0.0;
-  for (int i = 0; i < eblocks; ++i) carry += inner[unit * eblocks + i];
+  const int chunks = (pl.t1 - pl.t0 + CH - 1) / CH;
   const int64_t row0 = static_cast<int64_t>(pl.b) * T;
-  for (int c = (pl.t1 - pl.t0 - 1) / CH; c >= 0; --c) {  // lane l: the chunk's token CH - 1 - l
-    const int t = pl.t0 + c * CH + CH - 1 - lane;
-    double r = 0.0, ri = 0.0;
-    if (lane < CH && t < pl.t1)
+  // lane l: the chunk's token CH - 1 - l
+  auto token = [&](int c) { return pl.t0 + c * CH + CH - 1 - lane; };
+  auto get = [&](int c, int64_t which) {  // q's minus k's
+    double r = 0.0;
+    if (lane < CH && token(c) < pl.t1)
       for (int zb = 0; zb < zblocks; ++zb) {
-        const float* const at = rdot + (static_cast<int64_t>(zb) * H + h) * tokens + row0 + t;
+        const float* const at = rdot + which + (static_cast<int64_t>(zb) * H + h) * tokens + row0 + token(c);
         r += static_cast<double>(at[0]) - static_cast<double>(at[2 * one]);
-        ri += static_cast<double>(at[one]) - static_cast<double>(at[3 * one]);
       }
-    const double s = wave_scan_f64_dpp(r) + carry;
-    carry += __shfl(wave_scan_f64_dpp(ri), 63, kWave);
-    if (lane < CH && t < pl.t1) {
+    return r;
+  };
+  for (int c = w; c < chunks; c += 4) {
+    const double s = wave_scan_f64_dpp(get(c, one));
+    if (lane == 63) part[c] = s;
+  }
+  if (w == 0) {
+    double s = 0.0;
+    for (int i = lane; i < eblocks; i += 64) s += inner[unit * eblocks + i];
+    s = wave_scan_f64_dpp(s);
+    if (lane == 63) end = s;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {  // what every chunk takes over from those behind it
+    double carry = end;
+    for (int c = chunks - 1; c >= 0; --c) {
+      const double s = part[c];
+      part[c] = carry;
+      carry += s;
+    }
+  }
+  __syncthreads();
+  double sum = 0.0;
+  for (int c = w; c < chunks; c += 4) {
+    const double s = wave_scan_f64_dpp(get(c, 0)) + part[c];
+    if (lane < CH && token(c) < pl.t1) {
       sum += s;
-      if (!hsum) out[(row0 + t) * H + h] = static_cast<float>(s);
+      if (!hsum) out[(row0 + token(c)) * H + h] = static_cast<float>(s);
     }
   }
   if (hsum) {
     sum = wave_scan_f64_dpp(sum);
-    if (lane == 63) hsum[unit] = sum;
+    if (lane == 63) sums[w] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) hsum[unit] = (sums[0] + sums[1]) + (sums[2] + sums[3]);
   }
 }
 
@@ -252,18 +294,27 @@ __global__ __launch_bounds__(256) void attn_step_kernel(const T* __restrict__ q,
 
 // --- launches ------------------------------------------------------------------------------------
 
+// The forward is cut along time only where there are not enough workgroups for 256 compute units (of 64 columns; cut
+// ones take 128, see attn_columns): every segment but the last costs a pass over its k and v before, and
+// the carry. At B = 1, T = 65536, 16 heads of 128: 4096 tokens per segment 420 us, 2048 440, 8192 490;
+// at B = 8, T = 4096, 16 heads of 128, uncut 192 us, in two segments 210.
+// Packed batches are cut where a sequence is longer than 1.5 times a compute unit's share of all: the lengths are not known
+// here, and a segment of L tokens takes its time in the state pass even if it is the only one (64 sequences, 40001
+// tokens, 32 heads of 64: uncut 245 us, 2048 281, 256 443).
 AttnPlan attn_plan(int64_t B, int64_t T, int64_t H, int64_t V, int64_t N, bool packed) {
-  const int64_t units = H * attn_blocks(static_cast<int>(V));
-  if (!packed && B * units >= 256) return AttnPlan{0, N};
-  int64_t L = packed ? T * units / 512 : (T * B * units + 255) / 256;
-  L = L < 256 ? 256 : L > 4096 ? 4096 : (L + 63) / 64 * 64;
+  if (!packed && B * H * attn_blocks(static_cast<int>(V)) >= 256) return AttnPlan{0, N};
+  const int64_t units = H * ((V + 127) / 128);
+  int64_t L = packed ? T * units * 3 / 512 : (T * B * units + 255) / 256;
+  L = L < 256 ? 256 : L > 8192 ? 8192 : (L + 63) / 64 * 64;
   if (L >= T) return AttnPlan{0, N};
   return AttnPlan{static_cast<int>(L), packed ? T / L + N + 1 : B * ((T + L - 1) / L)};
 }
 
+// The backward's states at the ends of segments are what the sums of dlog_decay start from, so it always has some.
+// At B = 4, T = 2048, 16 heads of 128: 1024 tokens 239 us, 512 255, 256 306.
 AttnPlan attn_bwd_plan(int64_t B, int64_t T, int64_t H, int64_t N, bool packed) {
-  int64_t L = B * T * H / 256;
-  L = L < 256 ? 256 : L > 2048 ? 2048 : (L + 63) / 64 * 64;
+  int64_t L = B * T * H / 128;
+  L = L < 256 ? 256 : L > kAttnMaxSegment ? kAttnMaxSegment : (L + 63) / 64 * 64;
   return AttnPlan{static_cast<int>(L), packed ? T / L + N + 1 : B * ((T + L - 1) / L)};
 }
 
@@ -335,18 +386,15 @@ template <typename T> hipError_t attn_bwd_t(const AttnBwdArgs& a, const AttnPlan
   const AttnRole<T> rk_{v, dO, q, dk, dk32, kk, rk, one, a.grad, H, H, Hk, Hk, V, K, true, false, 1.f, f.scale, f.scale};
   const AttnRole<T> rv_{kk, q, dO, static_cast<T*>(a.dv), nullptr, nullptr, nullptr, 0, a.grad, Hk, Hk, H, 1, K, V, true, true,
                         1.f, f.scale, f.scale};
+  // dv needs no third term: it has a launch of its own
   k.role[0] = rq_;
   k.role[1] = rk_;
-  k.role[2] = rv_;
-  k.roles = padded(K) == padded(V) ? 3 : 2;
-  const int zblocks = (K + attn_columns(k, V) - 1) / attn_columns(k, V);
+  const int columns = attn_columns(k, V), zblocks = (K + columns - 1) / columns;
   if ((e = run_attn<T, 3, false>(k, V, st)) != hipSuccess) return e;
-  if (k.roles == 2) {
-    k.role[0] = rv_;
-    k.roles = 1;
-    if ((e = run_attn<T, 2, false>(k, K, st)) != hipSuccess) return e;
-  }
-  attn_decay_grad_kernel<<<static_cast<unsigned>((p.slots * H + 3) / 4), 256, 0, st>>>(
+  k.role[0] = rv_;
+  k.roles = 1;
+  if ((e = run_attn<T, 2, false>(k, K, st)) != hipSuccess) return e;
+  attn_decay_grad_kernel<<<static_cast<unsigned>(p.slots * H), 256, 0, st>>>(
       a.rdot, a.inner, f.cu_seqlens, f.N, f.T, H, p.L, attn_chunk<T>(padded(V)), p.slots, k.tokens, one, zblocks, eblocks, a.dlog_decay,
       f.per_token ? nullptr : a.hsum);
   if ((e = hipGetLastError()) != hipSuccess) return e;

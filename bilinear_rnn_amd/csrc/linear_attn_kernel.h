@@ -29,7 +29,7 @@ template <typename T> struct AttnRole {
 };
 
 template <typename T> struct AttnK {
-  AttnRole<T> role[3];
+  AttnRole<T> role[2];
   const float* log_decay;
   const float* init;          // [N, H, V, K] or null: incoming state of sequences of one segment (forward)
   float* fin;                 // [N, H, V, K] or null
@@ -236,13 +236,13 @@ template <typename T, int AP, bool X, bool WHOLE, int ZB> struct AttnStage {
 
 // A wavefront's 16 ZT columns of M, decayed over the chunk and with what the chunk adds; zf: the z operands of those
 // columns.
-template <typename T, int AP, int ZT, typename Chunk>
+template <typename T, int AP, int ZT, bool GROUPED, typename Chunk>
 __device__ __forceinline__ void attn_update(f32x4 (&m)[ZT][AP / 16], const typename Tiles<T>::Frag* zf, const Chunk& ck,
                                             int g, int l16) {
   typedef Tiles<T> Ti;
   constexpr int BLK = Ti::BLK, NS = Chunk::CH / BLK, EL = BLK / 4, NM = AP / 16, NTZ = Ti::TERMS(3);
-  // LDS reads are issued in groups, ahead of the products that wait for them: left to itself the compiler
-  // places them one by one before their use, and every one's latency shows.
+  // GROUPED: LDS reads are issued in groups, ahead of the products that wait for them, where the compiler would place
+  // them one by one before their use. That takes registers and pays where they are there.
   constexpr int FRAGS = NM * NS, GROUP = 4;  // operands, number j NS + b
   typename Ti::Frag y[2][GROUP];
   f32x4 r[NS][EL / 4];
@@ -257,7 +257,7 @@ __device__ __forceinline__ void attn_update(f32x4 (&m)[ZT][AP / 16], const typen
     for (int e = 0; e < EL; e += 4) r[b][e / 4] = *reinterpret_cast<const f32x4*>(ck.rs + BLK * b + Ti::down_row(g, e));
   const float keep = ck.whole;
   read(0);
-  __builtin_amdgcn_sched_barrier(0);
+  if (GROUPED) __builtin_amdgcn_sched_barrier(0);
   typename Ti::Frag zt[ZT][NS][NTZ];
 #pragma unroll
   for (int z = 0; z < ZT; ++z) {
@@ -275,7 +275,7 @@ __device__ __forceinline__ void attn_update(f32x4 (&m)[ZT][AP / 16], const typen
   for (int n = 0; n < FRAGS / GROUP; ++n) {
     if (n + 1 < FRAGS / GROUP) {
       read(n + 1);
-      __builtin_amdgcn_sched_barrier(0);
+      if (GROUPED) __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
     for (int k = 0; k < NTZ; ++k)
@@ -320,7 +320,7 @@ __global__ __launch_bounds__(512) void attn_state_kernel(AttnK<T> a) {
     typename Ti::Frag zf[NS];
 #pragma unroll
     for (int b = 0; b < NS; ++b) zf[b] = Ti::template down<ZB>(ck.zs, b, 16 * w, g, l16);
-    attn_update<T, AP, 1>(m, zf, ck, g, l16);
+    attn_update<T, AP, 1, false>(m, zf, ck, g, l16);
     __syncthreads();
   }
   const AttnRole<T>& R = a.role[at.role];
@@ -550,7 +550,7 @@ __global__ __launch_bounds__(512) void attn_kernel(AttnK<T> a) {
     float f[NU];
 #pragma unroll
     for (int i = 0; i < NU; ++i) f[i] = ck.fs[16 * i + l16];
-    attn_update<T, AP, ZT>(m, &zf[0][0], ck, g, l16);
+    attn_update<T, AP, ZT, (NT > 2)>(m, &zf[0][0], ck, g, l16);
 #pragma unroll
     for (int i = 0; i < NU; ++i)
 #pragma unroll
