@@ -31,7 +31,7 @@ struct GroupNormBwdArgs {
 // in channel block c lie at part g + c.
 struct GroupNormPlan {
   bool rows;
-  bool vec;                   // 16-byte pieces
+  bool vec;                   // rows: 16-byte pieces
   int L, E, lanes, cblocks;
   int64_t slots;
 };

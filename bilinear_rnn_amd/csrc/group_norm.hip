@@ -174,21 +174,6 @@ __global__ __launch_bounds__(LPR > kNormThreads ? LPR : kNormThreads) void group
 
 // --- sequences -----------------------------------------------------------------------------------
 
-struct Moments {  // count, mean, sum of squared distances from it
-  float n, mean, m2;
-  __device__ __forceinline__ void join(const Moments& o) {
-    const float all = n + o.n, d = o.mean - mean;
-    if (o.n == 0.f) return;
-    const float f = o.n / all;
-    mean = fmaf(d, f, mean);
-    m2 += fmaf(d * d, n * f, o.m2);
-    n = all;
-  }
-};
-__device__ __forceinline__ Moments shuffled(const Moments& m, int off) {
-  return {__shfl_xor(m.n, off, kWave), __shfl_xor(m.mean, off, kWave), __shfl_xor(m.m2, off, kWave)};
-}
-
 template <typename T> struct GroupK {
   const T* x;
   const T* dy;
@@ -204,10 +189,12 @@ template <typename T> struct GroupK {
   float* cols;                // [slots, 2, D] or null
 };
 
-// A workgroup's tile: tokens of one sequence and `lanes` pieces of E channels; 256 / lanes tokens at a time.
+// A workgroup's tile: tokens of one sequence and `lanes` pieces of E channels; 256 / lanes tokens at a time. A row's
+// last piece is moved back so that it lies inside the row; what it shares with its neighbour is the neighbour's.
 template <typename T, int E> struct GroupTile {
   ScanPlace pl;
-  int cb, CB, RG, l, rg, c0;
+  int cb, CB, RG, l, rg, first, c0;   // first: the piece's own first channel; c0: where it is read
+  int lo, width;              // the block's first channel and channels
   int gA, groups;             // groups that the block's channels belong to
   int64_t slot;
   bool have;
@@ -219,25 +206,28 @@ template <typename T, int E> struct GroupTile {
     RG = 256 / a.lanes;
     l = threadIdx.x & (a.lanes - 1);
     rg = threadIdx.x / a.lanes;
-    c0 = cb * CB + l * E;
-    have = c0 < a.D;
-    gA = cb * CB / a.C;
-    groups = (min(a.D, cb * CB + CB) - 1) / a.C - gA + 1;
+    lo = cb * CB;
+    width = min(CB, a.D - lo);
+    first = lo + l * E;
+    c0 = min(first, a.D - E);
+    have = first < a.D;
+    gA = lo / a.C;
+    groups = (lo + width - 1) / a.C - gA + 1;
   }
   template <typename Q> __device__ __forceinline__ Q* row(Q* base, const GroupK<T>& a, int t) const {
     return base + (static_cast<int64_t>(pl.b) * a.Tn + t) * a.D + c0;
   }
-  // Lanes that share a group of the block in the joins: a power of two.
+  // Lanes that share a group of the block in its sums: a power of two.
   __device__ __forceinline__ int join_lanes() const {
     int p = 64;
     while (p > 4 && groups * p > 256) p >>= 1;
     return p;
   }
-  // f(first piece, one past the last piece) of group gA + i in this block, in units of E channels.
-  __device__ __forceinline__ int piece_lo(const GroupK<T>& a, int i) const { return max(0, (gA + i) * a.C - cb * CB) / E; }
-  __device__ __forceinline__ int piece_hi(const GroupK<T>& a, int i) const {
-    return min(CB, (gA + i + 1) * a.C - cb * CB) / E;
-  }
+  // First channel of group gA + i in this block, and one past its last, counted from the block's first.
+  __device__ __forceinline__ int group_lo(const GroupK<T>& a, int i) const { return max(0, (gA + i) * a.C - lo); }
+  __device__ __forceinline__ int group_hi(const GroupK<T>& a, int i) const { return min(width, (gA + i + 1) * a.C - lo); }
+  // Tokens of the tile that row group q works on.
+  __device__ __forceinline__ int tokens(int q) const { return (pl.t1 - pl.t0 - q + RG - 1) / RG; }
 };
 
 template <typename T, int E> __device__ __forceinline__ void get(const T* p, float (&x)[E]) {
@@ -248,67 +238,87 @@ template <typename T, int E> __device__ __forceinline__ void put(T* p, const flo
   if constexpr (E == 1) Elem<T>::store(p, 0, x[0]);
   else Pack<T, E, true>::store(p, x, E);
 }
+// A piece's results, without what a moved one shares with its neighbour.
+template <typename T, int E> __device__ __forceinline__ void put_own(T* p, const float (&x)[E], int shared) {
+  if (shared == 0) {
+    put<T, E>(p, x);
+  } else {
+#pragma unroll
+    for (int e = 1; e < E; ++e)
+      if (e >= shared) Elem<T>::store(p, e, x[e]);
+  }
+}
+template <int E> __device__ __forceinline__ void params(const float* p, int c0, float none, float (&x)[E]) {
+#pragma unroll
+  for (int e = 0; e < E; ++e) x[e] = p ? p[c0 + e] : none;
+}
+// Sum over the P neighbouring lanes (a power of two) that a group has.
+__device__ __forceinline__ float lanes_sum(float x, int P) {
+  for (int off = P / 2; off > 0; off >>= 1) x += __shfl_xor(x, off, kWave);
+  return x;
+}
 
+// Mean and sum of squared distances of a tile's part of every group: per thread about its first value, so that a
+// far mean costs nothing, then from the channels' means.
 template <typename T, int E>
 __global__ __launch_bounds__(256) void group_moments_kernel(GroupK<T> a) {
   const GroupTile<T, E> t(a);
   if (!t.pl.ok || t.pl.t1 <= t.pl.t0) return;
-  __shared__ float cnt[256], mean[256], m2[256];
+  __shared__ float mean[256 * E], m2[256 * E];  // [row group][channel]
   float k[E], s[E], ss[E];
-  int n = 0;
-  if (t.have) {
-    for (int r = t.pl.t0 + t.rg; r < t.pl.t1; r += t.RG, ++n) {
+  if (t.have && t.tokens(t.rg) > 0) {
+    const int r0 = t.pl.t0 + t.rg;
+    get<T, E>(t.row(a.x, a, r0), k);
+#pragma unroll
+    for (int e = 0; e < E; ++e) s[e] = ss[e] = 0.f;
+#pragma unroll 4
+    for (int r = r0 + t.RG; r < t.pl.t1; r += t.RG) {
       float x[E];
       get<T, E>(t.row(a.x, a, r), x);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        if (n == 0) {  // sums about the first value, so that a far mean costs nothing
-          k[e] = x[e];
-          s[e] = ss[e] = 0.f;
-        }
         const float d = x[e] - k[e];
         s[e] += d;
         ss[e] = fmaf(d, d, ss[e]);
       }
     }
-  }
-  Moments m{0.f, 0.f, 0.f};
-  if (n > 0) {
-    const float fn = static_cast<float>(n), inv = 1.f / fn;
+    const float inv = 1.f / static_cast<float>(t.tokens(t.rg));
 #pragma unroll
     for (int e = 0; e < E; ++e) {
+      if (t.c0 + e < t.first) continue;
+      const int at = t.rg * t.CB + t.c0 + e - t.lo;
       const float d = s[e] * inv;
-      m.join({fn, k[e] + d, fmaxf(fmaf(-d, s[e], ss[e]), 0.f)});
+      mean[at] = k[e] + d;
+      m2[at] = fmaxf(fmaf(-d, s[e], ss[e]), 0.f);
     }
   }
-  cnt[threadIdx.x] = m.n;
-  mean[threadIdx.x] = m.mean;
-  m2[threadIdx.x] = m.m2;
   __syncthreads();
-  const int P = t.join_lanes(), j = threadIdx.x & (P - 1);
+  const int P = t.join_lanes(), j = threadIdx.x & (P - 1), rows = min(t.RG, t.pl.t1 - t.pl.t0);
   for (int i = threadIdx.x / P; i < t.groups; i += 256 / P) {
-    const int lo = t.piece_lo(a, i), w = t.piece_hi(a, i) - lo;
-    Moments g{0.f, 0.f, 0.f};
-    for (int q = j; q < w * t.RG; q += P) {
-      const int at = q / w * a.lanes + lo + q % w;
-      g.join({cnt[at], mean[at], m2[at]});
+    const int lo = t.group_lo(a, i), hi = t.group_hi(a, i);
+    float sum = 0.f, sq = 0.f;
+    for (int q = 0; q < rows; ++q) {
+      const float n = static_cast<float>(t.tokens(q));
+      for (int c = lo + j; c < hi; c += P) sum = fmaf(n, mean[q * t.CB + c], sum);
     }
-    for (int off = P / 2; off > 0; off >>= 1) {
-      // both sides join in the same order, so that they agree
-      const Moments o = shuffled(g, off);
-      Moments first = j & off ? o : g;
-      first.join(j & off ? g : o);
-      g = first;
+    const float mu = lanes_sum(sum, P) / (static_cast<float>(t.pl.t1 - t.pl.t0) * static_cast<float>(hi - lo));
+    for (int q = 0; q < rows; ++q) {
+      const float n = static_cast<float>(t.tokens(q));
+      for (int c = lo + j; c < hi; c += P) {
+        const float d = mean[q * t.CB + c] - mu;
+        sq += fmaf(n * d, d, m2[q * t.CB + c]);
+      }
     }
+    sq = lanes_sum(sq, P);
     if (j == 0) {
       float* const to = a.part + 2 * (t.slot * (a.G + a.cblocks) + t.gA + i + t.cb);
-      to[0] = g.mean;
-      to[1] = g.m2;
+      to[0] = mu;
+      to[1] = sq;
     }
   }
 }
 
-// Calls f(part, tokens of the tile, channels of the part) for every q-th part of group g of the tile's sequence.
+// Calls f(part, values in the part) for every P-th part of group g of the tile's sequence, from the j-th on.
 template <typename T, int E, typename F>
 __device__ __forceinline__ void for_parts(const GroupTile<T, E>& t, const GroupK<T>& a, int g, int j, int P, F f) {
   const int len = t.pl.s1 - t.pl.s0, nseg = segments_of(len, a.L);
@@ -318,7 +328,7 @@ __device__ __forceinline__ void for_parts(const GroupTile<T, E>& t, const GroupK
     const int tile = q / ncb, cb = cA + q % ncb;
     const int rows = min(a.L, len - tile * a.L);
     const int chans = min((g + 1) * a.C, (cb + 1) * t.CB) - max(g * a.C, cb * t.CB);
-    f(a.part + 2 * ((slot0 + tile) * (a.G + a.cblocks) + g + cb), rows, chans);
+    f(a.part + 2 * ((slot0 + tile) * (a.G + a.cblocks) + g + cb), static_cast<float>(rows) * static_cast<float>(chans));
   }
 }
 
@@ -326,53 +336,66 @@ template <typename T, int E>
 __global__ __launch_bounds__(256) void group_apply_kernel(GroupK<T> a) {
   const GroupTile<T, E> t(a);
   if (!t.pl.ok) return;
-  __shared__ float mean[72], rstd[72];
+  __shared__ float mean[64 * E + 8], rstd[64 * E + 8];
   const int P = t.join_lanes(), j = threadIdx.x & (P - 1);
   const bool some = t.pl.t1 > t.pl.t0;
+  const float inv = 1.f / (static_cast<float>(t.pl.s1 - t.pl.s0) * static_cast<float>(a.C));
   for (int i = threadIdx.x / P; i < t.groups; i += 256 / P) {
     const int g = t.gA + i;
-    Moments m{0.f, 0.f, 0.f};
+    float sum = 0.f, sq = 0.f;
+    if (some) for_parts(t, a, g, j, P, [&](const float* p, float n) { sum = fmaf(n, p[0], sum); });
+    const float mu = some ? lanes_sum(sum, P) * inv : 0.f;
     if (some)
-      for_parts(t, a, g, j, P, [&](const float* p, int rows, int chans) {
-        m.join({static_cast<float>(rows) * static_cast<float>(chans), p[0], p[1]});
+      for_parts(t, a, g, j, P, [&](const float* p, float n) {
+        const float d = p[0] - mu;
+        sq += fmaf(n * d, d, p[1]);
       });
-    for (int off = P / 2; off > 0; off >>= 1) {
-      const Moments o = shuffled(m, off);
-      Moments first = j & off ? o : m;
-      first.join(j & off ? m : o);
-      m = first;
-    }
+    sq = lanes_sum(sq, P);
     if (j == 0) {
-      const float rs = some ? 1.f / sqrtf(m.m2 / m.n + a.eps) : 0.f;
-      mean[i] = m.mean;
+      const float rs = some ? 1.f / sqrtf(fmaf(sq, inv, a.eps)) : 0.f;
+      mean[i] = mu;
       rstd[i] = rs;
       // one workgroup of the sequence hands them on: that of its first tile and the group's first channel
-      if (a.stats && t.pl.seg == 0 && g * a.C >= t.cb * t.CB) {
-        a.stats[2 * (static_cast<int64_t>(t.pl.n) * a.G + g)] = m.mean;
+      if (a.stats && t.pl.seg == 0 && g * a.C >= t.lo) {
+        a.stats[2 * (static_cast<int64_t>(t.pl.n) * a.G + g)] = mu;
         a.stats[2 * (static_cast<int64_t>(t.pl.n) * a.G + g) + 1] = rs;
       }
     }
   }
   __syncthreads();
   if (!t.have || !some) return;
-  const int i = t.c0 / a.C - t.gA;  // a piece lies in one group
-  const float mu = mean[i], rs = rstd[i];
-  float w[E], b[E];
+  float mu[E], rs[E], w[E], b[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    w[e] = a.weight ? a.weight[t.c0 + e] : 1.f;
-    b[e] = a.bias ? a.bias[t.c0 + e] : 0.f;
+    const int i = max(t.c0 + e, t.lo) / a.C - t.gA;  // a moved piece may begin before the block
+    mu[e] = mean[i];
+    rs[e] = rstd[i];
   }
-#pragma unroll 2
+  params<E>(a.weight, t.c0, 1.f, w);
+  params<E>(a.bias, t.c0, 0.f, b);
+#pragma unroll
+  for (int e = 0; e < E; ++e) w[e] *= rs[e];
+#pragma unroll 4
   for (int r = t.pl.t0 + t.rg; r < t.pl.t1; r += t.RG) {
     float x[E];
     get<T, E>(t.row(a.x, a, r), x);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const float p = fmaf((x[e] - mu) * rs, w[e], b[e]);
+      const float p = fmaf(x[e] - mu[e], w[e], b[e]);
       x[e] = a.silu ? p * sigmoid_fast(p) : p;
     }
-    put<T, E>(t.row(a.out, a, r), x);
+    put_own<T, E>(t.row(a.out, a, r), x, t.first - t.c0);
+  }
+}
+
+// The statistics of a piece's channels, given.
+template <typename T, int E>
+__device__ __forceinline__ void given_stats(const GroupTile<T, E>& t, const GroupK<T>& a, float (&mu)[E], float (&rs)[E]) {
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const float* const st = a.stats + 2 * (static_cast<int64_t>(t.pl.n) * a.G + (t.c0 + e) / a.C);
+    mu[e] = st[0];
+    rs[e] = st[1];
   }
 }
 
@@ -384,33 +407,28 @@ __global__ __launch_bounds__(256) void group_sums_kernel(GroupK<T> a) {
   const bool some = t.pl.ok && t.pl.t1 > t.pl.t0;
   if (!some) {
     if (a.cols)
-      for (int c = threadIdx.x; c < t.CB; c += 256)
-        if (t.cb * t.CB + c < a.D) {
-          a.cols[t.slot * 2 * a.D + t.cb * t.CB + c] = 0.f;
-          a.cols[t.slot * 2 * a.D + a.D + t.cb * t.CB + c] = 0.f;
-        }
+      for (int c = threadIdx.x; c < t.width; c += 256) {
+        a.cols[t.slot * 2 * a.D + t.lo + c] = 0.f;
+        a.cols[t.slot * 2 * a.D + a.D + t.lo + c] = 0.f;
+      }
     return;
   }
   float an[E], ad[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) an[e] = ad[e] = 0.f;
   if (t.have) {
-    const float* const st = a.stats + 2 * (static_cast<int64_t>(t.pl.n) * a.G + t.c0 / a.C);
-    const float mu = st[0], rs = st[1];
-    float w[E], b[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      w[e] = a.weight ? a.weight[t.c0 + e] : 1.f;
-      b[e] = a.bias ? a.bias[t.c0 + e] : 0.f;
-    }
-#pragma unroll 2
+    float mu[E], rs[E], w[E], b[E];
+    given_stats(t, a, mu, rs);
+    params<E>(a.weight, t.c0, 1.f, w);
+    params<E>(a.bias, t.c0, 0.f, b);
+#pragma unroll 4
     for (int r = t.pl.t0 + t.rg; r < t.pl.t1; r += t.RG) {
       float x[E], d[E];
       get<T, E>(t.row(a.x, a, r), x);
       get<T, E>(t.row(a.dy, a, r), d);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const float n = (x[e] - mu) * rs;
+        const float n = (x[e] - mu[e]) * rs[e];
         if (a.silu) {
           const float p = fmaf(n, w[e], b[e]), sg = sigmoid_fast(p);
           d[e] *= sg * fmaf(p, 1.f - sg, 1.f);
@@ -419,42 +437,39 @@ __global__ __launch_bounds__(256) void group_sums_kernel(GroupK<T> a) {
         ad[e] += d[e];
       }
     }
-  }
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    sn[t.rg * t.CB + t.l * E + e] = an[e];
-    sd[t.rg * t.CB + t.l * E + e] = ad[e];
+    for (int e = 0; e < E; ++e) {
+      if (t.c0 + e < t.first) continue;
+      sn[t.rg * t.CB + t.c0 + e - t.lo] = an[e];
+      sd[t.rg * t.CB + t.c0 + e - t.lo] = ad[e];
+    }
   }
   __syncthreads();
-  for (int c = threadIdx.x; c < t.CB; c += 256) {
+  for (int c = threadIdx.x; c < t.width; c += 256) {
     float n = sn[c], d = sd[c];
     for (int q = 1; q < t.RG; ++q) {
       n += sn[q * t.CB + c];
       d += sd[q * t.CB + c];
     }
-    const int ch = t.cb * t.CB + c;
-    const bool in = ch < a.D;
-    if (in && a.cols) {
+    const int ch = t.lo + c;
+    if (a.cols) {
       a.cols[t.slot * 2 * a.D + ch] = n;
       a.cols[t.slot * 2 * a.D + a.D + ch] = d;
     }
-    const float w = in ? (a.weight ? a.weight[ch] : 1.f) : 0.f;
+    const float w = a.weight ? a.weight[ch] : 1.f;
     sn[c] = n * w;
     sd[c] = d * w;
   }
   __syncthreads();
   const int P = t.join_lanes(), j = threadIdx.x & (P - 1);
   for (int i = threadIdx.x / P; i < t.groups; i += 256 / P) {
-    const int lo = t.piece_lo(a, i) * E, hi = t.piece_hi(a, i) * E;
     float n = 0.f, d = 0.f;
-    for (int c = lo + j; c < hi; c += P) {
+    for (int c = t.group_lo(a, i) + j; c < t.group_hi(a, i); c += P) {
       n += sn[c];
       d += sd[c];
     }
-    for (int off = P / 2; off > 0; off >>= 1) {
-      n += __shfl_xor(n, off, kWave);
-      d += __shfl_xor(d, off, kWave);
-    }
+    n = lanes_sum(n, P);
+    d = lanes_sum(d, P);
     if (j == 0) {
       float* const to = a.part + 2 * (t.slot * (a.G + a.cblocks) + t.gA + i + t.cb);
       to[0] = n;
@@ -467,19 +482,17 @@ template <typename T, int E>
 __global__ __launch_bounds__(256) void group_dx_kernel(GroupK<T> a) {
   const GroupTile<T, E> t(a);
   if (!t.pl.ok || t.pl.t1 <= t.pl.t0) return;
-  __shared__ float mgn[72], mg[72];
+  __shared__ float mgn[64 * E + 8], mg[64 * E + 8];
   const int P = t.join_lanes(), j = threadIdx.x & (P - 1);
   const float inv = 1.f / (static_cast<float>(t.pl.s1 - t.pl.s0) * static_cast<float>(a.C));
   for (int i = threadIdx.x / P; i < t.groups; i += 256 / P) {
     float n = 0.f, d = 0.f;
-    for_parts(t, a, t.gA + i, j, P, [&](const float* p, int, int) {
+    for_parts(t, a, t.gA + i, j, P, [&](const float* p, float) {
       n += p[0];
       d += p[1];
     });
-    for (int off = P / 2; off > 0; off >>= 1) {
-      n += __shfl_xor(n, off, kWave);
-      d += __shfl_xor(d, off, kWave);
-    }
+    n = lanes_sum(n, P);
+    d = lanes_sum(d, P);
     if (j == 0) {
       mgn[i] = n * inv;
       mg[i] = d * inv;
@@ -487,14 +500,16 @@ __global__ __launch_bounds__(256) void group_dx_kernel(GroupK<T> a) {
   }
   __syncthreads();
   if (!t.have) return;
-  const float* const st = a.stats + 2 * (static_cast<int64_t>(t.pl.n) * a.G + t.c0 / a.C);
-  const float mu = st[0], rs = st[1], mn = mgn[t.c0 / a.C - t.gA], md = mg[t.c0 / a.C - t.gA];
-  float w[E], b[E];
+  float mu[E], rs[E], mn[E], md[E], w[E], b[E];
+  given_stats(t, a, mu, rs);
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    w[e] = a.weight ? a.weight[t.c0 + e] : 1.f;
-    b[e] = a.bias ? a.bias[t.c0 + e] : 0.f;
+    const int i = max(t.c0 + e, t.lo) / a.C - t.gA;
+    mn[e] = mgn[i];
+    md[e] = mg[i];
   }
+  params<E>(a.weight, t.c0, 1.f, w);
+  params<E>(a.bias, t.c0, 0.f, b);
 #pragma unroll 2
   for (int r = t.pl.t0 + t.rg; r < t.pl.t1; r += t.RG) {
     float x[E], d[E];
@@ -502,14 +517,14 @@ __global__ __launch_bounds__(256) void group_dx_kernel(GroupK<T> a) {
     get<T, E>(t.row(a.dy, a, r), d);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const float n = (x[e] - mu) * rs;
+      const float n = (x[e] - mu[e]) * rs[e];
       if (a.silu) {
         const float p = fmaf(n, w[e], b[e]), sg = sigmoid_fast(p);
         d[e] *= sg * fmaf(p, 1.f - sg, 1.f);
       }
-      x[e] = rs * (d[e] * w[e] - md - n * mn);
+      x[e] = rs[e] * (d[e] * w[e] - md[e] - n * mn[e]);
     }
-    put<T, E>(t.row(a.out, a, r), x);
+    put_own<T, E>(t.row(a.out, a, r), x, t.first - t.c0);
   }
 }
 
@@ -539,7 +554,7 @@ GroupNormPlan group_norm_plan(int64_t B, int64_t T, int64_t D, int64_t G, int64_
     p.slots = k;
     return p;
   }
-  p.E = p.vec ? 8 : 1;
+  p.E = D >= 8 ? 8 : 1;
   p.lanes = 64;
   while (p.lanes > 1 && p.lanes / 2 * p.E >= D) p.lanes /= 2;
   p.cblocks = static_cast<int>((D + p.lanes * p.E - 1) / (p.lanes * p.E));
@@ -671,14 +686,14 @@ template <typename T> hipError_t group_fwd_t(const GroupNormArgs& a, float* ws, 
   const bool vec = norm_aligned(a.x) && norm_aligned(a.y);
   const GroupNormPlan p = group_norm_plan(a.B, a.T, a.D, a.G, a.N, a.cu_seqlens != nullptr, vec, false);
   if (p.rows) return p.vec ? rows_fwd<T, true>(a, p, st) : rows_fwd<T, false>(a, p, st);
-  return p.vec ? seqs_fwd<T, 8>(a, p, ws, st) : seqs_fwd<T, 1>(a, p, ws, st);
+  return p.E == 8 ? seqs_fwd<T, 8>(a, p, ws, st) : seqs_fwd<T, 1>(a, p, ws, st);
 }
 
 template <typename T> hipError_t group_bwd_t(const GroupNormBwdArgs& a, float* ws, hipStream_t st) {
   const bool vec = norm_aligned(a.f.x) && norm_aligned(a.dy) && norm_aligned(a.dx);
   const GroupNormPlan p = group_norm_plan(a.f.B, a.f.T, a.f.D, a.f.G, a.f.N, a.f.cu_seqlens != nullptr, vec, true);
   if (p.rows) return p.vec ? rows_bwd<T, true>(a, p, ws, st) : rows_bwd<T, false>(a, p, ws, st);
-  return p.vec ? seqs_bwd<T, 8>(a, p, ws, st) : seqs_bwd<T, 1>(a, p, ws, st);
+  return p.E == 8 ? seqs_bwd<T, 8>(a, p, ws, st) : seqs_bwd<T, 1>(a, p, ws, st);
 }
 
 }  // namespace
