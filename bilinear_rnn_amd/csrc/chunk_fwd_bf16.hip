@@ -160,6 +160,14 @@ __device__ __forceinline__ void put_split(u16* hi, u16* lo, int off, float x) {
   lo[off] = __builtin_bit_cast(u16, b);
 }
 
+// Producer-only barrier (4 wavefronts) through a monotonically increasing LDS counter.
+__device__ __forceinline__ void producer_sync(int* bar, int& epoch, int lane) {
+  epoch += 4;
+  if (lane == 0) __hip_atomic_fetch_add(bar, 1, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_WORKGROUP);
+  while (__hip_atomic_load(bar, __ATOMIC_ACQUIRE, __HIP_MEMORY_SCOPE_WORKGROUP) < epoch)
+    __builtin_amdgcn_s_sleep(1);
+}
+
 // K^T operand (rows = key channels 16kb..16kb+15, reduction = tokens
 // 32s2 + {4g..4g+3, 16+4g..16+4g+3}) from the row-major K tile.
 template <int K>

@@ -169,14 +169,6 @@ __device__ __forceinline__ double wave_inclusive_scan_f64(double x, int lane) {
   return x;
 }
 
-// Producer-only barrier (4 wavefronts) through a monotonically increasing LDS counter.
-__device__ __forceinline__ void producer_sync(int* bar, int& epoch, int lane) {
-  epoch += 4;
-  if (lane == 0) __hip_atomic_fetch_add(bar, 1, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_WORKGROUP);
-  while (__hip_atomic_load(bar, __ATOMIC_ACQUIRE, __HIP_MEMORY_SCOPE_WORKGROUP) < epoch)
-    __builtin_amdgcn_s_sleep(1);
-}
-
 template <typename T> struct Elem;
 template <> struct Elem<float> {
   __device__ static float load(const float* p, int64_t i) { return p[i]; }

@@ -530,6 +530,9 @@ __global__ __launch_bounds__(256) void group_dx_kernel(GroupK<T> a) {
 
 // --- launches ------------------------------------------------------------------------------------
 
+// Rows: forward, 32768 tokens of 16 heads of 128, with 1024 threads per compute unit 61 us (256: 92, 512: 70, 2048: 62);
+// backward, 8192 tokens, with 512 33 us (256: 39, 1024: 39, 2048: 55). Sequences: about 1024 workgroups; twice as many take
+// 17% longer (backward of 4 x 2048 tokens, 2048 channels in 32 groups), half as many the same.
 GroupNormPlan group_norm_plan(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N, bool packed, bool vec, bool bwd) {
   GroupNormPlan p{};
   const int64_t C = D / G;
@@ -561,6 +564,7 @@ GroupNormPlan group_norm_plan(int64_t B, int64_t T, int64_t D, int64_t G, int64_
   const int64_t step = 256 / p.lanes;
   int64_t L = B * T * p.cblocks / 1024;
   L = L < 4 * step ? 4 * step : L > 512 ? 512 : L;
+  if (L < T / 4096) L = T / 4096;  // every workgroup joins all tiles of its sequence
   L = (L + step - 1) / step * step;
   p.L = static_cast<int>(L);
   p.slots = packed ? T / L + N + 1 : B * ((T + L - 1) / L);

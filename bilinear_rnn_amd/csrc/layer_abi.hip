@@ -443,10 +443,10 @@ bool attn_sizes_ok(int32_t B, int32_t T, int32_t H, int32_t Hk, int32_t K, int32
          V >= comba::kAttnMinWidth && V <= comba::kAttnMaxWidth && static_cast<int64_t>(B) * T <= kMaxTokens;
 }
 
-// Column blocks of the largest launch per (segment, head), and the blocks of the scan over segments.
+// `blocks`: column blocks of the largest launch per (segment, head), of 512 threads; and the scan over segments.
 int32_t check_attn_grid(int64_t slots, int64_t H, int64_t N, int32_t K, int32_t V, int64_t blocks) {
   const int64_t units = slots * H + 8;
-  if (units * blocks * 4 > kMaxBlocks || N * H * comba::attn_inner_blocks(K, V) > kMaxBlocks)
+  if (units * blocks * 2 > kMaxBlocks || N * H * comba::attn_inner_blocks(K, V) > kMaxBlocks)
     return report(COMBA_ERR_UNSUPPORTED, "too many (segment, head) pairs for one launch");
   return COMBA_OK;
 }
@@ -562,7 +562,7 @@ COMBA_API int32_t comba_linear_attn_bwd(const void* q, const void* k, const void
   int64_t N = 0;
   if ((rc = check_batch(cu_seqlens, num_seqs, B, T, N)) != COMBA_OK) return rc;
   const comba::AttnPlan p = comba::attn_bwd_plan(B, T, H, N, cu_seqlens != nullptr);
-  if ((rc = check_attn_grid(p.slots, H, N, K, V, 2 * comba::attn_blocks(K) + 2 * comba::attn_blocks(V))) != COMBA_OK) return rc;
+  if ((rc = check_attn_grid(p.slots, H, N, K, V, 2 * comba::attn_blocks(K > V ? K : V))) != COMBA_OK) return rc;
   const int64_t rows = static_cast<int64_t>(B) * T, e = size_of(dtype);
   const AttnBwdWs w = attn_bwd_ws(p, rows, H, num_qk_heads, K, V);
   rc = check_workspace(workspace, workspace_bytes, w.total,

@@ -118,7 +118,11 @@ __global__ __launch_bounds__(256) void attn_carry_kernel(const float* __restrict
 // chunk the scores' parts of q . dq and k . dk have the same sum, so only the parts that come from
 // the states are carried from chunk to chunk: what is rounded in the others stays within the chunk.
 // rdot: [q and k][all and states' part][Z blocks, H, tokens], the four `one` floats apart.
+// A decay that is 0 in float32 has a gradient of 0: the sums only cancel to their rounding there.
+constexpr float kNoDecay = -104.f;  // e^-103.97 is half of float32's least number
+
 __global__ __launch_bounds__(256) void attn_decay_grad_kernel(const float* __restrict__ rdot, const double* __restrict__ inner,
+                                                              const float* __restrict__ log_decay,
                                                               const int32_t* __restrict__ cu, int N, int T, int H, int L,
                                                               int CH, int64_t slots, int64_t tokens, int64_t one,
                                                               int zblocks, int eblocks, float* __restrict__ out,
@@ -169,7 +173,10 @@ __global__ __launch_bounds__(256) void attn_decay_grad_kernel(const float* __res
     const double s = wave_scan_f64_dpp(get(c, 0)) + part[c];
     if (lane < CH && token(c) < pl.t1) {
       sum += s;
-      if (!hsum) out[(row0 + token(c)) * H + h] = static_cast<float>(s);
+      if (!hsum) {
+        const int64_t to = (row0 + token(c)) * H + h;
+        out[to] = log_decay[to] < kNoDecay ? 0.f : static_cast<float>(s);
+      }
     }
   }
   if (hsum) {
@@ -181,7 +188,8 @@ __global__ __launch_bounds__(256) void attn_decay_grad_kernel(const float* __res
 }
 
 // Constant decays: the heads' sums over all segments, in a fixed order.
-__global__ __launch_bounds__(256) void attn_head_sum_kernel(const double* __restrict__ hsum, int64_t slots, int H,
+__global__ __launch_bounds__(256) void attn_head_sum_kernel(const double* __restrict__ hsum,
+                                                            const float* __restrict__ log_decay, int64_t slots, int H,
                                                             float* __restrict__ out) {
   __shared__ double red[4];
   const int h = blockIdx.x, lane = threadIdx.x & 63;
@@ -190,7 +198,8 @@ __global__ __launch_bounds__(256) void attn_head_sum_kernel(const double* __rest
   s = wave_scan_f64_dpp(s);
   if (lane == 63) red[threadIdx.x >> 6] = s;
   __syncthreads();
-  if (threadIdx.x == 0) out[h] = static_cast<float>((red[0] + red[1]) + (red[2] + red[3]));
+  if (threadIdx.x == 0)
+    out[h] = log_decay[h] < kNoDecay ? 0.f : static_cast<float>((red[0] + red[1]) + (red[2] + red[3]));
 }
 
 // dq and dk of shared heads: sums over the value heads of a group, of the tokens that belong to a sequence.
@@ -395,11 +404,11 @@ template <typename T> hipError_t attn_bwd_t(const AttnBwdArgs& a, const AttnPlan
   k.roles = 1;
   if ((e = run_attn<T, 2, false>(k, K, st)) != hipSuccess) return e;
   attn_decay_grad_kernel<<<static_cast<unsigned>(p.slots * H), 256, 0, st>>>(
-      a.rdot, a.inner, f.cu_seqlens, f.N, f.T, H, p.L, attn_chunk<T>(padded(V)), p.slots, k.tokens, one, zblocks, eblocks, a.dlog_decay,
-      f.per_token ? nullptr : a.hsum);
+      a.rdot, a.inner, f.log_decay, f.cu_seqlens, f.N, f.T, H, p.L, attn_chunk<T>(padded(V)), p.slots, k.tokens, one, zblocks,
+      eblocks, a.dlog_decay, f.per_token ? nullptr : a.hsum);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   if (!f.per_token) {
-    attn_head_sum_kernel<<<H, 256, 0, st>>>(a.hsum, p.slots, H, a.dlog_decay);
+    attn_head_sum_kernel<<<H, 256, 0, st>>>(a.hsum, f.log_decay, p.slots, H, a.dlog_decay);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   if (a.dqk) {
