@@ -12,7 +12,7 @@
 #include "group_norm.h"
 #include "launch.h"
 #include "norm_rows.h"
-#include "scan_common.h"
+#include "packed_place.h"
 
 namespace comba {
 
@@ -201,7 +201,7 @@ template <typename T, int E> struct GroupTile {
   __device__ __forceinline__ GroupTile(const GroupK<T>& a) {
     slot = blockIdx.x / a.cblocks;
     cb = blockIdx.x % a.cblocks;
-    pl = scan_place<1>(slot, 0, a.cu, a.N, a.Tn, 1, 1, a.L);
+    pl = token_place(slot, a.cu, a.N, a.Tn, a.L);
     CB = a.lanes * E;
     RG = 256 / a.lanes;
     l = threadIdx.x & (a.lanes - 1);

@@ -17,7 +17,6 @@
 #include "comba.h"
 #include "linear_attn_kernel.h"
 #include "launch.h"
-#include "scan_common.h"
 
 namespace comba {
 
@@ -36,8 +35,14 @@ __global__ __launch_bounds__(256) void attn_carry_kernel(const float* __restrict
   __shared__ float red[4];
   const int blocks = (KV + kAttnScanElems - 1) / kAttnScanElems;
   const int eb = blockIdx.x % blocks;
-  const int64_t nh = blockIdx.x / blocks;
-  const int n = static_cast<int>(nh / H), h = static_cast<int>(nh - static_cast<int64_t>(n) * H);
+  int64_t nh = blockIdx.x / blocks;
+  int n = static_cast<int>(nh / H);
+  const int h = static_cast<int>(nh - static_cast<int64_t>(n) * H);
+  if (!BWD && cu) {  // the n-th sequence that is cut
+    int j = n;
+    if (!packed_item<8>(cu, N, T, [&](int len) { return len > L ? 1 : 0; }, j, n)) return;
+    nh = static_cast<int64_t>(n) * H + h;
+  }
   int b, t0, t1;
   sequence_range(cu, n, T, b, t0, t1);
   const int len = t1 - t0, nseg = segments_of(len, L);
@@ -129,9 +134,9 @@ __global__ __launch_bounds__(256) void attn_decay_grad_kernel(const float* __res
                                                               double* __restrict__ hsum) {
   __shared__ double part[kAttnMaxSegment / 16], end, sums[4];  // the states' part of every chunk; <gradient, state> at the end
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int64_t unit = blockIdx.x, slot = unit / H;
+  const int64_t unit = blockIdx.x, slot = blockIdx.x / static_cast<uint32_t>(H);
   const int h = static_cast<int>(unit - slot * H);
-  const ScanPlace pl = scan_place<1>(slot, 0, cu, N, T, 1, 1, L);
+  const ScanPlace pl = token_place(slot, cu, N, T, L);
   const bool some = pl.ok && pl.t1 > pl.t0;
   if (hsum && !some && threadIdx.x == 0) hsum[unit] = 0.0;
   if (!some) return;
@@ -309,7 +314,7 @@ __global__ __launch_bounds__(256) void attn_step_kernel(const T* __restrict__ q,
 // at B = 8, T = 4096, 16 heads of 128, uncut 192 us, in two segments 210.
 // Packed batches are cut where a sequence is longer than 1.5 times a compute unit's share of all: the lengths are not known
 // here, and a segment of L tokens takes its time in the state pass even if it is the only one (64 sequences, 40001
-// tokens, 32 heads of 64: uncut 245 us, 2048 281, 256 443).
+// tokens, 32 heads of 64: 7500 tokens, so uncut, 255 us, 2048 281, 256 443).
 AttnPlan attn_plan(int64_t B, int64_t T, int64_t H, int64_t V, int64_t N, bool packed) {
   if (!packed && B * H * attn_blocks(static_cast<int>(V)) >= 256) return AttnPlan{0, N};
   const int64_t units = H * ((V + 127) / 128);
@@ -356,9 +361,14 @@ template <typename T> hipError_t attn_t(const AttnArgs& f, const AttnPlan& p, co
                           f.K, f.V, false, true, f.scale, f.scale, 1.f};
   hipError_t e;
   if (p.L) {
+    // of a packed batch only the segments and sequences that have something to carry, at most T / L each: 64 sequences,
+    // 40001 tokens, 32 heads of 64, a workgroup for every slot 20 us
+    const int64_t most = f.cu_seqlens ? f.T / p.L : f.N;
+    k.cut = f.cu_seqlens ? most : 0;
     if ((e = run_attn<T, 2, true>(k, f.K, st)) != hipSuccess) return e;
+    k.cut = 0;
     const int blocks = attn_inner_blocks(f.K, f.V);
-    attn_carry_kernel<false><<<static_cast<unsigned>(static_cast<int64_t>(f.N) * f.H * blocks), 256, 0, st>>>(
+    attn_carry_kernel<false><<<static_cast<unsigned>((most < f.N ? most : f.N) * f.H * blocks), 256, 0, st>>>(
         f.init, nullptr, f.cu_seqlens, f.N, f.T, f.H, f.K * f.V, p.L, w.state, nullptr, w.decay, nullptr, nullptr);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }

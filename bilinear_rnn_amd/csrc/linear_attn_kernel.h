@@ -4,7 +4,7 @@
 #include "attn_tiles.h"
 #include "comba.h"
 #include "linear_attn.h"
-#include "scan_common.h"
+#include "packed_place.h"
 
 namespace comba {
 
@@ -37,6 +37,7 @@ template <typename T> struct AttnK {
   double* decay;              // [slots, H]: the segment's sum of log2 decays (state pass)
   int N, Tn, H, K, V, L, roles;
   int64_t slots, tokens;
+  int64_t cut;                // state pass of a packed forward: segments that are not their sequence's last, at most; else 0
   bool per_token;
   bool whole_pass;            // backward: every segment has its states in role.state; state pass: the last one too
 };
@@ -98,18 +99,37 @@ struct AttnPlace {
   int64_t unit, row0;         // row0: token 0 of the batch row
   ScanPlace pl;
   bool back, ok;
-  template <typename T> __device__ __forceinline__ AttnPlace(const AttnK<T>& a, int CH, int ZB) {
+  template <typename T, bool STATE> __device__ __forceinline__ AttnPlace(const AttnK<T>& a, int CH, int ZB,
+                                                                          std::bool_constant<STATE>) {
     // the workgroups of one (segment, head) on one XCD, whose L2 they share
     const int per_unit = attn_unit_blocks(a, ZB);
-    unit = static_cast<int64_t>(blockIdx.x / (8 * per_unit)) * 8 + blockIdx.x % 8;
-    ok = unit < a.slots * a.H;
+    const uint32_t u = blockIdx.x / (8 * per_unit) * 8 + blockIdx.x % 8;  // a launch has fewer than 2^23 workgroups
+    unit = u;
+    ok = unit < (STATE && a.cut ? a.cut : a.slots) * a.H;
     if (!ok) return;
     zb = blockIdx.x / 8 % per_unit;
     role = 0;
     while (zb >= (a.role[role].Z + ZB - 1) / ZB) zb -= (a.role[role++].Z + ZB - 1) / ZB;
-    const int64_t slot = unit / a.H;
-    h = static_cast<int>(unit - slot * a.H);
-    pl = scan_place<1>(slot, 0, a.cu_seqlens, a.N, a.Tn, 1, 1, a.L);
+    int slot = static_cast<int>(u / static_cast<uint32_t>(a.H));
+    h = static_cast<int>(u - static_cast<uint32_t>(slot) * a.H);
+    // Compute units are dealt out in turns, so a pattern of long and short workgroups leaves some idle: full segments come
+    // first, then every sequence's last one; slots that none has, at the end (12 packed sequences of 4096 tokens, 16 heads
+    // of 128: 441 us in the slots' order, 240 so). More sequences than a step of the search takes have few of them.
+    const bool cut = STATE && a.cut;
+    if (a.cu_seqlens && a.L && (cut || a.N <= 64)) {
+      const int L = a.L;
+      int n, s, e;
+      auto full = [=](int len) { return segments_of(len, L) - 1; };
+      const bool in = cut && a.N > 64 ? packed_item<8>(a.cu_seqlens, a.N, a.Tn, full, slot, n)
+                                      : packed_item<1>(a.cu_seqlens, a.N, a.Tn, full, slot, n);
+      if (!in) n = slot;
+      ok = in || (!cut && n < a.N);
+      if (!ok) return;
+      packed_range(a.cu_seqlens, n, a.Tn, s, e);
+      slot = (in ? slot : full(e - s)) + s / L + n;
+      unit = static_cast<int64_t>(slot) * a.H + h;
+    }
+    pl = token_place(slot, a.cu_seqlens, a.N, a.Tn, a.L);
     ok = pl.ok;
     chunks = (pl.t1 - pl.t0 + CH - 1) / CH;
     row0 = static_cast<int64_t>(pl.b) * a.Tn;
@@ -297,7 +317,7 @@ __global__ __launch_bounds__(512) void attn_state_kernel(AttnK<T> a) {
   typedef AttnChunk<T, AP, false, ZB> Chunk;
   constexpr int CH = Chunk::CH, NM = AP / 16, NS = CH / Ti::BLK;
   __shared__ Chunk chunk[2];
-  const AttnPlace at(a, CH, ZB);
+  const AttnPlace at(a, CH, ZB, std::true_type{});
   if (!at.ok || (last_segment(at.pl) && !a.whole_pass)) return;
   const int tid = threadIdx.x, w = tid >> 6, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
   const int chunks = at.chunks;
@@ -330,8 +350,9 @@ __global__ __launch_bounds__(512) void attn_state_kernel(AttnK<T> a) {
   for (int j = 0; j < NM; ++j) sm.store(to, Ti::index(j, g, 0), at.zb * ZB + 16 * w + l16, m[0][j]);
 }
 
-// LDS of the chunk kernel: two or three chunks and the scores of one or two, whatever there is room for.
-template <typename T, int AP, int NT, int ZT> struct AttnShared {
+// LDS of the chunk kernel: two or three chunks and the scores of one or two, whatever there is room for. PAIR: for two
+// workgroups per compute unit.
+template <typename T, int AP, int NT, int ZT, bool PAIR> struct AttnShared {
   typedef Tiles<T> Ti;
   typedef AttnChunk<T, AP, true, 64 * ZT> Chunk;
   static constexpr int CH = Chunk::CH, SCORES = Ti::score_elems(CH, Ti::TERMS(NT));
@@ -339,7 +360,7 @@ template <typename T, int AP, int NT, int ZT> struct AttnShared {
   static constexpr size_t bytes(int chunks, int scores) {
     return chunks * sizeof(Chunk) + scores * SCORES * sizeof(T) + OTHERS;
   }
-  static constexpr size_t ROOM = 160 * 1024;
+  static constexpr size_t ROOM = (PAIR ? 80 : 160) * 1024;
   static constexpr int CHUNKS = bytes(3, 1) <= ROOM ? 3 : 2, PS = bytes(CHUNKS, 2) <= ROOM ? 2 : 1;
   Chunk chunk[CHUNKS];
   alignas(16) T ps[PS][SCORES];
@@ -355,18 +376,19 @@ template <typename T, int AP, int NT, int ZT> struct AttnShared {
 // next chunks into LDS and form their scores, which do not depend on M, with the loads of one chunk more in
 // flight. With room for three chunks a chunk's scores are formed an iteration after it was brought; with two,
 // in the same, behind a barrier of the producers alone. One barrier for all per chunk.
-template <typename T, int AP, int NT, bool WHOLE, int ZT>
-__global__ __launch_bounds__(512) void attn_kernel(AttnK<T> a) {
+// PAIR: two workgroups on a compute unit hide each other's beginning, which most of a short sequence's time is.
+template <typename T, int AP, int NT, bool WHOLE, int ZT, bool PAIR>
+__global__ __launch_bounds__(512, PAIR ? 4 : 2) void attn_kernel(AttnK<T> a) {
   typedef Tiles<T> Ti;
   typedef typename Ti::Frag Frag;
-  typedef AttnShared<T, AP, NT, ZT> Shared;
+  typedef AttnShared<T, AP, NT, ZT, PAIR> Shared;
   typedef typename Shared::Chunk Chunk;
   constexpr int CH = Shared::CH, BLK = Ti::BLK, ZB = 64 * ZT, CHUNKS = Shared::CHUNKS, PS = Shared::PS;
   constexpr int NM = AP / 16, NA = AP / BLK, NS = CH / BLK, NU = CH / 16, NTM = Ti::TERMS(NT);
   __shared__ Shared sh;
   static_assert(sizeof(Shared) <= Shared::ROOM, "LDS");
 
-  const AttnPlace at(a, CH, ZB);
+  const AttnPlace at(a, CH, ZB, std::false_type{});
   if (!at.ok) return;
   const AttnRole<T> R = a.role[at.role];
   const int tid = threadIdx.x, w = tid >> 6, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
@@ -636,12 +658,20 @@ template <typename F> hipError_t with_width(int A, F f) {
   return hipGetLastError();
 }
 
-// Output columns per workgroup: 128, whose scores then serve twice the columns, where that leaves enough
-// workgroups and (A up to 128) the state its registers.
+// Output columns per workgroup: 128, whose scores then serve twice the columns, unless twice as many workgroups of 64 find a
+// compute unit each; and only where (A up to 128) the state has its registers. 4096 tokens, 16 heads of 128, 64 columns and
+// 128: 8 sequences 192 us and 275, 12 294 and 230, 16 384 and 271.
 template <typename T> int attn_columns(const AttnK<T>& k, int A) {
   bool narrow = A > 128;
   for (int r = 0; r < k.roles; ++r) narrow = narrow || k.role[r].Z <= 64;
-  return narrow || k.slots * k.H * attn_unit_blocks(k, 128) < 256 ? 64 : 128;
+  return narrow || k.slots * k.H * attn_unit_blocks(k, 128) <= 128 ? 64 : 128;
+}
+
+// Whether workgroups come in pairs: where there are two for every compute unit and segments are 512 tokens or less on
+// average. 49152 tokens, 32 heads of 64, by length (us alone / in pairs): 16 tokens 3040 / 1570, 64 826 / 482, 256 345 / 252,
+// 512 264 / 226, 1024 230 / 225, 4096 253 / 257; lengths apart, 625 on average, 256 / 262: the longest then takes longer.
+template <typename T> bool attn_in_pairs(const AttnK<T>& k) {
+  return k.slots * k.H * attn_unit_blocks(k, 64) >= 512 && k.tokens <= 512 * k.slots;
 }
 
 // The chunk kernel for the roles in k, of which all have A columns in x and y; STATE: the state kernel.
@@ -652,19 +682,26 @@ template <typename T, int NT, bool STATE> hipError_t run_attn(const AttnK<T>& k,
   for (int r = 0; r < k.roles; ++r)
     whole = whole && aligned(k.role[r].x) && aligned(k.role[r].y) && aligned(k.role[r].z) && aligned(k.role[r].out);
   const int columns = STATE ? 64 : attn_columns(k, A);
-  const unsigned grid = static_cast<unsigned>((k.slots * k.H + 7) / 8 * 8 * attn_unit_blocks(k, columns));
+  const unsigned grid = static_cast<unsigned>(((k.cut ? k.cut : k.slots) * k.H + 7) / 8 * 8 * attn_unit_blocks(k, columns));
   return with_width(A, [&](auto ap) {
     constexpr int AP = decltype(ap)::value;
     if constexpr (STATE) {
       if (whole) attn_state_kernel<T, AP, true><<<grid, 512, 0, st>>>(k);
       else attn_state_kernel<T, AP, false><<<grid, 512, 0, st>>>(k);
     } else {
+      if constexpr (AP == 64 && NT == 2) {
+        if (columns == 64 && attn_in_pairs(k)) {
+          if (whole) attn_kernel<T, AP, NT, true, 1, true><<<grid, 512, 0, st>>>(k);
+          else attn_kernel<T, AP, NT, false, 1, true><<<grid, 512, 0, st>>>(k);
+          return;
+        }
+      }
       if (columns == 64) {
-        if (whole) attn_kernel<T, AP, NT, true, 1><<<grid, 512, 0, st>>>(k);
-        else attn_kernel<T, AP, NT, false, 1><<<grid, 512, 0, st>>>(k);
+        if (whole) attn_kernel<T, AP, NT, true, 1, false><<<grid, 512, 0, st>>>(k);
+        else attn_kernel<T, AP, NT, false, 1, false><<<grid, 512, 0, st>>>(k);
       } else if constexpr (AP <= 128) {
-        if (whole) attn_kernel<T, AP, NT, true, 2><<<grid, 512, 0, st>>>(k);
-        else attn_kernel<T, AP, NT, false, 2><<<grid, 512, 0, st>>>(k);
+        if (whole) attn_kernel<T, AP, NT, true, 2, false><<<grid, 512, 0, st>>>(k);
+        else attn_kernel<T, AP, NT, false, 2, false><<<grid, 512, 0, st>>>(k);
       }
     }
   });

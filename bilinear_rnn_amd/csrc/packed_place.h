@@ -1,0 +1,93 @@
+// Places in packed batches, found by a wavefront at once: a search one sequence after another costs a workgroup a
+// memory latency per step, more than the work on a short sequence takes.
+#pragma once
+
+#include "scan_common.h"
+
+namespace comba {
+
+// scan_place's segment of a slot below 2^32, the same for the whole wavefront, without channels. 64 starts are looked at in
+// every step of the search.
+__device__ __forceinline__ ScanPlace token_place(int64_t slot, const int32_t* cu, int N, int T, int L) {
+  ScanPlace p{};
+  p.slot = slot;
+  if (!cu) {
+    const uint32_t at = static_cast<uint32_t>(slot), per = L ? (T + L - 1) / L : 1;
+    p.n = p.b = static_cast<int>(at / per);
+    p.seg = static_cast<int>(at - p.n * per);
+    p.s1 = T;
+  } else {
+    if (!L) {
+      p.n = static_cast<int>(slot);
+    } else {
+      // the last sequence whose first slot, start / L + n, is at or before this one
+      const int lane = threadIdx.x & 63;
+      int lo = 0, hi = N - 1;
+      while (lo < hi) {
+        const int step = (hi - lo + 63) / 64;
+        const int64_t m = lo + static_cast<int64_t>(step) * (lane + 1);
+        bool before = false;
+        if (m <= hi) {
+          int s, e;
+          packed_range(cu, static_cast<int>(m), T, s, e);
+          before = s / L + m <= slot;
+        }
+        lo += step * __popcll(__ballot(before));
+        hi = min(hi, lo + step - 1);
+      }
+      p.n = lo;
+    }
+    packed_range(cu, p.n, T, p.s0, p.s1);
+    p.seg = L ? static_cast<int>(slot - (p.s0 / L + p.n)) : 0;
+  }
+  // an empty sequence has one, empty, segment; slots between sequences belong to none
+  p.ok = p.seg >= 0 && p.seg < segments_of(p.s1 - p.s0, L);
+  p.t0 = p.s0 + (p.ok ? p.seg * L : 0);
+  p.t1 = L ? p.t0 + min(L, p.s1 - p.t0) : p.s1;
+  return p;
+}
+
+// The packed sequence n that holds item j, when a sequence of so many tokens has items(tokens) of them; j becomes the item's
+// number in it. Behind the last item false, with j's distance from there. By every wavefront for itself, 64 PER sequences
+// in a step.
+template <int PER, typename F>
+__device__ __forceinline__ bool packed_item(const int32_t* cu, int N, int T, F items, int& j, int& n) {
+  const int lane = threadIdx.x & 63;
+  for (int64_t n0 = 0; n0 < N; n0 += 64 * PER) {
+    int c[PER], own = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int64_t m = n0 + lane * PER + i;
+      int s = 0, e = 0;
+      if (m < N) packed_range(cu, static_cast<int>(m), T, s, e);
+      c[i] = m < N ? items(e - s) : 0;
+      own += c[i];
+    }
+    int sum = own;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int y = __shfl_up(sum, off, kWave);
+      sum += lane >= off ? y : 0;
+    }
+    const int all = __builtin_amdgcn_readlane(sum, 63);
+    const uint64_t behind = __ballot(sum > j);
+    if (j >= all || !behind) {
+      j -= all;
+      continue;
+    }
+    const int at = __builtin_ctzll(behind);
+    int rest = j - (sum - own), i = 0;
+#pragma unroll
+    for (int k = 0; k < PER - 1; ++k)
+      if (i == k && rest >= c[k]) {
+        rest -= c[k];
+        ++i;
+      }
+    j = __builtin_amdgcn_readlane(rest, at);
+    n = min(static_cast<int>(n0) + at * PER + __builtin_amdgcn_readlane(i, at), N - 1);
+    return true;
+  }
+  return false;
+}
+
+}  // namespace comba
