@@ -3,8 +3,8 @@
 The chunk-wise parallel forward and the recurrent (decode) step of Comba,
 a bilinear RNN with a scalar-plus-low-rank state transition and output
 correction, and the operators a recurrent layer needs around it (short causal
-convolution, selective state space scan, block norms), as hand-written HIP
-kernels behind a C ABI (include/comba.h).
+convolution, selective state space scan, block norms, decayed linear attention,
+group norm), as hand-written HIP kernels behind a C ABI (include/comba.h).
 This package is the thin Python binding over that library.
 """
 from .api import (CombaError, block_norm, block_norm_bwd, bwd_cached_workspace_size, bwd_workspace_size, check_inputs,  # noqa: F401

@@ -612,8 +612,8 @@ int32_t comba_block_norm_bwd(const void* y, const void* gate, const void* residu
  *   initial_state  [N, H, V, K]     float32, or NULL for zeros
  *   final_state    [N, H, V, K]     float32, or NULL (not written); may be
  *                                   initial_state itself, but no other overlap
- * comba_linear_attn_fwd works in chunks of 64 tokens (bf16; 32 in float32) on the
- * matrix cores. float32 operands of a product with bf16 inputs are split into
+ * comba_linear_attn_fwd works in chunks of 64 tokens (bf16; 32 in float32; half
+ * as many for K above 128) on the matrix cores. float32 operands of a product with bf16 inputs are split into
  * bf16 terms, two for o and three for the states, so that o is right to its own
  * rounding and states and gradients of the decay to float32's. An input that is
  * infinite or NaN makes outputs of the same sequence, head and chunk infinite or
@@ -627,7 +627,8 @@ int32_t comba_block_norm_bwd(const void* y, const void* gate, const void* residu
  * comba_linear_attn_bwd: gradients for d_o = dL/do [B, T, H, V] (dtype) and
  * d_final_state (float32 [N, H, V, K]; NULL: 0), from the forward's inputs:
  *   dq, dk [B, T, Hk, K], dv [B, T, H, V] dtype (dq and dk summed over the value
- *   heads that share them); dlog_decay float32, [B, T, H] or [H] as log_decay;
+ *   heads that share them); dlog_decay float32, [B, T, H] or [H] as log_decay
+ *   (0 where log_decay is below -104: its exponential is 0 in float32);
  *   d_initial_state [N, H, V, K] float32 (may be NULL: not written).
  * It needs comba_linear_attn_bwd_workspace_size(...) bytes, 256-byte aligned.
  * All three give the same bits on every run.
