@@ -123,11 +123,12 @@ __global__ __launch_bounds__(256) void attn_carry_kernel(const float* __restrict
 // chunk the scores' parts of q . dq and k . dk have the same sum, so only the parts that come from
 // the states are carried from chunk to chunk: what is rounded in the others stays within the chunk.
 // rdot: [q and k][all and states' part][Z blocks, H, tokens], the four `one` floats apart.
-// A decay that is 0 in float32 has a gradient of 0: the sums only cancel to their rounding there.
+// A decay that is 0 in float32 has a gradient of 0, and so has that of a sequence's first token without an initial state
+// (`from_zero`): the sums only cancel to their rounding there.
 constexpr float kNoDecay = -104.f;  // e^-103.97 is half of float32's least number
 
 __global__ __launch_bounds__(256) void attn_decay_grad_kernel(const float* __restrict__ rdot, const double* __restrict__ inner,
-                                                              const float* __restrict__ log_decay,
+                                                              const float* __restrict__ log_decay, bool from_zero,
                                                               const int32_t* __restrict__ cu, int N, int T, int H, int L,
                                                               int CH, int64_t slots, int64_t tokens, int64_t one,
                                                               int zblocks, int eblocks, float* __restrict__ out,
@@ -175,7 +176,8 @@ __global__ __launch_bounds__(256) void attn_decay_grad_kernel(const float* __res
   __syncthreads();
   double sum = 0.0;
   for (int c = w; c < chunks; c += 4) {
-    const double s = wave_scan_f64_dpp(get(c, 0)) + part[c];
+    double s = wave_scan_f64_dpp(get(c, 0)) + part[c];
+    if (from_zero && token(c) == pl.s0) s = 0.0;
     if (lane < CH && token(c) < pl.t1) {
       sum += s;
       if (!hsum) {
@@ -414,7 +416,7 @@ template <typename T> hipError_t attn_bwd_t(const AttnBwdArgs& a, const AttnPlan
   k.roles = 1;
   if ((e = run_attn<T, 2, false>(k, K, st)) != hipSuccess) return e;
   attn_decay_grad_kernel<<<static_cast<unsigned>(p.slots * H), 256, 0, st>>>(
-      a.rdot, a.inner, f.log_decay, f.cu_seqlens, f.N, f.T, H, p.L, attn_chunk<T>(padded(V)), p.slots, k.tokens, one, zblocks,
+      a.rdot, a.inner, f.log_decay, !f.init, f.cu_seqlens, f.N, f.T, H, p.L, attn_chunk<T>(padded(V)), p.slots, k.tokens, one, zblocks,
       eblocks, a.dlog_decay, f.per_token ? nullptr : a.hsum);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   if (!f.per_token) {

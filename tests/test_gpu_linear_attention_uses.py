@@ -108,7 +108,9 @@ def test_backward_without_a_final_gradient(dtype):
     on, ref = make(2, 90, 4, 2, 40, 24, dtype, seed=7)
     check_backward(backward(on, 1.0, dfin=False), ref, 1.0, dtype, dfin=False)
     on["init"] = ref["init"] = None
-    check_backward(backward(on, 1.0, dfin=False), ref, 1.0, dtype, dfin=False)
+    got = backward(on, 1.0, dfin=False)
+    check_backward(got, ref, 1.0, dtype, dfin=False)
+    assert (got["dlog_decay"][:, 0] == 0).all()   # decays nothing
 
 
 def off_by_one(t):
