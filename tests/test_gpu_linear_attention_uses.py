@@ -78,6 +78,50 @@ def test_backward_of_many_heads(B, T, H, Hk, K, V, dtype, lens, head):
     check_backward(backward(on, K ** -0.5, cu), ref, K ** -0.5, dtype, cu)
 
 
+# Two workgroups per compute unit (many short sequences, heads up to 64), several chunks each.
+@pytest.mark.parametrize("B,T,H,Hk,K,V,dtype", [(16, 300, 32, 32, 16, 24, BF16), (16, 140, 32, 16, 12, 20, F32),
+                                                (9, 200, 64, 64, 17, 10, BF16)])
+def test_pairs_of_workgroups(B, T, H, Hk, K, V, dtype):
+    on, ref = make(B, T, H, Hk, K, V, dtype, seed=14)
+    o, f = forward(on, K ** -0.5)
+    check_forward(o, f, ref, K ** -0.5, dtype)
+    check_backward(backward(on, K ** -0.5), ref, K ** -0.5, dtype)
+
+
+# Packed batches with a few long sequences among many short ones: more than a step of the search takes.
+@pytest.mark.parametrize("N,dtype", [(64, BF16), (65, F32), (100, BF16), (600, BF16), (1100, F32)])
+def test_few_long_sequences_among_many(N, dtype):
+    lens = rnd(15).integers(0, 12, size=N).tolist()
+    for n, x in ((3, 700), (N // 2, 1), (N - 30, 513), (N - 1, 1100)):
+        lens[n] = x
+    cu = cu_of(lens)
+    on, ref = make(1, sum(lens), 4, 2, 16, 24, dtype, lens, seed=16)
+    o, f = forward(on, 0.25, cu)
+    check_forward(o, f, ref, 0.25, dtype, cu)
+    check_backward(backward(on, 0.25, cu), ref, 0.25, dtype, cu)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_growing_states(dtype):
+    """Decays above 1: the state grows to about e^20 times a term. Relative to the whole tensor, an output is off by its
+    rounding, the rest by T + K + V roundings of 2^-24 and, for decays, four for each of the T exponents."""
+    T, K, V = 300, 24, 40
+    on, ref = make(2, T, 2, 2, K, V, dtype, seed=17)
+    on["log_decay"], ref["log_decay"] = dev(rnd(18).uniform(-0.05, 0.2, size=(2, T, 2)))
+    args = [ref[n] for n in ("q", "k", "v", "log_decay")]
+    o, f = forward(on, 0.2)
+    ro, rf = layer.linear_attention(*args, scale=0.2, init=ref["init"])
+    off = lambda a, b: np.linalg.norm(np64(a) - b) / np.linalg.norm(b)  # noqa: E731
+    u = U * (5 * T + K + V)
+    step = torch.finfo(dtype).eps / 2
+    assert off(o, ro) < step + u + 2.0 ** -16 and off(f, rf) < u
+    got = backward(on, 0.2)
+    r = layer.linear_attention(*args, scale=0.2, init=ref["init"], do=ref["do"], dfin=ref["dfin"])
+    for n in ("dq", "dk", "dv"):
+        assert off(got[n], r[n]) < step + u + 2.0 ** -16, n
+    assert off(got["dinitial_state"], r["dinitial_state"]) < u
+
+
 def extreme(on, ref, seed):
     """Decays from none at all to resets of the state."""
     some = np.array([0.0, -1e-7, -1e-3, -0.3, -5.0, -60.0, -150.0, -300.0, -1e30, -np.inf])
@@ -507,6 +551,20 @@ def test_past_2_31_elements():
                                                       silu=True)["dx"])
     del x, y, dx, dy, q
     torch.cuda.empty_cache()
+
+
+def test_norm_of_a_sequence_of_millions():
+    T, C = 4_300_007, 8
+    x = big(1, T, C) + 3
+    w = torch.linspace(0.5, 1.5, C, device="cuda")
+    y, st = comba.group_norm(x, 2, w, None)
+    d = x.double().view(T, 2, 4)
+    mean = d.mean((0, 2))
+    rstd = 1 / (d.sub(mean.view(1, 2, 1)).square().mean((0, 2)) + 1e-5).sqrt()
+    assert (st[0, :, 0] / mean - 1).abs().max() < 1e-5 and (st[0, :, 1] / rstd - 1).abs().max() < 1e-5
+    want = (d - mean.view(1, 2, 1)) * rstd.view(1, 2, 1) * w.view(1, 2, 4)
+    # half a step of bf16, and 1e-5 of the deviations, of which no value is more than 7 away
+    assert ((y.double().view(T, 2, 4) - want).abs() <= want.abs() * 2.0 ** -8 + 1.5e-4).all()
 
 
 def test_steps_past_2_31_state_elements():
