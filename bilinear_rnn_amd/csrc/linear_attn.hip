@@ -316,7 +316,8 @@ __global__ __launch_bounds__(256) void attn_step_kernel(const T* __restrict__ q,
 // at B = 8, T = 4096, 16 heads of 128, uncut 192 us, in two segments 210.
 // Packed batches are cut where a sequence is longer than 1.5 times a compute unit's share of all: the lengths are not known
 // here, and a segment of L tokens takes its time in the state pass even if it is the only one (64 sequences, 40001
-// tokens, 32 heads of 64: 7500 tokens, so uncut, 255 us, 2048 281, 256 443).
+// tokens, 32 heads of 64: 7500 tokens, so uncut, 255 us, 2048 281, 256 443;
+// 12 sequences of 4096, 16 heads of 128: at 1.5 shares 251 us, at one 333, at half of one 355).
 AttnPlan attn_plan(int64_t B, int64_t T, int64_t H, int64_t V, int64_t N, bool packed) {
   if (!packed && B * H * attn_blocks(static_cast<int>(V)) >= 256) return AttnPlan{0, N};
   const int64_t units = H * ((V + 127) / 128);
